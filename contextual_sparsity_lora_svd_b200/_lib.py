@@ -61,6 +61,23 @@ class FfnGrads(ctypes.Structure):
                 ("dBd", c_vp)]
 
 
+class Rotary(ctypes.Structure):
+    _fields_ = [("layout", c_i32), ("scaling", c_i32), ("dims", c_i32), ("orig_len", c_i32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("mscale", ctypes.c_double)]
+
+
+class QkRows(ctypes.Structure):
+    _fields_ = [("heads", c_i32), ("n_idx", c_i32), ("idx", c_vp), ("X", c_vp), ("ldx", c_i64),
+                ("X_ctx", c_vp), ("X_out", c_vp), ("g", c_vp), ("Y", c_vp), ("ldy", c_i64),
+                ("dY", c_vp), ("lddy", c_i64), ("dX", c_vp), ("lddx", c_i64), ("dX_ctx", c_vp),
+                ("dX_out", c_vp), ("dg", c_vp)]
+
+
+class Act8(ctypes.Structure):
+    _fields_ = [("codes", c_vp), ("scales", c_vp)]
+
+
 def _sig(name, res, args):
     f = getattr(_lib, name)
     f.restype = res
@@ -110,6 +127,21 @@ _sig("slora_rmsnorm_fwd", c_int,
 _sig("slora_rmsnorm_bwd", c_int,
      [c_int, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, P_SZ, c_vp])
 
+_QK = [ctypes.POINTER(Tokens), c_int, c_f32, ctypes.POINTER(Rotary), c_vp, ctypes.POINTER(QkRows),
+       ctypes.POINTER(QkRows), c_vp, P_SZ, c_vp]
+_sig("slora_qk_rotary_fwd", c_int, [c_int] + _QK)
+_sig("slora_qk_rotary_bwd", c_int, [c_int, c_int] + _QK)
+P_ACT8 = ctypes.POINTER(Act8)
+_sig("slora_act8_pack", c_int, [c_int, c_i64, c_i64, c_vp, c_i64, P_ACT8, c_vp, P_SZ, c_vp])
+_sig("slora_act8_unpack", c_int, [c_int, c_i64, c_i64, P_ACT8, c_vp, c_i64, c_vp, P_SZ, c_vp])
+_sig("slora_rmsnorm_fwd_act8", c_int,
+     [c_int, c_i64, c_i64, c_f32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, P_ACT8, P_ACT8, c_vp, P_SZ,
+      c_vp])
+_sig("slora_rmsnorm_bwd_act8", c_int,
+     [c_int, c_i64, c_i64, P_ACT8, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, P_SZ, c_vp])
+_sig("slora_linear_bwd_act8", c_int,
+     _LIN + [P_ACT8, P_ACT8, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, P_SZ, c_vp])
+
 _sig("slora_noalloc_scratch_bytes", c_sz, [])
 _sig("slora_estimate_select_noalloc", c_int,
      [c_int, c_vp, c_int, ctypes.POINTER(Tokens), c_i64, c_vp, c_vp, c_i64, c_vp, c_vp, c_i64,
@@ -127,7 +159,9 @@ EXPORTS = sorted(["slora_last_error_string", "slora_version", "slora_svd_prepare
                   "slora_set_wait_budget", "slora_ffn_bwd", "slora_ffn_fwd_bwd_per_seq",
                   "slora_rope_pack", "slora_rope_unpack",
                   "slora_attention_fwd", "slora_attention_bwd", "slora_rmsnorm_fwd",
-                  "slora_rmsnorm_bwd"])
+                  "slora_rmsnorm_bwd", "slora_qk_rotary_fwd", "slora_qk_rotary_bwd",
+                  "slora_act8_pack", "slora_act8_unpack", "slora_rmsnorm_fwd_act8",
+                  "slora_rmsnorm_bwd_act8", "slora_linear_bwd_act8"])
 
 
 def lib():
@@ -381,3 +415,176 @@ def slora_rmsnorm_bwd(H, rstd, g, dN0, dX, dN1=None, dN2=None, dRes=None, stream
     T, d = H.shape
     _run("slora_rmsnorm_bwd", [BF16, T, d, ptr(H), ptr(rstd), ptr(g), ptr(dN0), ptr(dN1),
                                ptr(dN2), ptr(dRes), ptr(dX)], None, stream)
+
+
+# ------------------------------------- rotation of q and k with head norms
+ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+
+
+def rotary(layout="half", dims=0, base=ROPE_BASE, scaling="none", factor=1.0, orig_len=0, low=0.0,
+           high=0.0, mscale=0.0) -> Rotary:
+    """How q and k are rotated (slora_rotary); dims 0: the whole head."""
+    return Rotary(ROTARY_LAYOUTS[layout], ROTARY_SCALINGS[scaling], int(dims), int(orig_len),
+                  float(base), float(factor), float(low), float(high), float(mscale))
+
+
+def _rows(t, what):
+    """(address, row stride) of a 2-D tensor whose rows are contiguous."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: a 2-D tensor with contiguous rows is needed")
+    return ptr(t), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _whole(t, what):
+    if t is not None and not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous tensor is needed")
+    return ptr(t)
+
+
+def qk_rows(heads, X=None, g=None, Y=None, dY=None, dX=None, dg=None, idx=None, X_ctx=None,
+            X_out=None, dX_ctx=None, dX_out=None) -> QkRows:
+    """The rows of q or k for slora_qk_rotary_fwd / _bwd: dense (X, Y, dX may
+    have any row stride), or with `idx` sliced (X_ctx, X_out, dX_ctx, dX_out
+    contiguous).  The struct keeps its tensors alive."""
+    px, ldx = _rows(X, "X")
+    py, ldy = _rows(Y, "Y")
+    pdy, lddy = _rows(dY, "dY")
+    pdx, lddx = _rows(dX, "dX")
+    sliced = idx is not None
+    # an empty list is still a list: its address, never read, may be null
+    pidx = (ptr(idx) or ptr(X_out) or ptr(dX_out) or ptr(Y)) if sliced else None
+    r = QkRows(int(heads), idx.numel() if sliced else 0, pidx, px, ldx, _whole(X_ctx, "X_ctx"),
+               _whole(X_out, "X_out"), _whole(g, "g"), py, ldy, pdy, lddy, pdx, lddx,
+               _whole(dX_ctx, "dX_ctx"), _whole(dX_out, "dX_out"), _whole(dg, "dg"))
+    r.tensors = (X, g, Y, dY, dX, dg, idx, X_ctx, X_out, dX_ctx, dX_out)
+    first = next(t for t in (X, X_ctx, X_out, dX, dX_ctx, dX_out, Y) if t is not None)
+    for t, what in ((X, "X"), (X_ctx, "X_ctx"), (X_out, "X_out"), (g, "g"), (Y, "Y"), (dX, "dX"),
+                    (dX_ctx, "dX_ctx"), (dX_out, "dX_out")):
+        if t is not None and t.dtype != first.dtype:
+            raise TypeError(f"{what} is {t.dtype}, the rows are {first.dtype}")
+    if sliced and idx.dtype != torch.int32:
+        raise TypeError("idx is an int32 tensor")
+    if dg is not None and dg.dtype != torch.float32:
+        raise TypeError("dg is an fp32 tensor")
+    r.dt = dtype_code(first)
+    r.gdt = F32 if dY is None else dtype_code(dY)
+    r.scratch = sliced or dg is not None
+    return r
+
+
+def _qk(fn, head, batch, seq, head_dim, q, k, rotary_, pos, eps, ctx_len, ws, stream):
+    tok, keep = make_tokens(batch, seq, [seq] * batch if ctx_len is None else ctx_len)
+    if pos is not None and (pos.dtype != torch.int32 or pos.numel() != batch * seq
+                            or not pos.is_contiguous()):
+        raise TypeError("pos is a contiguous int32 tensor with one position a row")
+    if k is not None and (k.dt, k.gdt) != (q.dt, q.gdt):
+        raise TypeError("q and k have the same dtypes")
+    args = head + [ctypes.byref(tok), head_dim, eps, ctypes.byref(rotary_ or rotary()), ptr(pos),
+                   ctypes.byref(q), None if k is None else ctypes.byref(k)]
+    if q.scratch or (k is not None and k.scratch):
+        _run(fn, args, ws, stream)
+    else:
+        _run_plain(fn, args, q, stream)
+    del keep
+
+
+def _run_plain(fn_name, args, anything, stream):
+    """A call that needs no scratch: any non-null workspace address runs it."""
+    _check(fn_name, getattr(_lib, fn_name)(*args, ctypes.addressof(anything) & ~15,
+                                           ctypes.byref(c_sz(0)), _stream(stream)))
+
+
+def slora_qk_rotary_fwd(batch, seq, head_dim, q, k=None, rotary=None, pos=None, eps=RMS_EPS,
+                        ctx_len=None, ws=None, stream=None):
+    """Rotates (and, with a gain, normalises) the heads of q and k, given as
+    `qk_rows`; `rotary` from rotary(), `pos` int32 [batch * seq]."""
+    _qk("slora_qk_rotary_fwd", [q.dt], batch, seq, head_dim, q, k, rotary, pos, eps, ctx_len, ws,
+        stream)
+
+
+def slora_qk_rotary_bwd(batch, seq, head_dim, q, k=None, rotary=None, pos=None, eps=RMS_EPS,
+                        ctx_len=None, ws=None, stream=None):
+    _qk("slora_qk_rotary_bwd", [q.dt, q.gdt], batch, seq, head_dim, q, k, rotary, pos, eps,
+        ctx_len, ws, stream)
+
+
+# ------------------------------------------- 8-bit activation checkpoints
+ACT8_BLOCK = 32
+
+
+def act8_empty(T, d, device="cuda"):
+    """(codes, scales) of a checkpoint of [T x d] activations."""
+    nb = (d + ACT8_BLOCK - 1) // ACT8_BLOCK
+    return (torch.empty((T, nb * ACT8_BLOCK), dtype=torch.int8, device=device),
+            torch.empty((T, nb), dtype=torch.uint8, device=device))
+
+
+def act8(codes, scales, T, d) -> Act8:
+    """The C struct of a checkpoint of [T x d] activations."""
+    nb = (d + ACT8_BLOCK - 1) // ACT8_BLOCK
+    if (codes.dtype != torch.int8 or scales.dtype != torch.uint8 or not codes.is_contiguous()
+            or not scales.is_contiguous() or codes.numel() != T * nb * ACT8_BLOCK
+            or scales.numel() != T * nb):
+        raise ValueError(f"a checkpoint of {T} x {d} activations is contiguous int8 "
+                         f"[{T} x {nb * ACT8_BLOCK}] and uint8 [{T} x {nb}]")
+    return Act8(ptr(codes), ptr(scales))
+
+
+def _ref(c):
+    return None if c is None else ctypes.byref(c)
+
+
+def slora_act8_pack(X, codes, scales, stream=None):
+    T, d = X.shape
+    px, ldx = _rows(X, "X")
+    c = act8(codes, scales, T, d)
+    _run_plain("slora_act8_pack", [dtype_code(X), T, d, px, ldx, ctypes.byref(c)], c, stream)
+
+
+def slora_act8_unpack(codes, scales, X, stream=None):
+    T, d = X.shape
+    px, ldx = _rows(X, "X")
+    c = act8(codes, scales, T, d)
+    _run_plain("slora_act8_unpack", [dtype_code(X), T, d, ctypes.byref(c), px, ldx], c, stream)
+
+
+def slora_rmsnorm_fwd_act8(X, g, N, rstd=None, A=None, H=None, H8=None, N8=None, eps=RMS_EPS,
+                           stream=None):
+    """H8, N8: (codes, scales) of the checkpoints to write, or None."""
+    T, d = X.shape
+    h8 = None if H8 is None else act8(*H8, T, d)
+    n8 = None if N8 is None else act8(*N8, T, d)
+    _run_plain("slora_rmsnorm_fwd_act8",
+               [BF16, T, d, eps, ptr(X), ptr(A), ptr(g), ptr(H), ptr(N), ptr(rstd), _ref(h8),
+                _ref(n8)], n8 or h8 or Act8(), stream)
+
+
+def slora_rmsnorm_bwd_act8(H8, rstd, g, dN0, dX, dN1=None, dN2=None, dRes=None, stream=None):
+    T, d = dN0.shape
+    h8 = act8(*H8, T, d)
+    _run_plain("slora_rmsnorm_bwd_act8",
+               [BF16, T, d, ctypes.byref(h8), ptr(rstd), ptr(g), ptr(dN0), ptr(dN1), ptr(dN2),
+                ptr(dRes), ptr(dX)], h8, stream)
+
+
+def slora_linear_bwd_act8(side, batch, seq, ctx_len, k, n, W, A, B, lora_scale, idx, X8_ctx,
+                          XA_save, dY_ctx, dX_ctx, dA, dB, X8_out=None, dY_out=None, dX_out=None,
+                          ws=None, stream=None):
+    """slora_linear_bwd with the layer input given as checkpoints: X8_ctx and,
+    for SLICE_IN_COLS, X8_out are (codes, scales)."""
+    tok, keep = make_tokens(batch, seq, ctx_len)
+    n_idx = 0 if idx is None else idx.numel()
+    T, TC = batch * seq, sum(int(c) for c in ctx_len)
+    cols = side == SLICE_IN_COLS
+    xc = None if X8_ctx is None else act8(*X8_ctx, TC if cols else T, n_idx if cols else k)
+    xo = None if X8_out is None else act8(*X8_out, T - TC, k)
+    # an empty channel list is still a list: its address, never read, may be null
+    pidx = ptr(idx) or (None if idx is None else ptr(XA_save))
+    _run("slora_linear_bwd_act8",
+         [dtype_code(W), ctypes.byref(tok), k, n, ptr(W), ptr(A), ptr(B), A.shape[0],
+          float(lora_scale), side, pidx, n_idx, _ref(xc), _ref(xo), ptr(XA_save),
+          ptr(dY_ctx), ptr(dY_out), ptr(dX_ctx), ptr(dX_out), ptr(dA), ptr(dB)], ws, stream)
+    del keep

@@ -377,6 +377,52 @@ extern "C" slora_status slora_linear_bwd(slora_dtype dt, const slora_tokens* tok
                         false, static_cast<cudaStream_t>(stream));
 }
 
+extern "C" slora_status slora_linear_bwd_act8(
+    slora_dtype dt, const slora_tokens* tok, int64_t k, int64_t n, const void* W, const void* A,
+    const void* B, int r_lora, float lora_scale, slora_slice side, const int32_t* idx,
+    int32_t n_idx, const slora_act8* X_ctx, const slora_act8* X_out, const float* XA_save,
+    const void* dY_ctx, const void* dY_out, void* dX_ctx, void* dX_out, float* dA, float* dB,
+    void* ws, size_t* ws_bytes, slora_stream_t stream) {
+  const char* fn = "slora_linear_bwd_act8";
+  clear_error();
+  TokenInfo ti;
+  SLORA_TRY(linear_common_checks(fn, dt, tok, k, n, W, A, B, r_lora, side, idx, n_idx, &ti));
+  if (dt != SLORA_BF16)
+    SLORA_FAIL(SLORA_ERR_UNSUPPORTED, "%s: 8-bit layer inputs run in bf16 only", fn);
+  REQ_PTR(XA_save); REQ_PTR(dA); REQ_PTR(dB); OPT_PTR(ws);
+  LinearDesc L{int(dt), ti, k, n, W, A, B, r_lora, lora_scale, side, idx, n_idx};
+  L.act8 = true;
+  const bool in_cols = side == SLORA_SLICE_IN_COLS, out_rows = side == SLORA_SLICE_OUT_ROWS;
+  // the operands of the rows and channels that there are
+  const bool ctx = in_cols ? ti.T_C > 0 && n_idx > 0 : true;
+  if (ctx) {
+    if (!X_ctx) SLORA_FAIL(SLORA_ERR_INVALID_ARG, "%s: required checkpoint X_ctx is NULL", fn);
+    REQ_PTR(X_ctx->codes); REQ_PTR(X_ctx->scales);
+    REQ_PTR(dX_ctx);
+    L.x8_ctx = *X_ctx;
+  }
+  if (in_cols && ti.T_O > 0) {
+    if (!X_out) SLORA_FAIL(SLORA_ERR_INVALID_ARG, "%s: required checkpoint X_out is NULL", fn);
+    REQ_PTR(X_out->codes); REQ_PTR(X_out->scales);
+    REQ_PTR(dX_out);
+    L.x8_out = *X_out;
+  }
+  if (!out_rows || (ti.T_C > 0 && n_idx > 0)) REQ_PTR(dY_ctx);
+  if (out_rows && ti.T_O > 0) REQ_PTR(dY_out);
+  Arena plan;
+  SLORA_TRY(linear_bwd_run(L, tok, nullptr, nullptr, XA_save, dY_ctx, dY_out, dX_ctx, dX_out, dA,
+                           dB, plan, true, nullptr));
+  const bool query = ws == nullptr;
+  SLORA_TRY(finish_ws(fn, plan, ws, ws_bytes));
+  if (query) return SLORA_OK;
+  SLORA_TRY(check_device());
+  Arena ar;
+  ar.base = static_cast<char*>(ws);
+  ar.cap = *ws_bytes;
+  return linear_bwd_run(L, tok, nullptr, nullptr, XA_save, dY_ctx, dY_out, dX_ctx, dX_out, dA, dB,
+                        ar, false, static_cast<cudaStream_t>(stream));
+}
+
 // ------------------------------------------------------------------- FFN
 namespace {
 // Checks shared by the per-batch and the per-sequence FFN calls; sets kkeep.

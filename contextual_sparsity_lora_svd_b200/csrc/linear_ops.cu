@@ -10,6 +10,7 @@
 // and output rows, S = selected channel set (idx).
 #include <algorithm>
 
+#include "act8.cuh"
 #include "estimator.cuh"
 #include "gemm.cuh"
 #include "gemm_tc.cuh"
@@ -907,6 +908,15 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
   const int64_t lr = round8(r), ldi = round8(std::max<int64_t>(ni, 1));
   const bool none = L.side == SLORA_SLICE_NONE, outr = L.side == SLORA_SLICE_OUT_ROWS;
   const int64_t nct = count_tiles(tok, true), nott = count_tiles(tok, false);
+  // rank operands in fp32: one bf16 term, three beside an 8-bit input, whose
+  // gradients are to be exact for the values it holds
+  const int terms = L.act8 ? 0 : 1;
+  auto rkv = [terms](const void* p, int dtp, int64_t si, int64_t sq, const int32_t* map = nullptr,
+                     int64_t map_limit = INT64_MAX) {
+    SkR rr = slora::rkv(p, dtp, si, sq, map, map_limit);
+    if (dtp == kF32) rr.terms = terms;
+    return rr;
+  };
   auto bf = [&](int64_t rows, int64_t cols) {
     return static_cast<void*>(ar.take<__nv_bfloat16>(size_t(std::max<int64_t>(rows * cols, 1))));
   };
@@ -923,7 +933,7 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
   void* AS = bf(ni, lr);      // A[:, idx]^T padded (IN_COLS)
   void* At = bf(k, lr);       // A^T padded (IN_COLS)
   void* dYpad = (outr && ni % 8) ? bf(TC, ldi) : nullptr;
-  void* Xpad = (!none && !outr && ni % 8) ? bf(TC, ldi) : nullptr;
+  void* Xpad = (!none && !outr && ni % 8 && !L.act8) ? bf(TC, ldi) : nullptr;
   float* part = ar.take<float>(size_t(skinny_part_bound(ti, k, n, ni, r)));
   const int64_t ncnt = skinny_counter_count(std::max({T, k, n}), std::max({T, k, n}));
   unsigned* rsp = ar.take<unsigned>(size_t(ncnt));
@@ -971,26 +981,59 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
     }
     const void* dYc0 = dYpad ? dYpad : dY_ctx;
     const int64_t lddc0 = dYpad ? ldi : ni;
+    if (!L.act8) bj[nbj++] = cjob(X_ctx, k, T, k, rkv(dYB, kF32, r, 1), rsDY, dA, k, 1);
     if (none) {
-      bj[nbj++] = cjob(X_ctx, k, T, k, rkv(dYB, kF32, r, 1), rsDY, dA, k, 1);
       bj[nbj++] = cjob(dY_ctx, n, T, n, rkv(XA, kF32, r, 1), rsX0, dB, r, 0);
     } else {
-      bj[nbj++] = cjob(X_ctx, k, T, k, rkv(dYB, kF32, r, 1), rsDY, dA, k, 1);
       bj[nbj++] = cjob(dY_out, n, TO, n, rkv(XA, kF32, r, 1, out_rows), rsX0, dB, r, 0);
       bj[nbj++] = cjob(dYc0, lddc0, TC, ni, rkv(XA, kF32, r, 1, ctx_rows), rsX1, SB, r, 0);
     }
   }
   float* bpart = nullptr;
-  unsigned* bcnt = nullptr;
+  int64_t nbcnt = 0;
   if (batched) {
     bpart = ar.take<float>(size_t(coldot_batch_part_floats(bj, nbj)));
-    bcnt = ar.take<unsigned>(size_t(coldot_batch_counter_count(bj, nbj)));
+    nbcnt = coldot_batch_counter_count(bj, nbj);
   }
+  // an 8-bit input's contractions; their arrival counters lie behind the
+  // batch's, so that the row-map launch zeroes both
+  float* part8 = nullptr;
+  void* rs8 = nullptr;
+  int64_t ncnt8 = 0;
+  if (L.act8) {
+    int64_t np8 = act8_dot_part_floats(T, k, r);
+    ncnt8 = act8_dot_counters(k, r);
+    if (!none && !outr) {
+      np8 = std::max(act8_dot_part_floats(TO, k, r), act8_dot_part_floats(TC, ni, r));
+      ncnt8 = std::max(ncnt8, act8_dot_counters(ni, r));
+    }
+    part8 = ar.take<float>(size_t(np8));
+    if (!batched) rs8 = rsbuf(T);
+  }
+  unsigned* bcnt = nbcnt + ncnt8 ? ar.take<unsigned>(size_t(nbcnt + ncnt8)) : nullptr;
+  unsigned* cnt8 = bcnt ? bcnt + nbcnt : nullptr;
   if (plan) return SLORA_OK;
   SLORA_TRY(arena_fits(ar, "workspace"));
+  // dA (+)= s dYB^T X over the rows of a checkpoint, rs the split dYB of its rows
+  auto dot8 = [&](const slora_act8& X, int64_t M, int64_t K, const void* rs, const int32_t* kmap,
+                  int accumulate) {
+    Act8Dot j;
+    j.X = X; j.M = M; j.K = K; j.P = rs; j.cols = r; j.out = dA; j.ldo = k; j.kmap = kmap;
+    j.scale = s; j.accumulate = accumulate;
+    return act8_dot(j, part8, cnt8, st);
+  };
+  // dYB of rows `map` split into rs8 (its rows' place in the checkpoint's order), then dot8
+  auto grad8 = [&](const slora_act8& X, int64_t M, int64_t K, const int32_t* map,
+                   const int32_t* kmap, int accumulate) -> slora_status {
+    if (M > 0) {
+      const SkPrep jd = {rkv(dYB, kF32, r, 1, map), r, M, rs8};
+      SLORA_TRY(prep_r_batch(&jd, 1, st));
+    }
+    return dot8(X, M, K, rs8, kmap, accumulate);
+  };
 
   SLORA_TRY(launch_rowmaps(tok, ti, ctx_rows, out_rows, st, ctiles, otiles, rsp, ncnt, bcnt,
-                           bcnt ? coldot_batch_counter_count(bj, nbj) : 0));
+                           nbcnt + ncnt8));
   if (batched && none) {
     const SkPrep jobs[2] = {{rkv(L.B, kBF16, r, 1), r, n, rsB0}, {rkv(XA, kF32, r, 1), r, T, rsX0}};
     SLORA_TRY(prep_r_batch(jobs, 2, st));
@@ -1005,6 +1048,7 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
     SLORA_TRY(gemm_tc(b.g, st));
     const SkPrep jd = {rkv(dYB, kF32, r, 1), r, T, rsDY};
     SLORA_TRY(prep_r_batch(&jd, 1, st));
+    if (L.act8) SLORA_TRY(dot8(L.x8_ctx, T, k, rsDY, nullptr, 0));
     return coldot_batch(bj, nbj, bpart, bcnt, st);
   }
   if (batched && outr) {
@@ -1041,6 +1085,7 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
     }
     const SkPrep jd = {rkv(dYB, kF32, r, 1), r, T, rsDY};
     SLORA_TRY(prep_r_batch(&jd, 1, st));
+    if (L.act8) SLORA_TRY(dot8(L.x8_ctx, T, k, rsDY, nullptr, 0));
     SLORA_TRY(coldot_batch(bj, nbj, bpart, bcnt, st));
     ScatterAddJob sj;
     sj.dst = dB; sj.ld_dst = r; sj.src = SB; sj.ld_src = r; sj.trans = 0;
@@ -1100,6 +1145,7 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
           .out(dX_ctx, nullptr, nullptr, k);
       SLORA_TRY(gemm_tc_pair(bc.g, b.g, st));
     }
+    if (L.act8) return grad8(L.x8_ctx, T, k, nullptr, nullptr, 0);
     SkColOut ca;  // dA = s dYB^T X over every row
     ca.out = dA; ca.ldo = k; ca.trans = 1; ca.scale = s;
     return coldot(ykv(X_ctx, k), T, k, rkv(dYB, kF32, r, 1), r, ca, sw, st);
@@ -1131,7 +1177,10 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
         .out(dX_out, nullptr, nullptr, k);
     SLORA_TRY(gemm_tc_pair(bc.g, b.g, st));
   }
-  {  // dA: output rows over every column, then += context rows on columns S
+  if (L.act8) {
+    SLORA_TRY(grad8(L.x8_out, TO, k, out_rows, nullptr, 0));
+    SLORA_TRY(grad8(L.x8_ctx, TC, ni, ctx_rows, L.idx, 1));
+  } else {  // dA: output rows over every column, then += context rows on columns S
     SkColOut ao;
     ao.out = dA; ao.ldo = k; ao.trans = 1; ao.scale = s;
     SLORA_TRY(coldot(ykv(X_out, k), TO, k, rkv(dYB, kF32, r, 1, out_rows), r, ao, sw, st));

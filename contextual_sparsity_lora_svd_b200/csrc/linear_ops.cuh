@@ -17,6 +17,10 @@ struct LinearDesc {
   slora_slice side;
   const int32_t* idx;
   int32_t n_idx;
+  // backward only: the layer input as 8-bit checkpoints in place of X_ctx and
+  // X_out (bf16 path); the rank operands then keep three bf16 terms
+  bool act8 = false;
+  slora_act8 x8_ctx = {nullptr, nullptr}, x8_out = {nullptr, nullptr};
 };
 
 // With plan == true only the arena is sized (no pointer is touched).

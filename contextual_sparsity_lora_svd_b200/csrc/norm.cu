@@ -6,6 +6,13 @@
 // between).  Longer rows: one warp per row in two passes.  Every value is
 // rounded to bf16 where it is stored, and the normalisation reads the rounded
 // residual sum, the value the backward sees.
+//
+// The variants with 8-bit checkpoints (act8.cuh) write the codes of H and N in
+// the same pass (a 32-channel block is four neighbouring lanes' chunks, its
+// maximum two shuffles), and read H as codes in the backward: 1.03 bytes a
+// value in place of 2, and no separate pass over H and N to pack them.
+#include "act8.cuh"
+#include "act8_dev.cuh"
 #include "attention.cuh"
 
 namespace slora {
@@ -228,6 +235,124 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
+template <int CPT>
+__global__ void __launch_bounds__(kRowThreads)
+    rmsnorm_fwd_act8_kernel(const uint4* __restrict__ X, const uint4* __restrict__ A,
+                            const uint4* __restrict__ g, int nch, float eps,
+                            uint4* __restrict__ Hout, uint4* __restrict__ N,
+                            float* __restrict__ rstd, uint2* __restrict__ h8,
+                            uint8_t* __restrict__ h8s, uint2* __restrict__ n8,
+                            uint8_t* __restrict__ n8s) {
+  __shared__ float red[4];
+  const int64_t o = int64_t(blockIdx.x) * nch;
+  const int nchp = (nch + 3) & ~3;  // chunks of a checkpoint's row
+  const int64_t o8 = int64_t(blockIdx.x) * nchp;
+  float h[CPT][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) {
+    const int c = threadIdx.x + k * kRowThreads;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[k][i] = 0.f;
+    if (c < nch) {
+      unpack8(X[o + c], h[k]);
+      if (A) {
+        float a[8];
+        unpack8(A[o + c], a);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[k][i] = __bfloat162float(__float2bfloat16_rn(h[k][i] + a[i]));
+        if (Hout) Hout[o + c] = pack8(h[k]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss += h[k][i] * h[k][i];
+    }
+    if (h8) {
+      const uint32_t byte = act8_byte(act8_block_max(act8_chunk_bits(h[k])));
+      if (c < nchp) {
+        h8[o8 + c] = act8_codes8(h[k], byte);
+        if ((c & 3) == 0) h8s[(o8 + c) >> 2] = uint8_t(byte);
+      }
+    }
+  }
+  const float r = rsqrtf(block_sum128(ss, red) / float(nch * 8) + eps);
+  if (threadIdx.x == 0 && rstd) rstd[blockIdx.x] = r;
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) {
+    const int c = threadIdx.x + k * kRowThreads;
+    float v[8] = {};
+    if (c < nch) {
+      float gg[8];
+      unpack8(g[c], gg);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[k][i] *= r * gg[i];
+      const uint4 u = pack8(h[k]);
+      N[o + c] = u;
+      unpack8(u, v);  // the checkpoint holds the stored, rounded values
+    }
+    if (n8) {
+      const uint32_t byte = act8_byte(act8_block_max(act8_chunk_bits(v)));
+      if (c < nchp) {
+        n8[o8 + c] = act8_codes8(v, byte);
+        if ((c & 3) == 0) n8s[(o8 + c) >> 2] = uint8_t(byte);
+      }
+    }
+  }
+}
+
+template <int CPT>
+__global__ void __launch_bounds__(kRowThreads)
+    rmsnorm_bwd_act8_kernel(const uint2* __restrict__ h8, const uint8_t* __restrict__ h8s,
+                            const float* __restrict__ rstd, const uint4* __restrict__ g,
+                            const uint4* __restrict__ dN0, const uint4* __restrict__ dN1,
+                            const uint4* __restrict__ dN2, const uint4* __restrict__ dRes,
+                            int nch, uint4* __restrict__ dX) {
+  __shared__ float red[4];
+  const int64_t o = int64_t(blockIdx.x) * nch, o8 = int64_t(blockIdx.x) * ((nch + 3) & ~3);
+  float h[CPT][8], gd[CPT][8];
+  float dot = 0.f;
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) {
+    const int c = threadIdx.x + k * kRowThreads;
+    if (c < nch) {
+      float t[8], gg[8];
+      act8_values8(h8[o8 + c], h8s[(o8 + c) >> 2], h[k]);
+      unpack8(g[c], gg);
+      unpack8(dN0[o + c], gd[k]);
+      if (dN1) {
+        unpack8(dN1[o + c], t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) gd[k][i] += t[i];
+      }
+      if (dN2) {
+        unpack8(dN2[o + c], t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) gd[k][i] += t[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        gd[k][i] *= gg[i];  // g dN
+        dot += h[k][i] * gd[k][i];
+      }
+    }
+  }
+  const float r = rstd[blockIdx.x];
+  const float coef = r * r * r * block_sum128(dot, red) / float(nch * 8);
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) {
+    const int c = threadIdx.x + k * kRowThreads;
+    if (c < nch) {
+      float res[8];
+      if (dRes) unpack8(dRes[o + c], res);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v = r * gd[k][i] - h[k][i] * coef;
+        h[k][i] = dRes ? res[i] + v : v;
+      }
+      dX[o + c] = pack8(h[k]);
+    }
+  }
+}
+
 }  // namespace
 
 slora_status rmsnorm_fwd_run(const void* X, const void* A, const void* g, int64_t T, int64_t d,
@@ -288,6 +413,62 @@ slora_status rmsnorm_bwd_run(const void* Hin, const float* rstd, const void* g, 
     rmsnorm_bwd_kernel<<<unsigned((T + 7) / 8), 256, 0, st>>>(hin, rstd, gg, n0, n1, n2, res, T,
                                                              nch, dx);
   }
+  SLORA_CHECK_LAUNCH();
+  return SLORA_OK;
+}
+
+#define SLORA_ROW_SWITCH(KERNEL, ...)                                             \
+  if (nch <= kRowThreads) {                                                       \
+    KERNEL<1><<<rows, kRowThreads, 0, st>>>(__VA_ARGS__);                         \
+  } else if (nch <= 2 * kRowThreads) {                                            \
+    KERNEL<2><<<rows, kRowThreads, 0, st>>>(__VA_ARGS__);                         \
+  } else if (nch <= 4 * kRowThreads) {                                            \
+    KERNEL<4><<<rows, kRowThreads, 0, st>>>(__VA_ARGS__);                         \
+  } else if (nch <= 8 * kRowThreads) {                                            \
+    KERNEL<8><<<rows, kRowThreads, 0, st>>>(__VA_ARGS__);                         \
+  } else {                                                                        \
+    KERNEL<16><<<rows, kRowThreads, 0, st>>>(__VA_ARGS__);                        \
+  }
+
+slora_status rmsnorm_fwd_act8_run(const void* X, const void* A, const void* g, int64_t T,
+                                  int64_t d, float eps, void* Hout, void* N, float* rstd,
+                                  const slora_act8* H8, const slora_act8* N8, cudaStream_t st) {
+  if (T == 0) return SLORA_OK;
+  const int nch = int(d / 8);
+  LaunchScope ls(kNorm, double(T) * d * (2.0 * (2 + (A ? 1 : 0) + (A && Hout ? 1 : 0)) +
+                                         1.03125 * ((H8 ? 1 : 0) + (N8 ? 1 : 0))), st);
+  const auto* x = static_cast<const uint4*>(X);
+  const auto* a = static_cast<const uint4*>(A);
+  const auto* gg = static_cast<const uint4*>(g);
+  auto* h = static_cast<uint4*>(Hout);
+  auto* n = static_cast<uint4*>(N);
+  uint2* h8 = H8 ? reinterpret_cast<uint2*>(H8->codes) : nullptr;
+  uint8_t* h8s = H8 ? H8->scales : nullptr;
+  uint2* n8 = N8 ? reinterpret_cast<uint2*>(N8->codes) : nullptr;
+  uint8_t* n8s = N8 ? N8->scales : nullptr;
+  const unsigned rows = unsigned(T);
+  SLORA_ROW_SWITCH(rmsnorm_fwd_act8_kernel, x, a, gg, nch, eps, h, n, rstd, h8, h8s, n8, n8s)
+  SLORA_CHECK_LAUNCH();
+  return SLORA_OK;
+}
+
+slora_status rmsnorm_bwd_act8_run(const slora_act8& H8, const float* rstd, const void* g,
+                                  const void* dN0, const void* dN1, const void* dN2,
+                                  const void* dRes, int64_t T, int64_t d, void* dX,
+                                  cudaStream_t st) {
+  if (T == 0) return SLORA_OK;
+  const int nch = int(d / 8);
+  const int nin = 2 + (dN1 ? 1 : 0) + (dN2 ? 1 : 0) + (dRes ? 1 : 0);
+  LaunchScope ls(kNorm, double(T) * d * (2.0 * nin + 1.03125), st);
+  const auto* h8 = reinterpret_cast<const uint2*>(H8.codes);
+  const auto* gg = static_cast<const uint4*>(g);
+  const auto* n0 = static_cast<const uint4*>(dN0);
+  const auto* n1 = static_cast<const uint4*>(dN1);
+  const auto* n2 = static_cast<const uint4*>(dN2);
+  const auto* res = static_cast<const uint4*>(dRes);
+  auto* dx = static_cast<uint4*>(dX);
+  const unsigned rows = unsigned(T);
+  SLORA_ROW_SWITCH(rmsnorm_bwd_act8_kernel, h8, H8.scales, rstd, gg, n0, n1, n2, res, nch, dx)
   SLORA_CHECK_LAUNCH();
   return SLORA_OK;
 }

@@ -7,6 +7,7 @@
 #include "estimator.cuh"
 #include "gemm_tc.cuh"
 #include "lora_pack.cuh"
+#include "qk_rotary.cuh"
 #include "skinny.cuh"
 
 namespace slora {
@@ -283,11 +284,16 @@ extern "C" slora_status slora_device_error(int clear) {
   const slora_status d = est_check_error(clear != 0);
   const std::string fourth = d != SLORA_OK ? g_error : std::string();
   const slora_status e = attn_check_error(clear != 0);
+  const std::string fifth = e != SLORA_OK ? g_error : std::string();
+  const slora_status f = qk_check_error(clear != 0);
   if (a != SLORA_OK) g_error = first;
   else if (b != SLORA_OK) g_error = second;
   else if (c != SLORA_OK) g_error = third;
   else if (d != SLORA_OK) g_error = fourth;
-  return a != SLORA_OK ? a : (b != SLORA_OK ? b : (c != SLORA_OK ? c : (d != SLORA_OK ? d : e)));
+  else if (e != SLORA_OK) g_error = fifth;
+  for (slora_status st : {a, b, c, d, e})
+    if (st != SLORA_OK) return st;
+  return f;
 }
 
 extern "C" slora_status slora_set_wait_budget(int64_t cycles) {

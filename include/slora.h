@@ -496,6 +496,167 @@ slora_status slora_rmsnorm_bwd(slora_dtype dt, int64_t T, int64_t d, const void*
                                const void* dN1, const void* dN2, const void* dRes, void* dX,
                                void* ws, size_t* ws_bytes, slora_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Rotation of q and k with optional per-head norms.  slora_rope_pack turns
+ * whole heads by half-split pairs at unscaled angles; these two calls cover
+ * the other forms of the same step: interleaved pairs, rotation of a head's
+ * leading channels only, angles scaled for contexts longer than the trained
+ * one, explicit positions, and a learned RMS norm of every q and k head
+ * before the rotation, in one pass over the rows and with q and k in one
+ * launch.
+ * ---------------------------------------------------------------------- */
+typedef enum {
+  SLORA_ROTARY_HALF = 0,       /* pair p of a head: channels p and p + dims/2 */
+  SLORA_ROTARY_INTERLEAVED = 1 /* pair p of a head: channels 2p and 2p + 1    */
+} slora_rotary_layout;
+
+typedef enum {
+  SLORA_ROTARY_PLAIN = 0,  /* f_p = base^(-2p / dims)                                    */
+  SLORA_ROTARY_LINEAR = 1, /* f_p / factor (interpolated positions)                      */
+  SLORA_ROTARY_NTK = 2,    /* base * factor^(dims / (dims - 2)) in place of base         */
+  SLORA_ROTARY_BANDS = 3,  /* by the turns t = orig_len f_p / 2 pi of a pair: f_p above
+                              `high` turns, f_p / factor below `low`, mixed linearly in t
+                              between                                                    */
+  SLORA_ROTARY_YARN = 4    /* mixed linearly in the pair index between the pairs that make
+                              `high` and `low` turns over orig_len (rounded outwards)    */
+} slora_rotary_scaling;
+
+typedef struct {
+  int32_t layout;   /* slora_rotary_layout                                              */
+  int32_t scaling;  /* slora_rotary_scaling                                             */
+  int32_t dims;     /* rotated leading channels of a head: even, <= head_dim; 0 = all.
+                       The other channels pass through unrotated (still normalised)     */
+  int32_t orig_len; /* trained context length (BANDS, YARN)                             */
+  double base;      /* > 1                                                              */
+  double factor;    /* >= 1; PLAIN ignores it                                           */
+  double low, high; /* turns, 0 < low < high; both 0 = the usual 1 and 4 (BANDS), 1 and 32 (YARN) */
+  double mscale;    /* factor on the rotated channels; 0 = 1, or 0.1 ln(factor) + 1 (YARN) */
+} slora_rotary;
+
+/* The rows of one tensor (q or k). Strides are in elements. */
+typedef struct {
+  int32_t heads;
+  int32_t n_idx;        /* sliced rows: channels computed on context rows                */
+  const int32_t* idx;   /* NULL: dense rows. Else device [n_idx], distinct, each in
+                           [0, heads * head_dim): the channels of X_ctx's columns        */
+  const void* X;        /* dense rows [T x heads*head_dim], row stride ldx              */
+  int64_t ldx;
+  const void* X_ctx;    /* sliced: context rows [T_C x n_idx], contiguous; the channels
+                           outside idx are zero                                          */
+  const void* X_out;    /* sliced: output rows [T_O x heads*head_dim], contiguous       */
+  const void* g;        /* gain [head_dim] of the head norm, in dt; NULL: no norm        */
+  void* Y;              /* forward: written, [T x heads*head_dim], row stride ldy        */
+  int64_t ldy;
+  const void* dY;       /* backward: gradient of Y, row stride lddy                      */
+  int64_t lddy;
+  void* dX;             /* backward, dense: written, row stride lddx                     */
+  int64_t lddx;
+  void* dX_ctx;         /* backward, sliced: written, shaped like X_ctx                  */
+  void* dX_out;         /* backward, sliced: written, shaped like X_out                  */
+  float* dg;            /* backward: gradient of g [head_dim], written; NULL: g frozen   */
+} slora_qk_rows;
+
+/*
+ * slora_qk_rotary_fwd — Y = R(x) or, with a gain, Y = R(x rstd g) for every
+ * head x of q and k, rstd = 1 / sqrt(mean(x^2) + eps) over all head_dim
+ * channels; R turns pair p by pos * f_p, counterclockwise.
+ *   dt        SLORA_BF16 or SLORA_F32 (sliced rows: SLORA_BF16 only).
+ *   tok       batch, seq and ctx_len as in every call (ctx_len divides the rows
+ *             of sliced tensors; dense tensors do not use it).
+ *   head_dim  even, 2 .. 256.
+ *   eps       > 0 (only a tensor with a gain uses it).
+ *   pos       device int32 [T], any values; NULL: the row's place in its sequence.
+ *   q, k      the tensors, both dense or both sliced; k may be NULL (one
+ *             tensor).  Y may be X itself (same stride) on dense rows; no other
+ *             overlap.
+ * Angles are exact to about 1e-7 at every position: the turns are counted in
+ * 64-bit fixed point.  Sliced tensors need a workspace; dense ones none.
+ * A sliced tensor's entry outside its channels, or twice in idx, is left out
+ * and reported by slora_device_error (SLORA_ERR_INVALID_ARG).
+ */
+slora_status slora_qk_rotary_fwd(slora_dtype dt, const slora_tokens* tok, int head_dim, float eps,
+                                 const slora_rotary* rot, const int32_t* pos,
+                                 const slora_qk_rows* q, const slora_qk_rows* k, void* ws,
+                                 size_t* ws_bytes, slora_stream_t stream);
+
+/*
+ * slora_qk_rotary_bwd — gradients of slora_qk_rotary_fwd for the upstream dY
+ * of dtype gdt (dt, or SLORA_F32 as slora_attention_bwd writes dQ and dK).
+ *   X (or X_ctx, X_out) is the forward's input, read only by tensors with a
+ *   gain (rstd is recomputed from it); without one it may be NULL.  dX may be
+ *   dY or X itself (same dtype and stride) on dense rows.  dg sums over rows
+ *   and heads in a fixed order: the same call gives the same bits.
+ */
+slora_status slora_qk_rotary_bwd(slora_dtype dt, slora_dtype gdt, const slora_tokens* tok,
+                                 int head_dim, float eps, const slora_rotary* rot,
+                                 const int32_t* pos, const slora_qk_rows* q,
+                                 const slora_qk_rows* k, void* ws, size_t* ws_bytes,
+                                 slora_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Activation checkpoints in 8 bits.  A layer keeps its saved activations for
+ * the backward pass at 1 + 1/32 bytes a value in place of 2: blocks of 32
+ * channels of a row share a power-of-two step, and each value is a signed
+ * 8-bit multiple of it (the microscaling INT8 layout).
+ *   d32     = d rounded up to a multiple of 32.
+ *   codes   int8 [T x d32]; the columns past d are zero (1 in a block of NaNs).
+ *   scales  uint8 [T x d32/32]: byte b of a block means step 2^(b - 133).  A
+ *           block whose largest magnitude is in [2^e, 2^(e+1)) has b = e + 127,
+ *           at least 7; value = code * step, |code| <= 127, rounded to nearest,
+ *           ties to even.  A block that holds an infinity or a NaN has b = 255
+ *           and stands for NaNs; a block of zeros has b = 7.
+ * Every value is exact in bf16 (7 bits of magnitude).  Rounding error: at most
+ * 2^-7 of the block's largest magnitude (saturation at 127 included).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int8_t* codes;
+  uint8_t* scales;
+} slora_act8;
+
+/* X [T x d] dtype dt, row stride ldx, to a checkpoint (written). d >= 1. */
+slora_status slora_act8_pack(slora_dtype dt, int64_t T, int64_t d, const void* X, int64_t ldx,
+                             const slora_act8* ckpt, void* ws, size_t* ws_bytes,
+                             slora_stream_t stream);
+
+/* The checkpoint's values to X [T x d] dtype dt, row stride ldx (written). */
+slora_status slora_act8_unpack(slora_dtype dt, int64_t T, int64_t d, const slora_act8* ckpt,
+                               void* X, int64_t ldx, void* ws, size_t* ws_bytes,
+                               slora_stream_t stream);
+
+/*
+ * slora_rmsnorm_fwd_act8 — slora_rmsnorm_fwd that also writes checkpoints of H
+ * and / or of N in the same pass (H8, N8 may be NULL).  N is required; with A
+ * and H8, H is required too (without A, H8 is the checkpoint of X).  d up to
+ * 16384 here and in slora_rmsnorm_bwd_act8.
+ */
+slora_status slora_rmsnorm_fwd_act8(slora_dtype dt, int64_t T, int64_t d, float eps,
+                                    const void* X, const void* A, const void* g, void* H,
+                                    void* N, float* rstd, const slora_act8* H8,
+                                    const slora_act8* N8, void* ws, size_t* ws_bytes,
+                                    slora_stream_t stream);
+
+/* slora_rmsnorm_bwd with H read from its checkpoint (rstd from the forward). */
+slora_status slora_rmsnorm_bwd_act8(slora_dtype dt, int64_t T, int64_t d, const slora_act8* H8,
+                                    const float* rstd, const void* g, const void* dN0,
+                                    const void* dN1, const void* dN2, const void* dRes, void* dX,
+                                    void* ws, size_t* ws_bytes, slora_stream_t stream);
+
+/*
+ * slora_linear_bwd_act8 — slora_linear_bwd whose layer input is a checkpoint:
+ * X_ctx (and X_out, for SLORA_SLICE_IN_COLS) of the same shapes, read as codes
+ * by the dA contraction itself.  SLORA_BF16 only.  The rank-r operands dY B and
+ * XA_save enter the sums at full fp32 precision (three bf16 terms), so dA and
+ * dB are exact to fp32 rounding for the values that the checkpoint holds.
+ */
+slora_status slora_linear_bwd_act8(slora_dtype dt, const slora_tokens* tok, int64_t k, int64_t n,
+                                   const void* W, const void* A, const void* B, int r_lora,
+                                   float lora_scale, slora_slice side, const int32_t* idx,
+                                   int32_t n_idx, const slora_act8* X_ctx,
+                                   const slora_act8* X_out, const float* XA_save,
+                                   const void* dY_ctx, const void* dY_out, void* dX_ctx,
+                                   void* dX_out, float* dA, float* dB, void* ws,
+                                   size_t* ws_bytes, slora_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

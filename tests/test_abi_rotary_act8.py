@@ -1,0 +1,231 @@
+"""Host-side validation of the q/k rotation and of the 8-bit checkpoints: what
+the calls refuse, and their workspace queries (no GPU: nothing is launched)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from tests import qk_reference as R
+
+FAKE = 0x10000  # 16-byte aligned dummy address: never dereferenced
+OK, INVALID, SHAPE, ALIGN, WORKSPACE, UNSUPPORTED = 0, 1, 2, 3, 4, 5
+
+
+@pytest.fixture(scope="module")
+def L():
+    from contextual_sparsity_lora_svd_b200 import build
+    build.build()
+    from contextual_sparsity_lora_svd_b200 import _lib
+    return _lib
+
+
+def status(L, name, args):
+    need = ctypes.c_size_t(0)
+    return getattr(L.lib(), name)(*args, None, ctypes.byref(need), None), int(need.value)
+
+
+def dense(L, heads=4, hd=64, **over):
+    n = heads * hd
+    f = dict(heads=heads, n_idx=0, idx=None, X=FAKE, ldx=n, X_ctx=None, X_out=None, g=FAKE,
+             Y=FAKE, ldy=n, dY=FAKE, lddy=n, dX=FAKE * 2, lddx=n, dX_ctx=None, dX_out=None, dg=None)
+    f.update(over)
+    return L.QkRows(*[f[name] for name, _ in L.QkRows._fields_])
+
+
+def fwd(L, q, k=None, dt=None, rot=None, hd=64, eps=1e-5, pos=None, ctx=(3, 2)):
+    tok, keep = L.make_tokens(2, 5, ctx)
+    rot = rot or L.rotary()
+    return status(L, "slora_qk_rotary_fwd",
+                  [L.BF16 if dt is None else dt, ctypes.byref(tok), hd, eps, ctypes.byref(rot), pos,
+                   ctypes.byref(q), None if k is None else ctypes.byref(k)])
+
+
+def bwd(L, q, k=None, dt=None, gdt=None, hd=64, ctx=(3, 2), **kw):
+    tok, keep = L.make_tokens(2, 5, ctx)
+    rot = L.rotary()
+    dt = L.BF16 if dt is None else dt
+    return status(L, "slora_qk_rotary_bwd",
+                  [dt, dt if gdt is None else gdt, ctypes.byref(tok), hd, 1e-5, ctypes.byref(rot),
+                   None, ctypes.byref(q), None if k is None else ctypes.byref(k)])
+
+
+def test_dense_calls_need_no_workspace(L):
+    assert fwd(L, dense(L), dense(L, 2)) == (OK, 0)
+    assert fwd(L, dense(L, g=None), dt=L.F32) == (OK, 0)
+    assert bwd(L, dense(L), dense(L, 2)) == (OK, 0)
+    st, need = bwd(L, dense(L, dg=FAKE))
+    assert st == OK and need >= 64 * 4
+
+
+def test_sliced_calls_need_the_channel_maps(L):
+    s = dict(idx=FAKE, n_idx=100, X=None, X_ctx=FAKE, X_out=FAKE, dX_ctx=FAKE, dX_out=FAKE)
+    st, need = fwd(L, dense(L, **s))
+    assert st == OK and need >= 4 * 64 * 4 + 3 * 4
+    assert bwd(L, dense(L, **s))[0] == OK
+    assert fwd(L, dense(L, **s), dense(L, 2))[0] == SHAPE              # one sliced, one dense
+    assert fwd(L, dense(L, **s), dt=L.F32)[0] == UNSUPPORTED
+    assert fwd(L, dense(L, **dict(s, n_idx=257)))[0] == SHAPE
+    assert fwd(L, dense(L, **dict(s, n_idx=-1)))[0] == SHAPE
+    assert fwd(L, dense(L, **dict(s, X_ctx=None)))[0] == INVALID
+    assert fwd(L, dense(L, **dict(s, X_ctx=None)), ctx=(0, 0))[0] == OK  # no context rows
+    assert fwd(L, dense(L, **dict(s, X_out=None)), ctx=(5, 5))[0] == OK  # no output rows
+    assert bwd(L, dense(L, **dict(s, dX_out=None)))[0] == INVALID
+    assert bwd(L, dense(L, **dict(s, X_ctx=None, X_out=None, g=None)))[0] == OK  # x unread
+
+
+def test_row_refusals(L):
+    assert fwd(L, dense(L, X=None))[0] == INVALID
+    assert fwd(L, dense(L, Y=None))[0] == INVALID
+    assert fwd(L, dense(L, X=FAKE + 8))[0] == ALIGN
+    assert fwd(L, dense(L, ldx=255))[0] == SHAPE
+    assert fwd(L, dense(L, ldy=255, Y=FAKE * 2))[0] == SHAPE
+    assert fwd(L, dense(L, ldy=512))[0] == INVALID                     # in place, another stride
+    assert fwd(L, dense(L, heads=0))[0] == SHAPE
+    assert fwd(L, dense(L), hd=63)[0] == SHAPE
+    assert fwd(L, dense(L), hd=258)[0] == SHAPE
+    assert fwd(L, dense(L), eps=0.0)[0] == INVALID
+    assert fwd(L, dense(L), eps=float("nan"))[0] == INVALID
+    assert fwd(L, dense(L, g=None), eps=0.0)[0] == OK                  # eps unused
+    assert fwd(L, dense(L), dt=7)[0] == INVALID
+    assert fwd(L, dense(L), pos=FAKE + 2)[0] == ALIGN
+    assert fwd(L, dense(L), ctx=(6, 0))[0] == SHAPE
+    assert bwd(L, dense(L, dY=None))[0] == INVALID
+    assert bwd(L, dense(L, X=None))[0] == INVALID
+    assert bwd(L, dense(L, X=None, g=None))[0] == OK
+    assert bwd(L, dense(L, dX=FAKE), gdt=L.F32)[0] == INVALID          # dX over a dY of another type
+    assert bwd(L, dense(L), dt=L.F32, gdt=L.BF16)[0] == INVALID
+    assert bwd(L, dense(L, dg=FAKE + 4))[0] == ALIGN
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(dims=66), SHAPE), (dict(dims=3), SHAPE), (dict(dims=-2), SHAPE), (dict(base=1.0), INVALID),
+    (dict(base=float("inf")), INVALID), (dict(scaling="linear", factor=0.5), INVALID),
+    (dict(scaling="linear", factor=float("nan")), INVALID), (dict(mscale=-1.0), INVALID),
+    (dict(scaling="bands", factor=2.0), SHAPE), (dict(scaling="yarn", factor=2.0), SHAPE),
+    (dict(scaling="bands", factor=2.0, orig_len=64, low=4.0, high=1.0), INVALID),
+    (dict(scaling="ntk", factor=2.0, dims=2), SHAPE),
+    (dict(scaling="ntk", factor=1e300, base=1e300, dims=4), INVALID),
+    (dict(factor=0.0), OK), (dict(dims=64), OK), (dict(scaling="ntk", factor=2.0), OK)])
+def test_rotary_refusals(L, kw, want):
+    assert fwd(L, dense(L), rot=L.rotary(**kw))[0] == want
+    assert fwd(L, dense(L), rot=L.Rotary(9, 0, 0, 0, 1e4, 1, 0, 0, 0))[0] == INVALID
+    assert fwd(L, dense(L), rot=L.Rotary(0, 9, 0, 0, 1e4, 1, 0, 0, 0))[0] == INVALID
+
+
+def test_binding_refuses_wrong_tensors(L):
+    X = torch.zeros(4, 128)
+    with pytest.raises(TypeError):
+        L.qk_rows(2, X=X, Y=X.bfloat16())
+    with pytest.raises(TypeError):
+        L.qk_rows(2, X=X, dg=torch.zeros(64, dtype=torch.float64))
+    with pytest.raises(TypeError):
+        L.qk_rows(2, X_ctx=X, idx=torch.zeros(4, dtype=torch.int64))
+    with pytest.raises(ValueError):
+        L.qk_rows(2, X=X.t())
+    with pytest.raises(ValueError):
+        L.act8(torch.zeros(4, 100, dtype=torch.int8), torch.zeros(4, 4, dtype=torch.uint8), 4, 100)
+    with pytest.raises(TypeError):
+        L.slora_qk_rotary_fwd(2, 2, 64, L.qk_rows(2, X=X, Y=X), pos=torch.zeros(4), stream=0)
+    with pytest.raises(KeyError):
+        L.rotary(scaling="other")
+
+
+def test_act8_refusals(L):
+    c = L.Act8(FAKE, FAKE)
+    ref = ctypes.byref(c)
+    pack = lambda dt, T, d, X, ld, ck: status(L, "slora_act8_pack", [dt, T, d, X, ld, ck])
+    assert pack(L.BF16, 4, 100, FAKE, 100, ref) == (OK, 0)
+    assert pack(L.F32, 4, 1, FAKE, 1, ref) == (OK, 0)
+    assert pack(L.BF16, 0, 100, None, 100, None) == (OK, 0)            # nothing to do
+    assert pack(5, 4, 100, FAKE, 100, ref)[0] == INVALID
+    assert pack(L.BF16, 4, 0, FAKE, 100, ref)[0] == SHAPE
+    assert pack(L.BF16, -1, 8, FAKE, 100, ref)[0] == SHAPE
+    assert pack(L.BF16, 4, 100, FAKE, 99, ref)[0] == SHAPE
+    assert pack(L.BF16, 4, 100, None, 100, ref)[0] == INVALID
+    assert pack(L.BF16, 4, 100, FAKE + 2, 100, ref)[0] == ALIGN
+    assert pack(L.BF16, 4, 100, FAKE, 100, None)[0] == INVALID
+    half = L.Act8(FAKE, None)
+    assert pack(L.BF16, 4, 100, FAKE, 100, ctypes.byref(half))[0] == INVALID
+    odd = L.Act8(FAKE, FAKE + 1)
+    assert pack(L.BF16, 4, 100, FAKE, 100, ctypes.byref(odd))[0] == ALIGN
+    un = lambda T, d, ck, X, ld: status(L, "slora_act8_unpack", [L.BF16, T, d, ck, X, ld])
+    assert un(4, 100, ref, FAKE, 100) == (OK, 0)
+    assert un(4, 100, None, FAKE, 100)[0] == INVALID
+    assert un(4, 100, ref, FAKE, 64)[0] == SHAPE
+
+
+def test_norm_act8_refusals(L):
+    c = L.Act8(FAKE, FAKE)
+    ref = ctypes.byref(c)
+    f = lambda d=64, A=None, H=None, N=FAKE, h8=ref, n8=ref, dt=L.BF16, eps=1e-5: status(
+        L, "slora_rmsnorm_fwd_act8", [dt, 4, d, eps, FAKE, A, FAKE, H, N, FAKE, h8, n8])
+    assert f() == (OK, 0)
+    assert f(h8=None, n8=None) == (OK, 0)
+    assert f(d=16384) == (OK, 0)
+    assert f(d=16392)[0] == SHAPE
+    assert f(d=60)[0] == SHAPE
+    assert f(dt=L.F32)[0] == UNSUPPORTED
+    assert f(N=None)[0] == INVALID
+    assert f(A=FAKE)[0] == INVALID                                     # H8 of an unstored sum
+    assert f(A=FAKE, h8=None) == (OK, 0)
+    assert f(eps=-1.0)[0] == INVALID
+    b = lambda h8=ref, dN=FAKE, d=64: status(
+        L, "slora_rmsnorm_bwd_act8", [L.BF16, 4, d, h8, FAKE, FAKE, dN, None, None, None, FAKE])
+    assert b() == (OK, 0)
+    assert b(h8=None)[0] == INVALID
+    assert b(dN=None)[0] == INVALID
+    assert b(d=16392)[0] == SHAPE
+
+
+def test_linear_bwd_act8_refusals(L):
+    tok, keep = L.make_tokens(2, 40, [30, 20])
+    c = L.Act8(FAKE, FAKE)
+    ref = ctypes.byref(c)
+
+    def call(side, dt=L.BF16, xc=ref, xo=ref, n_idx=20, dyc=FAKE, dyo=FAKE, dxo=FAKE, t=tok, k=72):
+        return status(L, "slora_linear_bwd_act8",
+                      [dt, ctypes.byref(t), k, 72, FAKE, FAKE, FAKE, 8, 1.0, side, FAKE, n_idx, xc, xo,
+                       FAKE, dyc, dyo, FAKE, dxo, FAKE, FAKE])
+
+    for side in (L.SLICE_NONE, L.SLICE_OUT_ROWS, L.SLICE_IN_COLS):
+        st, need = call(side)
+        assert st == OK and need > 0
+        assert call(side, dt=L.F32)[0] == UNSUPPORTED
+        assert call(side, xc=None)[0] == INVALID
+        assert call(side, dyc=None)[0] == INVALID
+        assert call(side, k=70)[0] == SHAPE
+    assert call(L.SLICE_IN_COLS, xo=None)[0] == INVALID
+    assert call(L.SLICE_IN_COLS, dxo=None)[0] == INVALID
+    assert call(L.SLICE_NONE, xo=None, dxo=None)[0] == OK
+    assert call(L.SLICE_OUT_ROWS, dyo=None)[0] == INVALID
+    assert call(L.SLICE_IN_COLS, n_idx=73)[0] == SHAPE
+    none, keep2 = L.make_tokens(2, 40, [0, 0])
+    assert call(L.SLICE_IN_COLS, xc=None, t=none)[0] == OK             # no context rows
+    assert call(L.SLICE_OUT_ROWS, dyc=None, t=none)[0] == OK
+
+
+def test_reference_checkpoint_values():
+    """The reference itself, on hand-worked blocks."""
+    x = np.zeros((1, 40))
+    x[0, :3] = [1.0, -0.5, 1.0 / 64]
+    x[0, 32] = 3.0
+    codes, scales, v = R.act8(x)
+    assert codes[0, :3].tolist() == [64, -32, 1] and scales[0].tolist() == [127, 128]
+    assert codes[0, 32] == 96 and v[0, 32] == 3.0 and codes[0, 40:].tolist() == [0] * 24
+    x[0, 0] = 255.0 / 128  # 127.5 steps: saturates
+    assert R.act8(x)[0][0, 0] == 127
+
+
+def test_reference_frequencies_by_hand():
+    f, m = R.frequencies(4, base=100.0)
+    assert np.allclose(f, [1.0, 0.1], rtol=1e-15) and m == 1.0
+    f, m = R.frequencies(4, base=100.0, scaling="linear", factor=4.0)
+    assert np.allclose(f, [0.25, 0.025], rtol=1e-15)
+    f, _ = R.frequencies(4, base=100.0, scaling="ntk", factor=10.0)
+    assert np.allclose(f, [1.0, 0.01], rtol=1e-12)  # base 100 * 10^2
+    # 2 pi / f = 6.28, 62.8 over a context of 31.4: 5 turns and half a turn
+    f, _ = R.frequencies(4, base=100.0, scaling="bands", factor=8.0, orig_len=31)
+    assert np.allclose(f, [1.0, 0.1 / 8], rtol=1e-15)
+    _, m = R.frequencies(8, scaling="yarn", factor=4.0, orig_len=4096)
+    assert m == pytest.approx(0.1 * np.log(4.0) + 1.0)

@@ -1,0 +1,331 @@
+"""GPU: 8-bit activation checkpoints (slora_act8_pack / _unpack), the RMS norm
+that writes and reads them, and the LoRA linear backward from one, against
+float64 definitions.  Codes, scale bytes and values are exact; gradients count
+the roundings of their stored type and of fp32 sums."""
+import numpy as np
+import pytest
+import torch
+
+from tests import qk_reference as R
+from tests.helpers import rel_frob
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def L():
+    from contextual_sparsity_lora_svd_b200 import _lib
+    return _lib
+
+
+def rand(gen, shape, dt=torch.bfloat16, scale=1.0):
+    return (torch.randn(shape, generator=gen, device="cuda") * scale).to(dt)
+
+
+def gen_of(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def rows_in_earnest(gen, T, d, dt):
+    """Loud channels, a zero row, wide and subnormal magnitudes."""
+    X = torch.randn((T, d), generator=gen, device="cuda")
+    X *= torch.exp2(torch.randint(-9, 9, (T, 1), generator=gen, device="cuda").float())
+    X[:, ::17] *= 50
+    if T > 2:
+        X[1] = 0
+        X[2] *= 2.0 ** -125
+    return X.to(dt)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,d", [(1, 1), (1, 32), (3, 31), (5, 33), (7, 688), (2, 4096), (13, 100),
+                                 (1, 4097), (260, 8)])
+def test_pack_and_unpack_are_exact(L, dt, T, d):
+    X = rows_in_earnest(gen_of(T + d), T, d, dt)
+    codes, scales = L.act8_empty(T, d)
+    codes.fill_(77)
+    scales.fill_(77)
+    L.slora_act8_pack(X, codes, scales)
+    c, b, v = R.act8(R.f64(X))
+    assert np.array_equal(codes.cpu().numpy(), c)
+    assert np.array_equal(scales.cpu().numpy(), b)
+    for out in (torch.bfloat16, torch.float32):
+        Y = torch.full((T, d), 9.0, dtype=out, device="cuda")
+        L.slora_act8_unpack(codes, scales, Y)
+        assert np.array_equal(R.f64(Y), v)
+    # the error bound of the format: 2^-7 of the block's largest magnitude
+    pad = np.zeros((T, codes.shape[1]))
+    pad[:, :d] = R.f64(X)
+    err = np.zeros_like(pad)
+    err[:, :d] = np.abs(v - R.f64(X))
+    top = np.abs(pad).reshape(T, -1, 32).max(2)
+    assert (err.reshape(T, -1, 32).max(2) <= np.maximum(top * 2.0 ** -7, 2.0 ** -127)).all()
+
+
+def test_ties_and_saturation(L):
+    X = torch.zeros(2, 32, device="cuda")
+    X[0, :6] = torch.tensor([64.0, 0.5, 1.5, 2.5, -0.5, -1.5])  # step 1: ties to even
+    X[1, :4] = torch.tensor([127.75, -127.75, 127.4, 126.5])     # past 127: saturated
+    codes, scales = L.act8_empty(2, 32)
+    L.slora_act8_pack(X, codes, scales)
+    assert codes[0, :6].tolist() == [64, 0, 2, 2, 0, -2] and scales[0, 0] == 133
+    assert codes[1, :4].tolist() == [127, -127, 127, 126]
+
+
+def test_infinities_and_nan_mark_their_block(L):
+    X = torch.randn(3, 96, device="cuda").bfloat16()
+    X[0, 40] = float("inf")
+    X[1, 3] = float("nan")
+    X[2, 95] = float("-inf")
+    codes, scales = L.act8_empty(3, 96)
+    L.slora_act8_pack(X, codes, scales)
+    Y = torch.empty_like(X)
+    L.slora_act8_unpack(codes, scales, Y)
+    nan = torch.zeros(3, 3, dtype=torch.bool, device="cuda")
+    nan[0, 1] = nan[1, 0] = nan[2, 2] = True
+    assert torch.equal(Y.view(3, 3, 32).isnan().all(2), nan)
+    assert torch.equal(Y.view(3, 3, 32).isnan().any(2), nan)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("pad", [1, 8, 24])
+def test_strided_rows(L, dt, pad):
+    T, d = 9, 72
+    B = rows_in_earnest(gen_of(1), T, d + pad, dt)
+    codes, scales = L.act8_empty(T, d)
+    L.slora_act8_pack(B[:, :d], codes, scales)
+    c, b, v = R.act8(R.f64(B[:, :d]))
+    assert np.array_equal(codes.cpu().numpy(), c) and np.array_equal(scales.cpu().numpy(), b)
+    out = torch.full((T, d + pad), 4.0, dtype=dt, device="cuda")
+    L.slora_act8_unpack(codes, scales, out[:, :d])
+    assert np.array_equal(R.f64(out[:, :d]), v) and (out[:, d:] == 4).all()
+
+
+def test_large_checkpoint_on_another_stream(L):
+    """More chunks than one wave, packed on a side stream while another runs."""
+    T, d = 3001, 5000
+    X = rand(gen_of(3), (T, d))
+    codes, scales = L.act8_empty(T, d)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    L.slora_act8_pack(X, codes, scales, stream=st)
+    st.synchronize()
+    rows = [0, 1, 1500, 3000]
+    c, b, _ = R.act8(R.f64(X[rows]))
+    assert np.array_equal(codes[rows].cpu().numpy(), c)
+    assert np.array_equal(scales[rows].cpu().numpy(), b)
+
+
+# ------------------------------------------------------------------ norm
+@pytest.mark.parametrize("T,d", [(1, 8), (5, 688), (3, 1032), (2, 4096), (70, 2040), (2, 8200),
+                                 (2, 16384)])
+@pytest.mark.parametrize("res", [True, False])
+def test_norm_writes_its_checkpoints(L, T, d, res):
+    gen = gen_of(d)
+    X, A, g = rand(gen, (T, d)), rand(gen, (T, d)) if res else None, rand(gen, (d,))
+    H, N, rstd = torch.empty_like(X), torch.empty_like(X), torch.empty(T, device="cuda")
+    H2, N2, rstd2 = torch.empty_like(X), torch.empty_like(X), torch.empty(T, device="cuda")
+    H8, N8 = L.act8_empty(T, d), L.act8_empty(T, d)
+    L.slora_rmsnorm_fwd(X, g, N=N, A=A, H=H if res else None, rstd=rstd)
+    L.slora_rmsnorm_fwd_act8(X, g, N2, rstd2, A=A, H=H2 if res else None, H8=H8, N8=N8)
+    assert torch.equal(N, N2) and torch.equal(rstd, rstd2)
+    if res:
+        assert torch.equal(H, H2)
+    for ck, src in ((H8, H if res else X), (N8, N)):
+        want = L.act8_empty(T, d)
+        L.slora_act8_pack(src, *want)
+        assert torch.equal(ck[0], want[0]) and torch.equal(ck[1], want[1])
+    # one of the two alone
+    H9, N9 = L.act8_empty(T, d), L.act8_empty(T, d)
+    L.slora_rmsnorm_fwd_act8(X, g, N2, A=A, H=H2 if res else None, H8=H9)
+    L.slora_rmsnorm_fwd_act8(X, g, N2, A=A, N8=N9)
+    assert torch.equal(H8[0], H9[0]) and torch.equal(N8[0], N9[0])
+
+
+@pytest.mark.parametrize("T,d", [(1, 8), (5, 688), (3, 1032), (9, 4096), (2, 8200), (2, 16384)])
+@pytest.mark.parametrize("extra", [0, 1, 2])
+def test_norm_backward_reads_its_checkpoint(L, T, d, extra):
+    """The bits of slora_rmsnorm_bwd on the checkpoint's values, and float64."""
+    gen = gen_of(d + extra)
+    X, g = rand(gen, (T, d)), rand(gen, (d,))
+    dN = [rand(gen, (T, d)) for _ in range(1 + extra)] + [None] * (2 - extra)
+    dRes = rand(gen, (T, d)) if extra else None
+    H8 = L.act8_empty(T, d)
+    L.slora_act8_pack(X, *H8)
+    V = torch.empty_like(X)
+    L.slora_act8_unpack(*H8, V)
+    x = R.f64(X)
+    rstd = torch.tensor(1 / np.sqrt((x ** 2).mean(1) + 1e-5), dtype=torch.float32, device="cuda")
+    dX, dX2 = torch.empty_like(X), torch.empty_like(X)
+    L.slora_rmsnorm_bwd_act8(H8, rstd, g, dN[0], dX, dN1=dN[1], dN2=dN[2], dRes=dRes)
+    L.slora_rmsnorm_bwd(V, rstd, g, dN[0], dX2, dN1=dN[1], dN2=dN[2], dRes=dRes)
+    assert torch.equal(dX, dX2)
+    v, r = R.f64(V), R.f64(rstd)[:, None]
+    u = sum(R.f64(t) for t in dN if t is not None) * R.f64(g)
+    c = r ** 3 * (u * v).mean(1, keepdims=True)
+    base = 0 if dRes is None else R.f64(dRes)
+    want = base + r * u - v * c
+    # half a bf16 step of the result; the fp32 sum of d terms within 2^-16 of their magnitudes
+    size = np.abs(base) + r * np.abs(u) + np.abs(v) * r ** 3 * np.abs(u * v).mean(1, keepdims=True)
+    assert (np.abs(R.f64(dX) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -16 * size).all()
+
+
+# -------------------------------------------------------- linear backward
+def linear_case(L, side, b, s, ctx, k, n, r, ni, seed=0, scale=2.0, idx=None):
+    """One call against float64; returns the outputs."""
+    gen = gen_of(seed)
+    T, TC = b * s, sum(ctx)
+    is_ctx = np.concatenate([np.arange(s) < c for c in ctx])
+    W = rand(gen, (n, k), scale=k ** -0.5)
+    A, B = rand(gen, (r, k), scale=k ** -0.5), rand(gen, (n, r), scale=0.1)
+    cols = {"none": n, "out_rows": n, "in_cols": k}[side]
+    if side != "none" and idx is None:
+        pick = torch.randperm(cols, generator=gen, device="cuda")[:ni]
+        idx = torch.sort(pick).values.int()
+    empty = lambda t: t if t.numel() else None
+    x = np.zeros((T, k))
+    dy = np.zeros((T, n))
+    if side == "in_cols":
+        Xc, Xo = rand(gen, (TC, ni)), rand(gen, (T - TC, k))
+        X8, O8 = L.act8_empty(TC, ni), L.act8_empty(T - TC, k)
+        if Xc.numel():
+            L.slora_act8_pack(Xc, *X8)
+            rows = np.zeros((TC, k))
+            rows[:, R.f64(idx).astype(int)] = R.act8(R.f64(Xc))[2]
+            x[is_ctx] = rows
+        if Xo.numel():
+            L.slora_act8_pack(Xo, *O8)
+            x[~is_ctx] = R.act8(R.f64(Xo))[2]
+        dYc, dYo = rand(gen, (T, n)), None
+        dy = R.f64(dYc)
+        dXc, dXo = torch.full_like(Xc, 3), torch.full_like(Xo, 3)
+    else:
+        X = rand(gen, (T, k))
+        X8, O8 = L.act8_empty(T, k), None
+        L.slora_act8_pack(X, *X8)
+        x = R.act8(R.f64(X))[2]
+        nc, rc = (n, T) if side == "none" else (ni, TC)
+        dYc, dYo = rand(gen, (rc, nc)), rand(gen, (T - rc, n))
+        if side == "none":
+            dy = R.f64(dYc)
+        else:
+            rows = np.zeros((TC, n))
+            rows[:, R.f64(idx).astype(int)] = R.f64(dYc)
+            dy[is_ctx], dy[~is_ctx] = rows, R.f64(dYo)
+        dXc, dXo = torch.full_like(X, 3), None
+    XA = rand(gen, (T, r), torch.float32)
+    dA, dB = torch.full((r, k), 3.0, device="cuda"), torch.full((n, r), 3.0, device="cuda")
+    Wd = W.t().contiguous() if side == "in_cols" else W
+    code = {"none": L.SLICE_NONE, "out_rows": L.SLICE_OUT_ROWS, "in_cols": L.SLICE_IN_COLS}[side]
+    L.slora_linear_bwd_act8(code, b, s, ctx, k, n, Wd, A, B, scale, idx, X8, XA, dYc, dXc, dA, dB,
+                            X8_out=O8, dY_out=None if dYo is None else empty(dYo), dX_out=dXo)
+    torch.cuda.synchronize()
+    w, a, bb, xa = R.f64(W), R.f64(A), R.f64(B), R.f64(XA)
+    p = dy @ bb
+    want = dy @ w + scale * p @ a
+    got = np.zeros((T, k))
+    if side == "in_cols":
+        sel = R.f64(idx).astype(int)
+        got, mask = np.zeros((T, k)), np.zeros((T, k), dtype=bool)
+        if TC and ni:
+            block = np.zeros((TC, k))
+            block[:, sel] = R.f64(dXc)
+            got[is_ctx] = block
+            m = np.zeros((TC, k), dtype=bool)
+            m[:, sel] = True
+            mask[is_ctx] = m
+        if T - TC:
+            got[~is_ctx] = R.f64(dXo)
+            mask[~is_ctx] = True
+        want = want * mask
+    else:
+        got = R.f64(dXc)
+    # dX in bf16: half a step of the result and the LoRA part's operand in bf16
+    # (2^-8 each of its terms), in the 2-norm well inside 2^-7
+    assert rel_frob(got, want) <= 2.0 ** -7
+    # fp32 gradients: dYB and the sums in fp32 (tensor-core sums of K or M terms,
+    # three bf16 terms of an fp32 operand to 2^-24): 1e-5 in the 2-norm
+    assert rel_frob(R.f64(dA), scale * p.T @ x) <= 1e-5
+    assert rel_frob(R.f64(dB), scale * dy.T @ xa) <= 1e-5
+    return dXc, dA, dB
+
+
+@pytest.mark.parametrize("side", ["none", "out_rows", "in_cols"])
+@pytest.mark.parametrize("b,s,ctx,k,n,r", [
+    (1, 1, [1], 64, 64, 8), (2, 9, [4, 7], 72, 152, 5), (1, 300, [200], 688, 256, 16),
+    (3, 90, [90, 0, 33], 256, 688, 32), (1, 130, [100], 136, 72, 64), (2, 700, [500, 400], 520, 264, 1),
+    (1, 16, [16], 128, 64, 17)])
+def test_linear_backward(L, side, b, s, ctx, k, n, r):
+    cols = {"none": 0, "out_rows": n, "in_cols": k}[side]
+    linear_case(L, side, b, s, ctx, k, n, r, cols // 2)
+
+
+@pytest.mark.parametrize("side", ["out_rows", "in_cols"])
+@pytest.mark.parametrize("ctx,ni", [([0, 0], 20), ([40, 40], 33), ([17, 40], 0), ([40, 40], 0),
+                                    ([1, 0], 1), ([23, 31], 72)])
+def test_linear_backward_empty_parts(L, side, ctx, ni):
+    linear_case(L, side, 2, 40, ctx, 72, 72, 8, ni)
+
+
+def test_linear_backward_is_the_bf16_call_on_the_values(L):
+    """dX has the bits of slora_linear_bwd (which does not read the activation
+    for it); the gradients agree to that call's bf16 operands."""
+    b, s, ctx, k, n, r = 2, 200, [150, 120], 256, 384, 16
+    gen = gen_of(9)
+    T = b * s
+    W, A, B = rand(gen, (n, k)), rand(gen, (r, k)), rand(gen, (n, r))
+    X, dY, XA = rand(gen, (T, k)), rand(gen, (T, n)), rand(gen, (T, r), torch.float32)
+    X8 = L.act8_empty(T, k)
+    L.slora_act8_pack(X, *X8)
+    V = torch.empty_like(X)
+    L.slora_act8_unpack(*X8, V)
+    o = [[torch.empty_like(X), torch.empty(r, k, device="cuda"), torch.empty(n, r, device="cuda")]
+         for _ in range(3)]
+    for i in range(2):
+        L.slora_linear_bwd_act8(L.SLICE_NONE, b, s, ctx, k, n, W, A, B, 0.5, None, X8, XA, dY, *o[i])
+    L.slora_linear_bwd(L.SLICE_NONE, b, s, ctx, k, n, W, A, B, 0.5, None, V, XA, dY, *o[2])
+    assert all(torch.equal(x, y) for x, y in zip(o[0], o[1]))  # the same bits again
+    assert torch.equal(o[0][0], o[2][0])
+    for i in (1, 2):
+        assert rel_frob(R.f64(o[0][i]), R.f64(o[2][i])) <= 2.0 ** -8
+
+
+def test_linear_backward_large_split(L):
+    """Many tokens and few channels: partial sums of many blocks, same bits twice."""
+    x = [linear_case(L, "none", 1, 6000, [4000], 64, 64, 16, 0, seed=3) for _ in range(2)]
+    assert all(torch.equal(p, q) for p, q in zip(*x))
+
+
+def test_linear_backward_captured(L):
+    """Captured and replayed twice: the eager bits (counters are left ready)."""
+    b, s, ctx, k, n, r = 1, 1024, [700], 512, 256, 16
+    gen = gen_of(5)
+    T = b * s
+    W, A, B = rand(gen, (n, k)), rand(gen, (r, k)), rand(gen, (n, r))
+    X, dY, XA = rand(gen, (T, k)), rand(gen, (T, n)), rand(gen, (T, r), torch.float32)
+    X8 = L.act8_empty(T, k)
+    out = [torch.empty_like(X), torch.empty(r, k, device="cuda"), torch.empty(n, r, device="cuda")]
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+
+    def step(st=None):
+        L.slora_act8_pack(X, *X8, stream=st)
+        L.slora_linear_bwd_act8(L.SLICE_NONE, b, s, ctx, k, n, W, A, B, 0.5, None, X8, XA, dY, *out,
+                                ws=ws, stream=st)
+
+    step()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in out]
+    st = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(st):
+        with torch.cuda.graph(graph, stream=st):
+            step(st)
+    for _ in range(2):
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(out, want))
+    assert L.lib().slora_device_error(1) == 0
