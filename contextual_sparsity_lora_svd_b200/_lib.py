@@ -431,48 +431,69 @@ def rotary(layout="half", dims=0, base=ROPE_BASE, scaling="none", factor=1.0, or
 
 def _rows(t, what):
     """(address, row stride) of a 2-D tensor whose rows are contiguous."""
-    if t is None:
-        return None, 0
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    st = t.stride()
+    n = t.shape
+    if len(st) != 2 or (st[1] != 1 and n[1] > 1):
         raise ValueError(f"{what}: a 2-D tensor with contiguous rows is needed")
-    return ptr(t), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return t.data_ptr(), st[0] if n[0] > 1 else max(st[0], n[1])
 
 
 def _whole(t, what):
-    if t is not None and not t.is_contiguous():
+    if not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous tensor is needed")
-    return ptr(t)
+    return t.data_ptr()
 
 
 def qk_rows(heads, X=None, g=None, Y=None, dY=None, dX=None, dg=None, idx=None, X_ctx=None,
             X_out=None, dX_ctx=None, dX_out=None) -> QkRows:
     """The rows of q or k for slora_qk_rotary_fwd / _bwd: dense (X, Y, dX may
     have any row stride), or with `idx` sliced (X_ctx, X_out, dX_ctx, dX_out
-    contiguous).  The struct keeps its tensors alive."""
-    px, ldx = _rows(X, "X")
-    py, ldy = _rows(Y, "Y")
-    pdy, lddy = _rows(dY, "dY")
-    pdx, lddx = _rows(dX, "dX")
-    sliced = idx is not None
-    # an empty list is still a list: its address, never read, may be null
-    pidx = (ptr(idx) or ptr(X_out) or ptr(dX_out) or ptr(Y)) if sliced else None
-    r = QkRows(int(heads), idx.numel() if sliced else 0, pidx, px, ldx, _whole(X_ctx, "X_ctx"),
-               _whole(X_out, "X_out"), _whole(g, "g"), py, ldy, pdy, lddy, pdx, lddx,
-               _whole(dX_ctx, "dX_ctx"), _whole(dX_out, "dX_out"), _whole(dg, "dg"))
+    contiguous).  The struct keeps its tensors alive; a program that calls more
+    than once on the same buffers builds it once."""
+    r = QkRows(heads)
+    dts = set()
+    if X is not None:
+        r.X, r.ldx = _rows(X, "X")
+        dts.add(X.dtype)
+    if Y is not None:
+        r.Y, r.ldy = _rows(Y, "Y")
+        dts.add(Y.dtype)
+    if dX is not None:
+        r.dX, r.lddx = _rows(dX, "dX")
+        dts.add(dX.dtype)
+    if g is not None:
+        r.g = _whole(g, "g")
+        dts.add(g.dtype)
+    r.gdt = F32
+    if dY is not None:
+        r.dY, r.lddy = _rows(dY, "dY")
+        r.gdt = dtype_code(dY)
+    if dg is not None:
+        r.dg = _whole(dg, "dg")
+        if dg.dtype != torch.float32:
+            raise TypeError("dg is an fp32 tensor")
+    r.scratch = dg is not None
+    if idx is not None:
+        if idx.dtype != torch.int32:
+            raise TypeError("idx is an int32 tensor")
+        r.scratch = True
+        r.n_idx = idx.numel()
+        for name, t in (("X_ctx", X_ctx), ("X_out", X_out), ("dX_ctx", dX_ctx), ("dX_out", dX_out)):
+            if t is not None:
+                setattr(r, name, _whole(t, name))
+                dts.add(t.dtype)
+        # an empty list is still a list: its address, never read, may be null
+        r.idx = _whole(idx, "idx") or r.X_out or r.dX_out or r.Y or r.dY
+    if len(dts) != 1:
+        raise TypeError(f"the rows and the gain have one dtype, not {dts}")
+    r.dt = _DTYPES.get(dts.pop())
+    if r.dt is None:
+        raise TypeError("the rows are bf16 or fp32 tensors")
     r.tensors = (X, g, Y, dY, dX, dg, idx, X_ctx, X_out, dX_ctx, dX_out)
-    first = next(t for t in (X, X_ctx, X_out, dX, dX_ctx, dX_out, Y) if t is not None)
-    for t, what in ((X, "X"), (X_ctx, "X_ctx"), (X_out, "X_out"), (g, "g"), (Y, "Y"), (dX, "dX"),
-                    (dX_ctx, "dX_ctx"), (dX_out, "dX_out")):
-        if t is not None and t.dtype != first.dtype:
-            raise TypeError(f"{what} is {t.dtype}, the rows are {first.dtype}")
-    if sliced and idx.dtype != torch.int32:
-        raise TypeError("idx is an int32 tensor")
-    if dg is not None and dg.dtype != torch.float32:
-        raise TypeError("dg is an fp32 tensor")
-    r.dt = dtype_code(first)
-    r.gdt = F32 if dY is None else dtype_code(dY)
-    r.scratch = sliced or dg is not None
     return r
+
+
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 def _qk(fn, head, batch, seq, head_dim, q, k, rotary_, pos, eps, ctx_len, ws, stream):
@@ -480,10 +501,13 @@ def _qk(fn, head, batch, seq, head_dim, q, k, rotary_, pos, eps, ctx_len, ws, st
     if pos is not None and (pos.dtype != torch.int32 or pos.numel() != batch * seq
                             or not pos.is_contiguous()):
         raise TypeError("pos is a contiguous int32 tensor with one position a row")
-    if k is not None and (k.dt, k.gdt) != (q.dt, q.gdt):
-        raise TypeError("q and k have the same dtypes")
+    kr = None
+    if k is not None:
+        if k.dt != q.dt or k.gdt != q.gdt:
+            raise TypeError("q and k have the same dtypes")
+        kr = ctypes.byref(k)
     args = head + [ctypes.byref(tok), head_dim, eps, ctypes.byref(rotary_ or rotary()), ptr(pos),
-                   ctypes.byref(q), None if k is None else ctypes.byref(k)]
+                   ctypes.byref(q), kr]
     if q.scratch or (k is not None and k.scratch):
         _run(fn, args, ws, stream)
     else:
@@ -493,8 +517,10 @@ def _qk(fn, head, batch, seq, head_dim, q, k, rotary_, pos, eps, ctx_len, ws, st
 
 def _run_plain(fn_name, args, anything, stream):
     """A call that needs no scratch: any non-null workspace address runs it."""
-    _check(fn_name, getattr(_lib, fn_name)(*args, ctypes.addressof(anything) & ~15,
-                                           ctypes.byref(c_sz(0)), _stream(stream)))
+    st = getattr(_lib, fn_name)(*args, ctypes.addressof(anything) & ~15, ctypes.byref(c_sz(0)),
+                                _stream(stream))
+    if st:
+        _check(fn_name, st)
 
 
 def slora_qk_rotary_fwd(batch, seq, head_dim, q, k=None, rotary=None, pos=None, eps=RMS_EPS,

@@ -39,32 +39,15 @@ __device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) {
 constexpr int kThreads = 256;
 constexpr int kChunks = 4;  // chunks of 8 channels a thread has in flight
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&f)[8]) {
+__device__ __forceinline__ void load8(const float* p, int n, bool vec, float (&f)[8]) {
   if (vec && n >= 8) {
-    if constexpr (std::is_same<T, float>::value) {
-      const float4 a = reinterpret_cast<const float4*>(p)[0];
-      const float4 b = reinterpret_cast<const float4*>(p)[1];
-      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    } else {
-      const uint4 u = *reinterpret_cast<const uint4*>(p);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-    }
+    const float4 a = reinterpret_cast<const float4*>(p)[0];
+    const float4 b = reinterpret_cast<const float4*>(p)[1];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      f[i] = 0.0f;
-      if (i < n) {
-        if constexpr (std::is_same<T, float>::value) f[i] = p[i];
-        else f[i] = __bfloat162float(p[i]);
-      }
-    }
+    for (int i = 0; i < 8; ++i) f[i] = i < n ? p[i] : 0.0f;
   }
 }
 template <typename T>
@@ -90,27 +73,51 @@ __device__ __forceinline__ void store8(T* p, int n, bool vec, const float (&f)[8
   }
 }
 
+// A chunk as packed bf16 (rows that are no whole 16-byte units by elements).
+__device__ __forceinline__ uint4 load8_bf16(const __nv_bfloat16* p, int n, bool vec) {
+  if (vec && n >= 8) return *reinterpret_cast<const uint4*>(p);
+  uint4 u = make_uint4(0, 0, 0, 0);
+  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) w[i / 2] |= uint32_t(__bfloat16_as_ushort(p[i])) << (16 * (i & 1));
+  return u;
+}
+
 // Chunk i of the rows: row i / per_row, channels 8 (i % per_row) ...; a block
 // of threads takes kChunks * 256 consecutive chunks, each thread every 256th.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) act8_pack_kernel(
     const T* __restrict__ X, int64_t ldx, int64_t d, uint32_t total, const FastDiv per_row,
     bool vec, uint2* __restrict__ codes, uint8_t* __restrict__ scales) {
+  constexpr bool kF = std::is_same<T, float>::value;
   const uint32_t base = blockIdx.x * uint32_t(kThreads * kChunks) + threadIdx.x;
-  float f[kChunks][8];
+  float f[kF ? kChunks : 1][8];
+  uint4 u[kF ? 1 : kChunks];
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) {
     const uint32_t i = base + k * kThreads;
     const uint32_t row = div_by(i, per_row), c = (i - row * per_row.d) * 8;
     const int64_t left = i < total ? d - int64_t(c) : 0;
-    load8(X + (left > 0 ? int64_t(row) * ldx + c : 0), int(left < 8 ? left : 8), vec, f[k]);
+    const T* x = X + (left > 0 ? int64_t(row) * ldx + c : 0);
+    const int n = int(left < 8 ? left : 8);
+    if constexpr (kF) load8(x, n, vec, f[k]);
+    else u[k] = load8_bf16(x, n, vec);
   }
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) {
     const uint32_t i = base + k * kThreads;
-    const uint32_t byte = act8_byte(act8_block_max(act8_chunk_bits(f[k])));
+    uint32_t byte;
+    uint2 c;
+    if constexpr (kF) {
+      byte = act8_byte(act8_block_max(act8_chunk_bits(f[k])));
+      c = act8_codes8_f32(f[k], byte);
+    } else {
+      byte = act8_byte_bf16(u[k]);
+      c = act8_codes8_bf16(u[k], byte);
+    }
     if (i >= total) continue;
-    codes[i] = act8_codes8(f[k], byte);
+    codes[i] = c;
     if ((threadIdx.x & 3) == 0) scales[i >> 2] = uint8_t(byte);
   }
 }

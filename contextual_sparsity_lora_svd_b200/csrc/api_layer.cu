@@ -271,6 +271,9 @@ slora_status qk_common(const char* fn, bool backward, slora_dtype dt, slora_dtyp
         SLORA_FAIL(SLORA_ERR_UNSUPPORTED, "%s: sliced rows run in bf16 only", fn);
       if (r.n_idx < 0 || r.n_idx > n)
         SLORA_FAIL(SLORA_ERR_SHAPE, "%s: n_idx=%d outside [0, %lld]", fn, r.n_idx, (long long)n);
+      if (n > kMaxSlicedChannels)
+        SLORA_FAIL(SLORA_ERR_SHAPE, "%s: %lld channels of sliced rows, at most %d", fn,
+                   (long long)n, kMaxSlicedChannels);
       LREQ(r.idx);
       const bool ctx = D.ti.T_C > 0 && r.n_idx > 0;
       if (ctx && reads_x) LREQ(r.X_ctx);

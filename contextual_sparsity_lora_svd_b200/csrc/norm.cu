@@ -235,6 +235,8 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
+// A row's chunks stay packed between the two passes over them (4 registers a
+// chunk); the arithmetic and its order are those of the kernels above.
 template <int CPT>
 __global__ void __launch_bounds__(kRowThreads)
     rmsnorm_fwd_act8_kernel(const uint4* __restrict__ X, const uint4* __restrict__ A,
@@ -247,29 +249,36 @@ __global__ void __launch_bounds__(kRowThreads)
   const int64_t o = int64_t(blockIdx.x) * nch;
   const int nchp = (nch + 3) & ~3;  // chunks of a checkpoint's row
   const int64_t o8 = int64_t(blockIdx.x) * nchp;
-  float h[CPT][8];
+  uint4 u[CPT], a[CPT];
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) {
+    const int c = threadIdx.x + k * kRowThreads;
+    u[k] = c < nch ? X[o + c] : make_uint4(0, 0, 0, 0);
+    if (A && c < nch) a[k] = A[o + c];
+  }
   float ss = 0.f;
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
     const int c = threadIdx.x + k * kRowThreads;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[k][i] = 0.f;
     if (c < nch) {
-      unpack8(X[o + c], h[k]);
+      float h[8];
+      unpack8(u[k], h);
       if (A) {
-        float a[8];
-        unpack8(A[o + c], a);
+        float b[8];
+        unpack8(a[k], b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[k][i] = __bfloat162float(__float2bfloat16_rn(h[k][i] + a[i]));
-        if (Hout) Hout[o + c] = pack8(h[k]);
+        for (int i = 0; i < 8; ++i) h[i] += b[i];
+        u[k] = pack8(h);
+        unpack8(u[k], h);
+        if (Hout) Hout[o + c] = u[k];
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss += h[k][i] * h[k][i];
+      for (int i = 0; i < 8; ++i) ss += h[i] * h[i];
     }
     if (h8) {
-      const uint32_t byte = act8_byte(act8_block_max(act8_chunk_bits(h[k])));
+      const uint32_t byte = act8_byte_bf16(u[k]);
       if (c < nchp) {
-        h8[o8 + c] = act8_codes8(h[k], byte);
+        h8[o8 + c] = act8_codes8_bf16(u[k], byte);
         if ((c & 3) == 0) h8s[(o8 + c) >> 2] = uint8_t(byte);
       }
     }
@@ -279,20 +288,19 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
     const int c = threadIdx.x + k * kRowThreads;
-    float v[8] = {};
     if (c < nch) {
-      float gg[8];
+      float h[8], gg[8];
+      unpack8(u[k], h);
       unpack8(g[c], gg);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[k][i] *= r * gg[i];
-      const uint4 u = pack8(h[k]);
-      N[o + c] = u;
-      unpack8(u, v);  // the checkpoint holds the stored, rounded values
+      for (int i = 0; i < 8; ++i) h[i] *= r * gg[i];
+      u[k] = pack8(h);  // the checkpoint holds the stored, rounded values
+      N[o + c] = u[k];
     }
     if (n8) {
-      const uint32_t byte = act8_byte(act8_block_max(act8_chunk_bits(v)));
+      const uint32_t byte = act8_byte_bf16(u[k]);
       if (c < nchp) {
-        n8[o8 + c] = act8_codes8(v, byte);
+        n8[o8 + c] = act8_codes8_bf16(u[k], byte);
         if ((c & 3) == 0) n8s[(o8 + c) >> 2] = uint8_t(byte);
       }
     }
@@ -308,16 +316,33 @@ __global__ void __launch_bounds__(kRowThreads)
                             int nch, uint4* __restrict__ dX) {
   __shared__ float red[4];
   const int64_t o = int64_t(blockIdx.x) * nch, o8 = int64_t(blockIdx.x) * ((nch + 3) & ~3);
-  float h[CPT][8], gd[CPT][8];
+  // every input of the row is on its way before the first use
+  uint2 hc[CPT];
+  uint32_t hb[CPT];
+  uint4 d0[CPT], res[CPT];
+  const float r = rstd[blockIdx.x];
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) {
+    const int c = threadIdx.x + k * kRowThreads;
+    hc[k] = make_uint2(0, 0);
+    hb[k] = 7u;
+    d0[k] = res[k] = make_uint4(0, 0, 0, 0);
+    if (c < nch) {
+      hc[k] = h8[o8 + c];
+      hb[k] = h8s[(o8 + c) >> 2];
+      d0[k] = dN0[o + c];
+      if (dRes) res[k] = dRes[o + c];
+    }
+  }
+  float gd[CPT][8];
   float dot = 0.f;
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
     const int c = threadIdx.x + k * kRowThreads;
     if (c < nch) {
-      float t[8], gg[8];
-      act8_values8(h8[o8 + c], h8s[(o8 + c) >> 2], h[k]);
-      unpack8(g[c], gg);
-      unpack8(dN0[o + c], gd[k]);
+      float t[8], h[8];
+      act8_values8(hc[k], hb[k], h);
+      unpack8(d0[k], gd[k]);
       if (dN1) {
         unpack8(dN1[o + c], t);
 #pragma unroll
@@ -328,27 +353,28 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
         for (int i = 0; i < 8; ++i) gd[k][i] += t[i];
       }
+      unpack8(g[c], t);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        gd[k][i] *= gg[i];  // g dN
-        dot += h[k][i] * gd[k][i];
+        gd[k][i] *= t[i];  // g dN
+        dot += h[i] * gd[k][i];
       }
     }
   }
-  const float r = rstd[blockIdx.x];
   const float coef = r * r * r * block_sum128(dot, red) / float(nch * 8);
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
     const int c = threadIdx.x + k * kRowThreads;
     if (c < nch) {
-      float res[8];
-      if (dRes) unpack8(dRes[o + c], res);
+      float h[8], b[8];
+      act8_values8(hc[k], hb[k], h);
+      unpack8(res[k], b);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float v = r * gd[k][i] - h[k][i] * coef;
-        h[k][i] = dRes ? res[i] + v : v;
+        const float v = r * gd[k][i] - h[i] * coef;
+        h[i] = dRes ? b[i] + v : v;
       }
-      dX[o + c] = pack8(h[k]);
+      dX[o + c] = pack8(h);
     }
   }
 }

@@ -17,13 +17,18 @@
 // sin and cos take an argument in [-1, 1) half turns.  A product in fp32 is off
 // by 4e-3 rad at position 100000.
 //
-// Bound: memory.  Forward 2 + 2 bytes a channel, backward 2 + 4 + 2 (fp32 dy).
-// A team of lanes owns one head (V pairs a lane: two 16-byte loads at V = 8),
-// so the norm is a few shuffles and every value is read and written once.  A
-// block takes R rows of one tensor at a time, computes their R * hd / 2
-// sines and cosines once into shared memory (sincospi costs about as much as
-// four heads' rotation) and its teams walk the rows' heads, loading one head
-// ahead.
+// Bound: memory.  Forward 2 + 2 bytes a channel, backward 2 + 4 + 2 (fp32 dy);
+// the arithmetic is close behind, so it runs on packed pairs of fp32 values
+// (fma.rn.f32x2).  A team of lanes owns one head (V pairs a lane: two 16-byte
+// loads at V = 8), so the norm is a few shuffles and every value is read and
+// written once.  A warp owns one row at a time, or a share of its heads where
+// rows are few: it computes the row's hd / 2 sines and cosines once, spread
+// over its lanes, keeps each lane's in registers and walks the heads, loading
+// one head ahead.  Nothing in the loop waits for another warp.
+//
+// Sliced rows: the inverse channel list lies in shared memory, and a context
+// row's compact channels are staged there with wide loads, gathered from (and
+// in the backward scattered back to) by channel, and stored with wide stores.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -36,8 +41,7 @@ __device__ int g_qk_bad_index = 0;
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxRows = 8;  // rows of a chunk
+constexpr int kWarps = 8;  // of a block, fewer where sliced rows need the shared memory
 
 struct QkPart {
   const void* X;
@@ -53,16 +57,38 @@ struct QkPart {
   long long ldy;
   float* dgp;  // [blocks of this part][hd] partial sums of dg, or null
   int heads, blocks;
+  int chunks, per_chunk;  // a row's heads in `chunks` shares of per_chunk
 };
 struct QkParams {
   QkPart part[2];
   unsigned long long turns[kMaxHeadDim / 2];
   const int32_t* pos;
   const int32_t* ctx_off;  // sliced: context rows before sequence b, [batch + 1]
-  long long T;
-  int seq, hd, dims, R, units, tl;
+  int T, seq, hd, dims, units, tl;
+  int stage;  // sliced: elements of a warp's staged row (a multiple of 8)
   float eps, mscale;
 };
+
+// Two fp32 values as one operand of the packed instructions.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+  f2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack2(f2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
 
 template <typename T, int V>
 struct alignas(V * sizeof(T) >= 16 ? 16 : V * sizeof(T)) Raw {
@@ -146,34 +172,88 @@ template <int V>
 constexpr int units_per_lane() {
   return V == 8 ? 1 : (V == 2 ? 2 : 4);
 }
+// Packed pairs of a unit (V = 1: the second value of the one is zero).
+template <int V>
+constexpr int packs() {
+  return V == 1 ? 1 : V / 2;
+}
+template <int V>
+__device__ __forceinline__ void pack_all(const float (&v)[V], f2 (&p)[packs<V>()]) {
+  if constexpr (V == 1) {
+    p[0] = pack2(v[0], 0.0f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) p[i] = pack2(v[2 * i], v[2 * i + 1]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void unpack_all(const f2 (&p)[packs<V>()], float (&v)[V]) {
+  if constexpr (V == 1) {
+    float z;
+    unpack2(p[0], v[0], z);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) unpack2(p[i], v[2 * i], v[2 * i + 1]);
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void zero(Raw<T, V>& r) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) r.v[i] = from_f<T>(0.0f);
+}
+// Raw groups of a unit to its packed first and second members.
+template <typename T, int V, bool kInter>
+__device__ __forceinline__ void members(const Raw<T, V>& ra, const Raw<T, V>& rb,
+                                        f2 (&lo)[packs<V>()], f2 (&hi)[packs<V>()]) {
+  float a[V], b[V], l[V], h[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    a[i] = to_f(ra.v[i]);
+    b[i] = to_f(rb.v[i]);
+  }
+  Pairs<V, kInter>::split(a, b, l, h);
+  pack_all<V>(l, lo);
+  pack_all<V>(h, hi);
+}
 
-// One head's raw rows in flight.
+// One head's rows in flight (zeros where this lane has none).
 template <typename T, typename G, int V, bool kBwd>
 struct Item {
-  Raw<T, V> xa[units_per_lane<V>()], xb[units_per_lane<V>()];
-  Raw<G, V> ya[kBwd ? units_per_lane<V>() : 1], yb[kBwd ? units_per_lane<V>() : 1];
+  static constexpr int NU = units_per_lane<V>();
+  Raw<T, V> xa[NU], xb[NU];
+  Raw<G, V> ya[kBwd ? NU : 1], yb[kBwd ? NU : 1];
 };
 
 template <typename T, typename G, int V, bool kInter, bool kBwd, bool kSliced>
-__global__ void __launch_bounds__(kThreads) qk_rotary_kernel(const __grid_constant__ QkParams P) {
-  constexpr int NU = units_per_lane<V>();
-  extern __shared__ __align__(16) float2 tab[];  // [R][V / 2][units][2] (V = 1: [R][units])
+__global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
+    qk_rotary_kernel(const __grid_constant__ QkParams P) {
+  constexpr int NU = units_per_lane<V>(), NP = packs<V>();
+  // [warps][hd / 2] cosines and sines (the backward's dg at the end), then for
+  // sliced rows the inverse channel list and the warps' staged rows
+  extern __shared__ __align__(16) float2 smem[];
   __shared__ unsigned long long s_turns[kMaxHeadDim / 2];
-  __shared__ int s_kind[kMaxRows];  // sliced: context row, or -1 - output row
-  __shared__ float s_red[kBwd ? kThreads / 32 : 1][kBwd ? kMaxHeadDim : 1];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nwarps = blockDim.x >> 5;
   const bool second = int(blockIdx.x) >= P.part[0].blocks;
   const QkPart& q = P.part[second ? 1 : 0];
   const int blk = int(blockIdx.x) - (second ? P.part[0].blocks : 0);
   const int hd = P.hd, dims = P.dims, np = hd / 2, U = P.units, tl = P.tl;
-  for (int p = tid; p < dims / 2; p += kThreads) s_turns[p] = P.turns[p];
+  const int heads = q.heads;
+  float2* tab = smem + warp * np;
+  uint16_t* s_inv = nullptr;
+  T* stage = nullptr;
+  if constexpr (kSliced) {
+    s_inv = reinterpret_cast<uint16_t*>(smem + (nwarps * np + 1) / 2 * 2);  // 16-byte aligned
+    stage = reinterpret_cast<T*>(s_inv + (heads * hd + 7) / 8 * 8) + warp * P.stage;
+    for (int i = tid; i < heads * hd; i += blockDim.x) s_inv[i] = uint16_t(q.inv[i]);  // -1: 65535
+  }
+  for (int p = tid; p < dims / 2; p += blockDim.x) s_turns[p] = P.turns[p];
+  __syncthreads();
 
-  // this lane's place: team `team` of the block, units lt, lt + tl, ...
-  const int lt = tid % tl, nteams = kThreads / tl;
-  const int team = tid / tl, team0 = (tid & ~31) / tl;  // first team of this warp
+  // this lane's place: team `team` of the warp, units lt, lt + tl, ...
+  const int lt = lane % tl, team = lane / tl, tpw = 32 / tl;
   int offa[NU], offb[NU];
   bool act[NU];
-  float glo[NU][V], ghi[NU][V];
+  f2 glo[NU][NP], ghi[NU][NP];
   const bool norm = q.g != nullptr;
 #pragma unroll
   for (int j = 0; j < NU; ++j) {
@@ -186,10 +266,10 @@ __global__ void __launch_bounds__(kThreads) qk_rotary_kernel(const __grid_consta
       offa[j] = p0;
       offb[j] = p0 + dims / 2;
     } else {
-      offa[j] = p0 + dims / 2;          // dims + (p0 - dims / 2)
+      offa[j] = p0 + dims / 2;            // dims + (p0 - dims / 2)
       offb[j] = offa[j] + np - dims / 2;  // + half of the unrotated channels
     }
-    float a[V], b[V];
+    float a[V], b[V], l[V], h[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) a[i] = b[i] = 1.0f;
     if (norm && act[j]) {
@@ -200,257 +280,302 @@ __global__ void __launch_bounds__(kThreads) qk_rotary_kernel(const __grid_consta
         b[i] = to_f(g[offb[j] + i]);
       }
     }
-    Pairs<V, kInter>::split(a, b, glo[j], ghi[j]);
+    Pairs<V, kInter>::split(a, b, l, h);
+    pack_all<V>(l, glo[j]);
+    pack_all<V>(h, ghi[j]);
   }
-  float dglo[kBwd ? NU : 1][V], dghi[kBwd ? NU : 1][V];
+  f2 dglo[kBwd ? NU : 1][NP], dghi[kBwd ? NU : 1][NP];
   if constexpr (kBwd) {
 #pragma unroll
     for (int j = 0; j < NU; ++j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) dglo[j][i] = dghi[j][i] = 0.0f;
+      for (int i = 0; i < NP; ++i) dglo[j][i] = dghi[j][i] = 0ull;
   }
+  f2 cs[NU][NP], sn[NU][NP];
+  const f2 minus1 = pack2(-1.0f, -1.0f);
 
-  const long long nchunks = (P.T + P.R - 1) / P.R;
-  const int dr = nteams / q.heads, dh = nteams % q.heads;
-  for (long long ch = blk; ch < nchunks; ch += q.blocks) {
-    const long long t0 = ch * P.R;
-    const int nrow = int(min((long long)P.R, P.T - t0));
-    const int place = P.pos ? 0 : int(t0 % P.seq);  // of the chunk's first row in its sequence
-    __syncthreads();  // the previous chunk's table has been read (and s_turns is written)
-    for (int e = tid; e < nrow * np; e += kThreads) {
-      const int r = e / np, p = e - r * np;
-      float s = 0.0f, c = 1.0f;
-      if (p < dims / 2) {
-        const long long pos = P.pos ? P.pos[t0 + r] : int(unsigned(place + r) % unsigned(P.seq));
-        const unsigned long long turn = (unsigned long long)pos * s_turns[p];
-        // the top 32 bits as a signed fraction: half turns in [-1, 1)
-        sincospif(float(int(turn >> 32)) * 4.656612873077393e-10f, &s, &c);
-        s *= P.mscale;
-        c *= P.mscale;
-      }
-      const int at = V == 1 ? r * U + p
-                            : ((r * (V / 2) + (p % V) / 2) * U + p / V) * 2 + (p & 1);
-      tab[at] = make_float2(c, s);
-    }
-    if constexpr (kSliced) {
-      if (tid < nrow) {
-        const long long t = t0 + tid;
-        const int b = int(t / P.seq), i = int(t % P.seq);
-        const int o0 = P.ctx_off[b], o1 = P.ctx_off[b + 1];
-        s_kind[tid] = i < o1 - o0 ? o0 + i : int(-1 - (t - o1));
-      }
-    }
-    __syncthreads();
-
-    const int items = nrow * q.heads;
-    auto load = [&](int r, int h, bool valid, Item<T, G, V, kBwd>& it) {
-      if (!valid) return;
-      const long long t = t0 + r;
-      const T* x = nullptr;
-      int kind = -1;
-      if constexpr (kSliced) {
-        kind = s_kind[r];
-        if (kind < 0)
-          x = static_cast<const T*>(q.Xo) + (long long)(-1 - kind) * q.heads * hd + h * hd;
-        else
-          x = static_cast<const T*>(q.Xc) + (long long)kind * q.n_idx;
-      } else {
-        x = static_cast<const T*>(q.X) + t * q.ldx + h * hd;
-      }
+  // compact context row of row t, or -1 - its output row
+  auto kind_of = [&](int t) {
+    const int b = t / P.seq, i = t - b * P.seq;
+    const int o0 = P.ctx_off[b], o1 = P.ctx_off[b + 1];
+    return i < o1 - o0 ? o0 + i : -1 - (t - o1);
+  };
+  // the rows of one head that global memory holds at full width
+  auto load = [&](int t, int h, bool valid, int kind, Item<T, G, V, kBwd>& it) {
 #pragma unroll
-      for (int j = 0; j < NU; ++j) {
-        if (!act[j]) continue;
-        if (!kBwd || norm) {
-          if (kSliced && kind >= 0) {
-            const int32_t* inv = q.inv + h * hd;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-              const int ia = inv[offa[j] + i], ib = inv[offb[j] + i];
-              it.xa[j].v[i] = ia >= 0 ? x[ia] : from_f<T>(0.0f);
-              it.xb[j].v[i] = ib >= 0 ? x[ib] : from_f<T>(0.0f);
-            }
-          } else {
-            ld_vec(x + offa[j], it.xa[j]);
-            ld_vec(x + offb[j], it.xb[j]);
-          }
-        }
-        if constexpr (kBwd) {
+    for (int j = 0; j < NU; ++j) {
+      const bool on = valid && act[j];
+      zero(it.xa[j]);
+      zero(it.xb[j]);
+      if (on && (!kBwd || norm) && (!kSliced || kind < 0)) {
+        const T* x = kSliced ? static_cast<const T*>(q.Xo) +
+                                   ((long long)(-1 - kind) * heads + h) * hd
+                             : static_cast<const T*>(q.X) + t * q.ldx + h * hd;
+        ld_vec(x + offa[j], it.xa[j]);
+        ld_vec(x + offb[j], it.xb[j]);
+      }
+      if constexpr (kBwd) {
+        zero(it.ya[j]);
+        zero(it.yb[j]);
+        if (on) {
           const G* y = static_cast<const G*>(q.dY) + t * q.ldy + h * hd;
           ld_vec(y + offa[j], it.ya[j]);
           ld_vec(y + offb[j], it.yb[j]);
         }
       }
-    };
-    auto table = [&](int r, int j, float2 (&cs)[V]) {
-      const int u = lt + j * tl;
-      if constexpr (V == 1) {
-        cs[0] = tab[r * U + u];
-      } else {
-#pragma unroll
-        for (int k = 0; k < V / 2; ++k) {
-          const float4 f = reinterpret_cast<const float4*>(tab)[(r * (V / 2) + k) * U + u];
-          cs[2 * k] = make_float2(f.x, f.y);
-          cs[2 * k + 1] = make_float2(f.z, f.w);
-        }
+    }
+  };
+  // cosines and sines of a row, from the warp's lanes to each lane's pairs
+  auto angles = [&](int pos) {
+    __syncwarp();
+    for (int p = lane; p < np; p += 32) {
+      float s = 0.0f, c = 1.0f;
+      if (p < dims / 2) {
+        const unsigned long long turn = (unsigned long long)(long long)pos * s_turns[p];
+        // the top 32 bits as a signed fraction: half turns in [-1, 1)
+        sincospif(float(int(turn >> 32)) * 4.656612873077393e-10f, &s, &c);
+        s *= P.mscale;
+        c *= P.mscale;
       }
-    };
-    auto team_sum = [&](float v) {
-      for (int s = tl >> 1; s; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-      return v;
-    };
-    auto store = [&](int r, int h, int j, const float (&lo)[V], const float (&hi)[V]) {
-      float a[V], b[V];
-      Pairs<V, kInter>::join(lo, hi, a, b);
-      Raw<T, V> ra, rb;
+      tab[p] = make_float2(c, s);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      const int p0 = (lt + j * tl) * V;
+      float c[V], s[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        ra.v[i] = from_f<T>(a[i]);
-        rb.v[i] = from_f<T>(b[i]);
+        const float2 w = act[j] ? tab[p0 + i] : make_float2(1.0f, 0.0f);
+        c[i] = w.x;
+        s[i] = w.y;
       }
-      T* o;
-      if constexpr (kSliced && kBwd) {
-        const int kind = s_kind[r];
-        if (kind >= 0) {
-          T* oc = static_cast<T*>(q.outc) + (long long)kind * q.n_idx;
-          const int32_t* inv = q.inv + h * hd;
+      pack_all<V>(c, cs[j]);
+      pack_all<V>(s, sn[j]);
+    }
+  };
+  auto team_sum = [&](float v) {
+    for (int s = tl >> 1; s; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+    return v;
+  };
+  auto store = [&](int t, int h, int kind, int j, const f2 (&lo)[NP], const f2 (&hi)[NP]) {
+    float l[V], m[V], a[V], b[V];
+    unpack_all<V>(lo, l);
+    unpack_all<V>(hi, m);
+    Pairs<V, kInter>::join(l, m, a, b);
+    Raw<T, V> ra, rb;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      ra.v[i] = from_f<T>(a[i]);
+      rb.v[i] = from_f<T>(b[i]);
+    }
+    if constexpr (kSliced && kBwd) {
+      if (kind >= 0) {  // into the staged row, over this lane's own x
+        const uint16_t* inv = s_inv + h * hd;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int ia = inv[offa[j] + i], ib = inv[offb[j] + i];
+          if (ia != 65535) stage[ia] = ra.v[i];
+          if (ib != 65535) stage[ib] = rb.v[i];
+        }
+        return;
+      }
+    }
+    T* o = kSliced && kBwd
+               ? static_cast<T*>(q.outo) + ((long long)(-1 - kind) * heads + h) * hd
+               : static_cast<T*>(q.out) + t * q.ldo + h * hd;
+    st_vec(o + offa[j], ra);
+    st_vec(o + offb[j], rb);
+  };
+  auto compute = [&](int t, int h, bool valid, int kind, Item<T, G, V, kBwd>& it) {
+    f2 xlo[NU][NP], xhi[NU][NP];
+    f2 ss = 0ull;
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      if constexpr (kSliced) {
+        if (kind >= 0 && valid && act[j] && (!kBwd || norm)) {
+          const uint16_t* inv = s_inv + h * hd;
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             const int ia = inv[offa[j] + i], ib = inv[offb[j] + i];
-            if (ia >= 0) oc[ia] = ra.v[i];
-            if (ib >= 0) oc[ib] = rb.v[i];
+            if (ia != 65535) it.xa[j].v[i] = stage[ia];
+            if (ib != 65535) it.xb[j].v[i] = stage[ib];
           }
-          return;
         }
-        o = static_cast<T*>(q.outo) + (long long)(-1 - kind) * q.heads * hd + h * hd;
-      } else {
-        o = static_cast<T*>(q.out) + (t0 + r) * q.ldo + h * hd;
       }
-      st_vec(o + offa[j], ra);
-      st_vec(o + offb[j], rb);
-    };
-    auto compute = [&](int r, int h, bool valid, const Item<T, G, V, kBwd>& it) {
-      float xlo[NU][V], xhi[NU][V];
-      float ss = 0.0f;
+      members<T, V, kInter>(it.xa[j], it.xb[j], xlo[j], xhi[j]);
+      if (norm) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          ss = fma2(xlo[j][i], xlo[j][i], ss);
+          ss = fma2(xhi[j][i], xhi[j][i], ss);
+        }
+      }
+    }
+    float rs = 1.0f;
+    if (norm) {
+      float a, b;
+      unpack2(ss, a, b);
+      rs = rsqrtf(team_sum(a + b) / float(hd) + P.eps);
+    }
+    const f2 rs2 = pack2(rs, rs);
+    if constexpr (!kBwd) {
 #pragma unroll
       for (int j = 0; j < NU; ++j) {
-        float a[V], b[V];
+        f2 lo[NP], hi[NP];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const bool on = valid && act[j] && (!kBwd || norm);
-          a[i] = on ? to_f(it.xa[j].v[i]) : 0.0f;
-          b[i] = on ? to_f(it.xb[j].v[i]) : 0.0f;
-          ss += a[i] * a[i] + b[i] * b[i];
+        for (int i = 0; i < NP; ++i) {
+          f2 l = xlo[j][i], m = xhi[j][i];
+          if (norm) {
+            l = mul2(mul2(l, rs2), glo[j][i]);
+            m = mul2(mul2(m, rs2), ghi[j][i]);
+          }
+          lo[i] = fma2(mul2(m, sn[j][i]), minus1, mul2(l, cs[j][i]));
+          hi[i] = fma2(m, cs[j][i], mul2(l, sn[j][i]));
         }
-        Pairs<V, kInter>::split(a, b, xlo[j], xhi[j]);
+        if (valid && act[j]) store(t, h, kind, j, lo, hi);
       }
-      float rs = 1.0f;
-      if (norm) rs = rsqrtf(team_sum(ss) / float(hd) + P.eps);
-      if constexpr (!kBwd) {
-        if (!valid) return;
+    } else {
+      f2 dlo[NU][NP], dhi[NU][NP];  // dn = R^T dy, then g dn
+      f2 dot = 0ull;                // sum of x g dn
 #pragma unroll
-        for (int j = 0; j < NU; ++j) {
-          if (!act[j]) continue;
-          float2 cs[V];
-          table(r, j, cs);
-          float lo[V], hi[V];
+      for (int j = 0; j < NU; ++j) {
+        f2 ylo[NP], yhi[NP];
+        members<G, V, kInter>(it.ya[j], it.yb[j], ylo, yhi);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float l = norm ? xlo[j][i] * rs * glo[j][i] : xlo[j][i];
-            const float m = norm ? xhi[j][i] * rs * ghi[j][i] : xhi[j][i];
-            lo[i] = l * cs[i].x - m * cs[i].y;
-            hi[i] = m * cs[i].x + l * cs[i].y;
+        for (int i = 0; i < NP; ++i) {
+          f2 l = fma2(yhi[i], sn[j][i], mul2(ylo[i], cs[j][i]));
+          f2 m = fma2(mul2(ylo[i], sn[j][i]), minus1, mul2(yhi[i], cs[j][i]));
+          if (norm) {
+            dglo[j][i] = fma2(l, mul2(xlo[j][i], rs2), dglo[j][i]);
+            dghi[j][i] = fma2(m, mul2(xhi[j][i], rs2), dghi[j][i]);
+            l = mul2(l, glo[j][i]);
+            m = mul2(m, ghi[j][i]);
+            dot = fma2(xlo[j][i], l, dot);
+            dot = fma2(xhi[j][i], m, dot);
           }
-          store(r, h, j, lo, hi);
+          dlo[j][i] = l;
+          dhi[j][i] = m;
         }
-      } else {
-        float dlo[NU][V], dhi[NU][V];  // dn = R^T dy
-        float dot = 0.0f;              // sum of x g dn
-#pragma unroll
-        for (int j = 0; j < NU; ++j) {
-          const bool on = valid && act[j];
-          float a[V], b[V], lo[V], hi[V];
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            a[i] = on ? to_f(it.ya[j].v[i]) : 0.0f;
-            b[i] = on ? to_f(it.yb[j].v[i]) : 0.0f;
-          }
-          Pairs<V, kInter>::split(a, b, lo, hi);
-          float2 cs[V];
-          if (on) table(r, j, cs);
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float c = on ? cs[i].x : 1.0f, s = on ? cs[i].y : 0.0f;
-            dlo[j][i] = lo[i] * c + hi[i] * s;
-            dhi[j][i] = hi[i] * c - lo[i] * s;
-            dot += xlo[j][i] * glo[j][i] * dlo[j][i] + xhi[j][i] * ghi[j][i] * dhi[j][i];
-          }
-        }
-        if (norm) {
-          const float coef = rs * rs * rs * (team_sum(dot) / float(hd));
-#pragma unroll
-          for (int j = 0; j < NU; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-              dglo[j][i] += dlo[j][i] * (xlo[j][i] * rs);
-              dghi[j][i] += dhi[j][i] * (xhi[j][i] * rs);
-              dlo[j][i] = rs * (glo[j][i] * dlo[j][i]) - xlo[j][i] * coef;
-              dhi[j][i] = rs * (ghi[j][i] * dhi[j][i]) - xhi[j][i] * coef;
-            }
-        }
-        if (!valid) return;
+      }
+      if (norm) {
+        float a, b;
+        unpack2(dot, a, b);
+        const float coef = -(rs * rs * rs) * (team_sum(a + b) / float(hd));
+        const f2 coef2 = pack2(coef, coef);
 #pragma unroll
         for (int j = 0; j < NU; ++j)
-          if (act[j]) store(r, h, j, dlo[j], dhi[j]);
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            dlo[j][i] = fma2(dlo[j][i], rs2, mul2(xlo[j][i], coef2));
+            dhi[j][i] = fma2(dhi[j][i], rs2, mul2(xhi[j][i], coef2));
+          }
       }
-    };
-
-    // the next head's rows load while this one is computed; every lane of a
-    // warp runs the same number of rounds (the team sums are warp-wide)
-    int r = team / q.heads, h = team % q.heads;
-    Item<T, G, V, kBwd> cur, nxt;
-    load(r, h, team < items, cur);
-    for (int base = team0; base < items; base += nteams) {
-      const int it = base + (team - team0);
-      int r2 = r + dr, h2 = h + dh;
-      if (h2 >= q.heads) {
-        h2 -= q.heads;
-        ++r2;
-      }
-      load(r2, h2, it + nteams < items, nxt);
-      compute(r, h, it < items, cur);
-      cur = nxt;
-      r = r2;
-      h = h2;
+#pragma unroll
+      for (int j = 0; j < NU; ++j)
+        if (valid && act[j]) store(t, h, kind, j, dlo[j], dhi[j]);
     }
+  };
+  // a context row's compact channels to the stage, and back from it
+  auto stage_in = [&](int kind) {
+    const T* x = static_cast<const T*>(q.Xc) + (long long)kind * q.n_idx;
+    __syncwarp();
+    if (q.n_idx % 8 == 0) {
+      for (int i = lane * 8; i < q.n_idx; i += 256)
+        *reinterpret_cast<uint4*>(stage + i) = *reinterpret_cast<const uint4*>(x + i);
+    } else {
+      for (int i = lane; i < q.n_idx; i += 32) stage[i] = x[i];
+    }
+    __syncwarp();
+  };
+  auto stage_out = [&](int kind) {
+    T* x = static_cast<T*>(q.outc) + (long long)kind * q.n_idx;
+    __syncwarp();
+    if (q.n_idx % 8 == 0) {
+      for (int i = lane * 8; i < q.n_idx; i += 256)
+        *reinterpret_cast<uint4*>(x + i) = *reinterpret_cast<const uint4*>(stage + i);
+    } else {
+      for (int i = lane; i < q.n_idx; i += 32) x[i] = stage[i];
+    }
+    __syncwarp();
+  };
+  auto position = [&](int t) { return P.pos ? P.pos[t] : t % P.seq; };
+
+  // unit u: share u % chunks of row u / chunks
+  const int units = P.T * q.chunks, stride = q.blocks * nwarps;
+  int u = blk * nwarps + warp;
+  Item<T, G, V, kBwd> cur, nxt;
+  int t = 0, h0 = 0, h1 = 0, pos = 0, kind = -1;
+  if (u < units) {
+    t = u / q.chunks;
+    h0 = (u - t * q.chunks) * q.per_chunk;
+    h1 = min(heads, h0 + q.per_chunk);
+    pos = position(t);
+    if constexpr (kSliced) kind = kind_of(t);
+    load(t, h0 + team, h0 + team < h1, kind, cur);
+  }
+  while (u < units) {  // the same rounds for every lane of a warp
+    const int u2 = u + stride;
+    int t2 = 0, h02 = 0, h12 = 0, pos2 = 0, kind2 = -1;
+    if (u2 < units) {
+      t2 = u2 / q.chunks;
+      h02 = (u2 - t2 * q.chunks) * q.per_chunk;
+      h12 = min(heads, h02 + q.per_chunk);
+      pos2 = position(t2);
+      if constexpr (kSliced) kind2 = kind_of(t2);
+    }
+    if constexpr (kSliced) {
+      if (kind >= 0 && (!kBwd || norm)) stage_in(kind);
+    }
+    angles(pos);
+    for (int hb = h0; hb < h1; hb += tpw) {
+      const int h = hb + team;
+      const bool more = hb + tpw < h1;
+      const int hn = more ? h + tpw : h02 + team;
+      load(more ? t : t2, hn, hn < (more ? h1 : h12), more ? kind : kind2, nxt);
+      compute(t, h, h < h1, kind, cur);
+      cur = nxt;
+    }
+    if constexpr (kSliced && kBwd) {
+      if (kind >= 0) stage_out(kind);
+    }
+    u = u2;
+    t = t2;
+    h0 = h02;
+    h1 = h12;
+    pos = pos2;
+    kind = kind2;
   }
 
   if constexpr (kBwd) {
     if (!q.dgp) return;
-    // this block's dg: lanes of a warp that own the same channels, then the
-    // warps in order
+    // this block's dg: the warp's teams by shuffles, then the warps in order
+    float* red = reinterpret_cast<float*>(smem) + warp * hd;  // over this warp's table
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
+      float l[V], m[V], a[V], b[V];
+      unpack_all<V>(dglo[j], l);
+      unpack_all<V>(dghi[j], m);
 #pragma unroll
       for (int i = 0; i < V; ++i)
         for (int s = tl; s < 32; s <<= 1) {
-          dglo[j][i] += __shfl_xor_sync(0xffffffffu, dglo[j][i], s);
-          dghi[j][i] += __shfl_xor_sync(0xffffffffu, dghi[j][i], s);
+          l[i] += __shfl_xor_sync(0xffffffffu, l[i], s);
+          m[i] += __shfl_xor_sync(0xffffffffu, m[i], s);
         }
-      float a[V], b[V];
-      Pairs<V, kInter>::join(dglo[j], dghi[j], a, b);
-      if (act[j] && (tid & 31) < tl) {
+      Pairs<V, kInter>::join(l, m, a, b);
+      if (act[j] && lane < tl) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          s_red[tid >> 5][offa[j] + i] = a[i];
-          s_red[tid >> 5][offb[j] + i] = b[i];
+          red[offa[j] + i] = a[i];
+          red[offb[j] + i] = b[i];
         }
       }
     }
     __syncthreads();
-    for (int c = tid; c < hd; c += kThreads) {
+    for (int c = tid; c < hd; c += blockDim.x) {
       float v = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) v += s_red[w][c];
+      for (int w = 0; w < nwarps; ++w) v += reinterpret_cast<const float*>(smem)[w * hd + c];
       q.dgp[(long long)blk * hd + c] = v;
     }
   }
@@ -546,31 +671,37 @@ void launch_slices(const QkDesc& D, const slora_tokens* tok, int32_t* const* inv
   qk_slice_kernel<CAP><<<3, 1024, 0, st>>>(p);
 }
 
+struct Geometry {
+  int warps, smem, grid;
+};
+
 template <typename T, typename G, int V, bool kInter, bool kBwd, bool kSliced>
-slora_status launch(const QkParams& P, int grid, cudaStream_t st) {
-  const int smem = P.R * (P.hd / 2) * int(sizeof(float2));  // at most 8 KB
-  qk_rotary_kernel<T, G, V, kInter, kBwd, kSliced><<<grid, kThreads, smem, st>>>(P);
+slora_status launch(const QkParams& P, const Geometry& g, cudaStream_t st) {
+  auto kernel = qk_rotary_kernel<T, G, V, kInter, kBwd, kSliced>;
+  if (g.smem > 48 * 1024)
+    SLORA_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, g.smem));
+  kernel<<<g.grid, g.warps * 32, g.smem, st>>>(P);
   SLORA_CHECK_LAUNCH();
   return SLORA_OK;
 }
 template <typename T, typename G, int V, bool kInter, bool kBwd>
-slora_status launch_s(bool sliced, const QkParams& P, int grid, cudaStream_t st) {
+slora_status launch_s(bool sliced, const QkParams& P, const Geometry& g, cudaStream_t st) {
   if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-    if (sliced) return launch<T, G, V, kInter, kBwd, true>(P, grid, st);
+    if (sliced) return launch<T, G, V, kInter, kBwd, true>(P, g, st);
   }
-  return launch<T, G, V, kInter, kBwd, false>(P, grid, st);
+  return launch<T, G, V, kInter, kBwd, false>(P, g, st);
 }
 template <typename T, typename G, bool kBwd>
-slora_status launch_v(int V, bool inter, bool sliced, const QkParams& P, int grid,
-                      cudaStream_t st) {
+slora_status launch_v(int V, bool inter, bool sliced, const QkParams& P,
+                      const Geometry& g, cudaStream_t st) {
   if (V == 8)
-    return inter ? launch_s<T, G, 8, true, kBwd>(sliced, P, grid, st)
-                 : launch_s<T, G, 8, false, kBwd>(sliced, P, grid, st);
+    return inter ? launch_s<T, G, 8, true, kBwd>(sliced, P, g, st)
+                 : launch_s<T, G, 8, false, kBwd>(sliced, P, g, st);
   if (V == 2)
-    return inter ? launch_s<T, G, 2, true, kBwd>(sliced, P, grid, st)
-                 : launch_s<T, G, 2, false, kBwd>(sliced, P, grid, st);
-  return inter ? launch_s<T, G, 1, true, kBwd>(sliced, P, grid, st)
-               : launch_s<T, G, 1, false, kBwd>(sliced, P, grid, st);
+    return inter ? launch_s<T, G, 2, true, kBwd>(sliced, P, g, st)
+                 : launch_s<T, G, 2, false, kBwd>(sliced, P, g, st);
+  return inter ? launch_s<T, G, 1, true, kBwd>(sliced, P, g, st)
+               : launch_s<T, G, 1, false, kBwd>(sliced, P, g, st);
 }
 
 // The widest vector (in channels of one group) that every row of the call
@@ -591,9 +722,25 @@ int vector_width(const QkDesc& D, bool backward) {
   return 1;
 }
 
-constexpr int kBlocksPerSm = 4;
-
-int grid_blocks() { return num_sms() * kBlocksPerSm; }
+// Blocks an SM holds at once (registers: launch bounds of the kernel).
+int blocks_per_sm(bool backward) { return backward ? 2 : 3; }
+// Warps of a block and its shared memory: tables, and for sliced rows the
+// inverse channel list and a staged row a warp, within half an SM's memory as
+// long as that leaves a warp.
+void block_shape(const QkDesc& D, bool sliced, Geometry* g, int* stage) {
+  int n = 0, ni = 0;
+  for (int i = 0; i < D.nparts; ++i) {
+    n = std::max(n, D.part[i].heads * D.head_dim);
+    ni = std::max(ni, D.part[i].idx ? D.part[i].n_idx : 0);
+  }
+  *stage = (ni + 7) / 8 * 8;
+  g->warps = kWarps;
+  for (;; g->warps /= 2) {
+    g->smem = (g->warps * D.head_dim * 4 + 15) / 16 * 16;
+    if (sliced) g->smem += (n + 7) / 8 * 16 + g->warps * *stage * 2;
+    if (!sliced || g->warps == 1 || g->smem <= 100 * 1024) return;
+  }
+}
 
 }  // namespace
 
@@ -648,8 +795,11 @@ slora_status rotary_plan(const char* fn, const slora_rotary* rot, int head_dim, 
     yhi = std::min(std::ceil(pair_of(low)), double(dims - 1));
   }
   auto clamp01 = [](double v) { return std::min(1.0, std::max(0.0, v)); };
-  for (int p = 0; p < dims / 2; ++p) {
-    const double f = std::pow(base, -2.0 * p / dims);
+  // f_p = base^(-2p / dims) by products in long double (2^-64 each)
+  const long double ratio = std::pow((long double)base, -2.0L / dims);
+  long double power = 1.0L;
+  for (int p = 0; p < dims / 2; ++p, power *= ratio) {
+    const double f = double(power);
     double g = f;
     if (rot->scaling == SLORA_ROTARY_LINEAR) g = f / s;
     if (bands) {
@@ -677,7 +827,7 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
     sliced = sliced || D.part[i].idx;
     any_dg = any_dg || (backward && D.part[i].g && D.part[i].dg);
   }
-  const int max_blocks = grid_blocks();
+  const int max_blocks = num_sms() * blocks_per_sm(backward);
   int32_t* inv[2] = {nullptr, nullptr};
   int32_t* ctx_off = nullptr;
   float* dgp = nullptr;
@@ -702,7 +852,7 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
   QkParams P{};
   P.pos = D.pos;
   P.ctx_off = ctx_off;
-  P.T = D.ti.T;
+  P.T = int(D.ti.T);
   P.seq = D.ti.seq;
   P.hd = hd;
   P.dims = D.rot.dims;
@@ -713,13 +863,11 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
   const int nu = V == 8 ? 1 : (V == 2 ? 2 : 4);
   P.tl = 1;
   while (P.tl < 32 && P.tl * nu < P.units) P.tl *= 2;
-  // rows of a chunk: eight share a table, fewer where the rows would not give
-  // every block one
-  P.R = int(std::min<int64_t>(kMaxRows, std::max<int64_t>(1, D.ti.T / max_blocks)));
-  const int64_t nchunks = (D.ti.T + P.R - 1) / P.R;
+  Geometry g;
+  block_shape(D, sliced, &g, &P.stage);
   int heads = 0;
   for (int i = 0; i < D.nparts; ++i) heads += D.part[i].heads;
-  int grid = 0;
+  g.grid = 0;
   double bytes = 0.0;
   const double es = D.dt == kF32 ? 4 : 2, gs = D.gdt == kF32 ? 4 : 2;
   for (int i = 0; i < D.nparts; ++i) {
@@ -733,12 +881,19 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
     } else {
       q.out = s.Y; q.ldo = s.ldy;
     }
-    // blocks in proportion to the heads
-    const int64_t share = i == 0 ? std::max<int64_t>(1, int64_t(max_blocks) * s.heads / heads)
-                                 : std::max<int64_t>(1, max_blocks - P.part[0].blocks);
-    q.blocks = int(std::min<int64_t>(share, nchunks));
-    if (any_dg && s.g && s.dg) q.dgp = dgp + int64_t(grid) * hd;
-    grid += q.blocks;
+    // blocks in proportion to the heads; a row's heads in as many shares as
+    // give every warp about eight units, down to one round of a warp's teams
+    // (sliced rows stay whole: their stage is a row)
+    const int share = i == 0 ? std::max(1, int(int64_t(max_blocks) * s.heads / heads))
+                             : std::max(1, max_blocks - P.part[0].blocks);
+    const int rounds = (s.heads + 32 / P.tl - 1) / (32 / P.tl);
+    const int64_t want = int64_t(share) * g.warps * 8;
+    q.chunks = s.idx ? 1 : int(std::min<int64_t>(rounds, (want + D.ti.T - 1) / D.ti.T));
+    q.per_chunk = (rounds + q.chunks - 1) / q.chunks * (32 / P.tl);
+    q.chunks = (s.heads + q.per_chunk - 1) / q.per_chunk;
+    q.blocks = int(std::min<int64_t>(share, (D.ti.T * q.chunks + g.warps - 1) / g.warps));
+    if (any_dg && s.g && s.dg) q.dgp = dgp + int64_t(g.grid) * hd;
+    g.grid += q.blocks;
     const double n = double(D.ti.T) * s.heads * hd;
     bytes += n * (backward ? (s.g ? es : 0) + gs + es : 2 * es);
   }
@@ -747,15 +902,15 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
     const bool in = D.rot.inter != 0;
     if (!backward) {
       if (D.dt == kF32)
-        SLORA_TRY((launch_v<float, float, false>(V, in, sliced, P, grid, st)));
+        SLORA_TRY((launch_v<float, float, false>(V, in, sliced, P, g, st)));
       else
-        SLORA_TRY((launch_v<__nv_bfloat16, float, false>(V, in, sliced, P, grid, st)));
+        SLORA_TRY((launch_v<__nv_bfloat16, float, false>(V, in, sliced, P, g, st)));
     } else if (D.dt == kF32) {
-      SLORA_TRY((launch_v<float, float, true>(V, in, sliced, P, grid, st)));
+      SLORA_TRY((launch_v<float, float, true>(V, in, sliced, P, g, st)));
     } else if (D.gdt == kF32) {
-      SLORA_TRY((launch_v<__nv_bfloat16, float, true>(V, in, sliced, P, grid, st)));
+      SLORA_TRY((launch_v<__nv_bfloat16, float, true>(V, in, sliced, P, g, st)));
     } else {
-      SLORA_TRY((launch_v<__nv_bfloat16, __nv_bfloat16, true>(V, in, sliced, P, grid, st)));
+      SLORA_TRY((launch_v<__nv_bfloat16, __nv_bfloat16, true>(V, in, sliced, P, g, st)));
     }
   }
   if (any_dg) {
@@ -766,7 +921,7 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
       d.dg[i] = P.part[i].dgp ? D.part[i].dg : nullptr;
       d.blocks[i] = P.part[i].blocks;
     }
-    LaunchScope ls(kAux, double(grid) * hd * 4, st);
+    LaunchScope ls(kAux, double(g.grid) * hd * 4, st);
     qk_dg_kernel<<<dim3(unsigned((hd + 31) / 32), unsigned(D.nparts)), 1024, 0, st>>>(d);
     SLORA_CHECK_LAUNCH();
   }

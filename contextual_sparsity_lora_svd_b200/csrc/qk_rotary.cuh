@@ -6,6 +6,7 @@
 namespace slora {
 
 constexpr int kMaxHeadDim = 256;
+constexpr int kMaxSlicedChannels = 32768;  // heads * head_dim of a sliced tensor
 
 // A checked slora_rotary: turns per position of each pair in units of 2^-64
 // turn (exact modulo one turn under integer multiplication), and the factor on
