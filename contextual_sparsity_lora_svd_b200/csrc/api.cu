@@ -391,7 +391,7 @@ extern "C" slora_status slora_linear_bwd_act8(
     SLORA_FAIL(SLORA_ERR_UNSUPPORTED, "%s: 8-bit layer inputs run in bf16 only", fn);
   REQ_PTR(XA_save); REQ_PTR(dA); REQ_PTR(dB); OPT_PTR(ws);
   LinearDesc L{int(dt), ti, k, n, W, A, B, r_lora, lora_scale, side, idx, n_idx};
-  L.act8 = true;
+  slora_act8 x8_ctx = {nullptr, nullptr}, x8_out = {nullptr, nullptr};
   const bool in_cols = side == SLORA_SLICE_IN_COLS, out_rows = side == SLORA_SLICE_OUT_ROWS;
   // the operands of the rows and channels that there are
   const bool ctx = in_cols ? ti.T_C > 0 && n_idx > 0 : true;
@@ -399,19 +399,19 @@ extern "C" slora_status slora_linear_bwd_act8(
     if (!X_ctx) SLORA_FAIL(SLORA_ERR_INVALID_ARG, "%s: required checkpoint X_ctx is NULL", fn);
     REQ_PTR(X_ctx->codes); REQ_PTR(X_ctx->scales);
     REQ_PTR(dX_ctx);
-    L.x8_ctx = *X_ctx;
+    x8_ctx = *X_ctx;
   }
   if (in_cols && ti.T_O > 0) {
     if (!X_out) SLORA_FAIL(SLORA_ERR_INVALID_ARG, "%s: required checkpoint X_out is NULL", fn);
     REQ_PTR(X_out->codes); REQ_PTR(X_out->scales);
     REQ_PTR(dX_out);
-    L.x8_out = *X_out;
+    x8_out = *X_out;
   }
   if (!out_rows || (ti.T_C > 0 && n_idx > 0)) REQ_PTR(dY_ctx);
   if (out_rows && ti.T_O > 0) REQ_PTR(dY_out);
   Arena plan;
-  SLORA_TRY(linear_bwd_run(L, tok, nullptr, nullptr, XA_save, dY_ctx, dY_out, dX_ctx, dX_out, dA,
-                           dB, plan, true, nullptr));
+  SLORA_TRY(linear_bwd_act8_run(L, tok, x8_ctx, x8_out, XA_save, dY_ctx, dY_out, dX_ctx, dX_out,
+                                dA, dB, plan, true, nullptr));
   const bool query = ws == nullptr;
   SLORA_TRY(finish_ws(fn, plan, ws, ws_bytes));
   if (query) return SLORA_OK;
@@ -419,8 +419,8 @@ extern "C" slora_status slora_linear_bwd_act8(
   Arena ar;
   ar.base = static_cast<char*>(ws);
   ar.cap = *ws_bytes;
-  return linear_bwd_run(L, tok, nullptr, nullptr, XA_save, dY_ctx, dY_out, dX_ctx, dX_out, dA, dB,
-                        ar, false, static_cast<cudaStream_t>(stream));
+  return linear_bwd_act8_run(L, tok, x8_ctx, x8_out, XA_save, dY_ctx, dY_out, dX_ctx, dX_out, dA,
+                             dB, ar, false, static_cast<cudaStream_t>(stream));
 }
 
 // ------------------------------------------------------------------- FFN

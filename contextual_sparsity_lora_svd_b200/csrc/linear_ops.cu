@@ -10,11 +10,11 @@
 // and output rows, S = selected channel set (idx).
 #include <algorithm>
 
-#include "act8.cuh"
 #include "estimator.cuh"
 #include "gemm.cuh"
 #include "gemm_tc.cuh"
 #include "linear_ops.cuh"
+#include "lora_grad.cuh"
 #include "lora_pack.cuh"
 #include "skinny.cuh"
 #include "swiglu.cuh"
@@ -908,15 +908,6 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
   const int64_t lr = round8(r), ldi = round8(std::max<int64_t>(ni, 1));
   const bool none = L.side == SLORA_SLICE_NONE, outr = L.side == SLORA_SLICE_OUT_ROWS;
   const int64_t nct = count_tiles(tok, true), nott = count_tiles(tok, false);
-  // rank operands in fp32: one bf16 term, three beside an 8-bit input, whose
-  // gradients are to be exact for the values it holds
-  const int terms = L.act8 ? 0 : 1;
-  auto rkv = [terms](const void* p, int dtp, int64_t si, int64_t sq, const int32_t* map = nullptr,
-                     int64_t map_limit = INT64_MAX) {
-    SkR rr = slora::rkv(p, dtp, si, sq, map, map_limit);
-    if (dtp == kF32) rr.terms = terms;
-    return rr;
-  };
   auto bf = [&](int64_t rows, int64_t cols) {
     return static_cast<void*>(ar.take<__nv_bfloat16>(size_t(std::max<int64_t>(rows * cols, 1))));
   };
@@ -933,7 +924,7 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
   void* AS = bf(ni, lr);      // A[:, idx]^T padded (IN_COLS)
   void* At = bf(k, lr);       // A^T padded (IN_COLS)
   void* dYpad = (outr && ni % 8) ? bf(TC, ldi) : nullptr;
-  void* Xpad = (!none && !outr && ni % 8 && !L.act8) ? bf(TC, ldi) : nullptr;
+  void* Xpad = (!none && !outr && ni % 8) ? bf(TC, ldi) : nullptr;
   float* part = ar.take<float>(size_t(skinny_part_bound(ti, k, n, ni, r)));
   const int64_t ncnt = skinny_counter_count(std::max({T, k, n}), std::max({T, k, n}));
   unsigned* rsp = ar.take<unsigned>(size_t(ncnt));
@@ -981,59 +972,26 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
     }
     const void* dYc0 = dYpad ? dYpad : dY_ctx;
     const int64_t lddc0 = dYpad ? ldi : ni;
-    if (!L.act8) bj[nbj++] = cjob(X_ctx, k, T, k, rkv(dYB, kF32, r, 1), rsDY, dA, k, 1);
     if (none) {
+      bj[nbj++] = cjob(X_ctx, k, T, k, rkv(dYB, kF32, r, 1), rsDY, dA, k, 1);
       bj[nbj++] = cjob(dY_ctx, n, T, n, rkv(XA, kF32, r, 1), rsX0, dB, r, 0);
     } else {
+      bj[nbj++] = cjob(X_ctx, k, T, k, rkv(dYB, kF32, r, 1), rsDY, dA, k, 1);
       bj[nbj++] = cjob(dY_out, n, TO, n, rkv(XA, kF32, r, 1, out_rows), rsX0, dB, r, 0);
       bj[nbj++] = cjob(dYc0, lddc0, TC, ni, rkv(XA, kF32, r, 1, ctx_rows), rsX1, SB, r, 0);
     }
   }
   float* bpart = nullptr;
-  int64_t nbcnt = 0;
+  unsigned* bcnt = nullptr;
   if (batched) {
     bpart = ar.take<float>(size_t(coldot_batch_part_floats(bj, nbj)));
-    nbcnt = coldot_batch_counter_count(bj, nbj);
+    bcnt = ar.take<unsigned>(size_t(coldot_batch_counter_count(bj, nbj)));
   }
-  // an 8-bit input's contractions; their arrival counters lie behind the
-  // batch's, so that the row-map launch zeroes both
-  float* part8 = nullptr;
-  void* rs8 = nullptr;
-  int64_t ncnt8 = 0;
-  if (L.act8) {
-    int64_t np8 = act8_dot_part_floats(T, k, r);
-    ncnt8 = act8_dot_counters(k, r);
-    if (!none && !outr) {
-      np8 = std::max(act8_dot_part_floats(TO, k, r), act8_dot_part_floats(TC, ni, r));
-      ncnt8 = std::max(ncnt8, act8_dot_counters(ni, r));
-    }
-    part8 = ar.take<float>(size_t(np8));
-    if (!batched) rs8 = rsbuf(T);
-  }
-  unsigned* bcnt = nbcnt + ncnt8 ? ar.take<unsigned>(size_t(nbcnt + ncnt8)) : nullptr;
-  unsigned* cnt8 = bcnt ? bcnt + nbcnt : nullptr;
   if (plan) return SLORA_OK;
   SLORA_TRY(arena_fits(ar, "workspace"));
-  // dA (+)= s dYB^T X over the rows of a checkpoint, rs the split dYB of its rows
-  auto dot8 = [&](const slora_act8& X, int64_t M, int64_t K, const void* rs, const int32_t* kmap,
-                  int accumulate) {
-    Act8Dot j;
-    j.X = X; j.M = M; j.K = K; j.P = rs; j.cols = r; j.out = dA; j.ldo = k; j.kmap = kmap;
-    j.scale = s; j.accumulate = accumulate;
-    return act8_dot(j, part8, cnt8, st);
-  };
-  // dYB of rows `map` split into rs8 (its rows' place in the checkpoint's order), then dot8
-  auto grad8 = [&](const slora_act8& X, int64_t M, int64_t K, const int32_t* map,
-                   const int32_t* kmap, int accumulate) -> slora_status {
-    if (M > 0) {
-      const SkPrep jd = {rkv(dYB, kF32, r, 1, map), r, M, rs8};
-      SLORA_TRY(prep_r_batch(&jd, 1, st));
-    }
-    return dot8(X, M, K, rs8, kmap, accumulate);
-  };
 
   SLORA_TRY(launch_rowmaps(tok, ti, ctx_rows, out_rows, st, ctiles, otiles, rsp, ncnt, bcnt,
-                           nbcnt + ncnt8));
+                           bcnt ? coldot_batch_counter_count(bj, nbj) : 0));
   if (batched && none) {
     const SkPrep jobs[2] = {{rkv(L.B, kBF16, r, 1), r, n, rsB0}, {rkv(XA, kF32, r, 1), r, T, rsX0}};
     SLORA_TRY(prep_r_batch(jobs, 2, st));
@@ -1048,7 +1006,6 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
     SLORA_TRY(gemm_tc(b.g, st));
     const SkPrep jd = {rkv(dYB, kF32, r, 1), r, T, rsDY};
     SLORA_TRY(prep_r_batch(&jd, 1, st));
-    if (L.act8) SLORA_TRY(dot8(L.x8_ctx, T, k, rsDY, nullptr, 0));
     return coldot_batch(bj, nbj, bpart, bcnt, st);
   }
   if (batched && outr) {
@@ -1085,7 +1042,6 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
     }
     const SkPrep jd = {rkv(dYB, kF32, r, 1), r, T, rsDY};
     SLORA_TRY(prep_r_batch(&jd, 1, st));
-    if (L.act8) SLORA_TRY(dot8(L.x8_ctx, T, k, rsDY, nullptr, 0));
     SLORA_TRY(coldot_batch(bj, nbj, bpart, bcnt, st));
     ScatterAddJob sj;
     sj.dst = dB; sj.ld_dst = r; sj.src = SB; sj.ld_src = r; sj.trans = 0;
@@ -1145,7 +1101,6 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
           .out(dX_ctx, nullptr, nullptr, k);
       SLORA_TRY(gemm_tc_pair(bc.g, b.g, st));
     }
-    if (L.act8) return grad8(L.x8_ctx, T, k, nullptr, nullptr, 0);
     SkColOut ca;  // dA = s dYB^T X over every row
     ca.out = dA; ca.ldo = k; ca.trans = 1; ca.scale = s;
     return coldot(ykv(X_ctx, k), T, k, rkv(dYB, kF32, r, 1), r, ca, sw, st);
@@ -1177,10 +1132,7 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
         .out(dX_out, nullptr, nullptr, k);
     SLORA_TRY(gemm_tc_pair(bc.g, b.g, st));
   }
-  if (L.act8) {
-    SLORA_TRY(grad8(L.x8_out, TO, k, out_rows, nullptr, 0));
-    SLORA_TRY(grad8(L.x8_ctx, TC, ni, ctx_rows, L.idx, 1));
-  } else {  // dA: output rows over every column, then += context rows on columns S
+  {  // dA: output rows over every column, then += context rows on columns S
     SkColOut ao;
     ao.out = dA; ao.ldo = k; ao.trans = 1; ao.scale = s;
     SLORA_TRY(coldot(ykv(X_out, k), TO, k, rkv(dYB, kF32, r, 1, out_rows), r, ao, sw, st));
@@ -1191,6 +1143,134 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
   SkColOut cb;  // dB = s dY^T XA over every row
   cb.out = dB; cb.ldo = r; cb.scale = s;
   return coldot(ykv(dY_ctx, n), T, n, rkv(XA, kF32, r, 1), r, cb, sw, st);
+}
+
+// The backward from 8-bit checkpoints: dX as above, on the same GEMMs; the
+// rank-r contractions on the kernels of lora_grad.cu, which read the
+// checkpoint's codes and keep dY B and X A^T in fp32.  Per call: one launch
+// for dY B (both row kinds), one for dA and dB; the part of a gradient that
+// belongs to the selected channels lands in a buffer of its own and is added
+// onto them.
+slora_status linear_bwd_act8_run(const LinearDesc& L0, const slora_tokens* tok,
+                                 const slora_act8& X_ctx, const slora_act8& X_out,
+                                 const float* XA, const void* dY_ctx, const void* dY_out,
+                                 void* dX_ctx, void* dX_out, float* dA, float* dB, Arena& ar,
+                                 bool plan, cudaStream_t st) {
+  LinearDesc L;
+  SLORA_TRY(safe_indices(L0, ar, plan, st, &L));
+  const TokenInfo& ti = L.ti;
+  const int r = L.r;
+  const int64_t k = L.k, n = L.n, ni = L.n_idx, T = ti.T, TC = ti.T_C, TO = ti.T_O;
+  const float s = L.s;
+  const int64_t lr = round8(r), ldi = round8(std::max<int64_t>(ni, 1));
+  const bool none = L.side == SLORA_SLICE_NONE, outr = L.side == SLORA_SLICE_OUT_ROWS;
+  const int64_t nct = count_tiles(tok, true), nott = count_tiles(tok, false);
+  auto bf = [&](int64_t rows, int64_t cols) {
+    return static_cast<void*>(ar.take<__nv_bfloat16>(size_t(std::max<int64_t>(rows * cols, 1))));
+  };
+  int32_t* ctx_rows = ar.take<int32_t>(size_t(std::max<int64_t>(TC, 1)));
+  int32_t* out_rows = ar.take<int32_t>(size_t(std::max<int64_t>(TO, 1)));
+  int4* ctiles = ar.take<int4>(size_t(std::max<int64_t>(nct, 1)));
+  int4* otiles = ar.take<int4>(size_t(std::max<int64_t>(nott, 1)));
+  int4* ptiles = none ? ar.take<int4>(size_t((T + 127) / 128)) : nullptr;
+  float* dYB = ar.take<float>(size_t(T) * r);
+  // s dY B in bf16, the GEMMs' LoRA operand: full rows, or compact by row kind
+  void* dYBb = outr ? nullptr : bf(T, lr);
+  void* dYBbC = outr ? bf(TC, lr) : nullptr;
+  void* dYBbO = outr ? bf(TO, lr) : nullptr;
+  void* WS = none ? nullptr : bf(ni, outr ? k : n);  // rows idx of W
+  void* AS = none || outr ? nullptr : bf(ni, lr);    // A[:, idx]^T and A^T, padded
+  void* At = none || outr ? nullptr : bf(k, lr);
+  void* dYpad = outr && ni % 8 ? bf(TC, ldi) : nullptr;
+  float* SG = none ? nullptr : ar.take<float>(size_t(std::max<int64_t>(ni, 1)) * r);
+  void* rsB0 = ar.take<__nv_bfloat16>(size_t(skinny_rsplit_elems(outr ? ni : n)));
+  void* rsB1 = outr ? ar.take<__nv_bfloat16>(size_t(skinny_rsplit_elems(n))) : nullptr;
+  const void* dYc = dYpad ? dYpad : dY_ctx;
+  const int64_t lddc = dYpad ? ldi : ni;
+
+  RankSum sums[kRankSums];
+  int nsums = 0;
+  auto add_sum = [&](int64_t M, int64_t K, const float* P, const int32_t* map, float* out,
+                     int64_t ldo, int trans) -> RankSum& {
+    RankSum& j = sums[nsums++];
+    j.M = M; j.K = K; j.P = P; j.ldp = r; j.map = map; j.out = out; j.ldo = ldo; j.trans = trans;
+    return j;
+  };
+  if (none || outr) add_sum(T, k, dYB, nullptr, dA, k, 1).X8 = X_ctx;
+  else add_sum(TO, k, dYB, out_rows, dA, k, 1).X8 = X_out;
+  {
+    RankSum& j = outr ? add_sum(TO, n, XA, out_rows, dB, r, 0) : add_sum(T, n, XA, nullptr, dB, r, 0);
+    j.X = outr ? dY_out : dY_ctx;
+    j.ld = n;
+  }
+  const bool sliced = !none && TC > 0 && ni > 0;
+  if (sliced && outr) {
+    RankSum& j = add_sum(TC, ni, XA, ctx_rows, SG, r, 0);
+    j.X = dYc;
+    j.ld = lddc;
+  } else if (sliced) {
+    add_sum(TC, ni, dYB, ctx_rows, SG, ni, 1).X8 = X_ctx;
+  }
+  float* part = ar.take<float>(size_t(rank_sums_part(sums, nsums, r)));
+  const int64_t ncnt = rank_sums_counters(sums, nsums, r);
+  unsigned* cnt = ar.take<unsigned>(size_t(ncnt));
+  if (plan) return SLORA_OK;
+  SLORA_TRY(arena_fits(ar, "workspace"));
+
+  SLORA_TRY(launch_rowmaps(tok, ti, ctx_rows, out_rows, st, ctiles, otiles, cnt, ncnt));
+  if (dYpad) SLORA_TRY(gather_pad(dY_ctx, ni, nullptr, TC, ni, dYpad, ldi, st, TC));
+  {  // dY B, one bf16 term of B (B is bf16: exact)
+    const SkPrep jobs[2] = {{rkv(L.B, kBF16, r, 1, outr ? L.idx : nullptr, n), r, outr ? ni : n, rsB0},
+                            {rkv(L.B, kBF16, r, 1), r, n, rsB1}};
+    SLORA_TRY(prep_r_batch(jobs, outr ? 2 : 1, st));
+    RankRows rows[2];
+    rows[0].Y = outr ? dYc : dY_ctx; rows[0].ld = outr ? lddc : n;
+    rows[0].M = outr ? TC : T; rows[0].K = outr ? ni : n; rows[0].R = rsB0;
+    rows[0].out1 = dYB; rows[0].ld1 = r; rows[0].map1 = outr ? ctx_rows : nullptr;
+    rows[0].out2 = outr ? dYBbC : dYBb; rows[0].ld2 = lr;
+    rows[1].Y = dY_out; rows[1].ld = n; rows[1].M = TO; rows[1].K = n; rows[1].R = rsB1;
+    rows[1].out1 = dYB; rows[1].ld1 = r; rows[1].map1 = out_rows;
+    rows[1].out2 = dYBbO; rows[1].ld2 = lr;
+    SLORA_TRY(rank_rows(rows, outr ? 2 : 1, r, s, st));
+  }
+  if (none) {
+    SLORA_TRY(make_plain_tiles(ptiles, T, st));
+    TcBuilder b(ptiles, (T + 127) / 128, 0, 0, T, k, 0, EPI_STORE);
+    b.seg(mat(dY_ctx, T, n, n), mat(L.W, n, k, k), B_MN, n)
+        .seg(mat(dYBb, T, r, lr), mat(L.A, r, k, k), B_MN, r)
+        .out(dX_ctx, nullptr, nullptr, k);
+    SLORA_TRY(gemm_tc(b.g, st));
+  } else if (outr) {
+    SLORA_TRY(gather_rows(L.W, k, L.idx, ni, k, WS, k, st, n));
+    TcBuilder bc(ctiles, nct, 1, 0, TC, k, 0, EPI_STORE);
+    bc.seg(mat(dYc, TC, ni, lddc), mat(WS, ni, k, k), B_MN, ni)
+        .seg(mat(dYBbC, TC, r, lr), mat(L.A, r, k, k), B_MN, r)
+        .out(dX_ctx, nullptr, nullptr, k);
+    TcBuilder b(otiles, nott, 1, 0, TO, k, 0, EPI_STORE);
+    b.seg(mat(dY_out, TO, n, n), mat(L.W, n, k, k), B_MN, n)
+        .seg(mat(dYBbO, TO, r, lr), mat(L.A, r, k, k), B_MN, r)
+        .out(dX_ctx, nullptr, nullptr, k);
+    SLORA_TRY(gemm_tc_pair(bc.g, b.g, st));
+  } else {
+    SLORA_TRY(gather_rows(L.W, n, L.idx, ni, n, WS, n, st, k));
+    SLORA_TRY(transpose_rows(L.A, r, k, L.idx, ni, lr, AS, st));
+    SLORA_TRY(transpose_rows(L.A, r, k, nullptr, k, lr, At, st));
+    TcBuilder bc(ctiles, nct, 0, 1, TC, ni, 0, EPI_STORE);
+    bc.seg(mat(dY_ctx, T, n, n), mat(WS, ni, n, n), B_K, n)
+        .seg(mat(dYBb, T, r, lr), mat(AS, ni, r, lr), B_K, r)
+        .out(dX_ctx, nullptr, nullptr, ni);
+    TcBuilder b(otiles, nott, 0, 1, TO, k, 0, EPI_STORE);
+    b.seg(mat(dY_ctx, T, n, n), mat(L.W, k, n, n), B_K, n)
+        .seg(mat(dYBb, T, r, lr), mat(At, k, r, lr), B_K, r)
+        .out(dX_out, nullptr, nullptr, k);
+    SLORA_TRY(gemm_tc_pair(bc.g, b.g, st));
+  }
+  SLORA_TRY(rank_sums(sums, nsums, r, s, part, cnt, st));
+  if (!sliced) return SLORA_OK;
+  ScatterAddJob sj;
+  sj.dst = outr ? dB : dA; sj.ld_dst = outr ? r : k;
+  sj.src = SG; sj.ld_src = outr ? r : ni; sj.trans = outr ? 0 : 1;
+  return scatter_add_cols(&sj, 1, L.idx, ni, r, outr ? n : k, st);
 }
 
 }  // namespace slora

@@ -17,10 +17,6 @@ struct LinearDesc {
   slora_slice side;
   const int32_t* idx;
   int32_t n_idx;
-  // backward only: the layer input as 8-bit checkpoints in place of X_ctx and
-  // X_out (bf16 path); the rank operands then keep three bf16 terms
-  bool act8 = false;
-  slora_act8 x8_ctx = {nullptr, nullptr}, x8_out = {nullptr, nullptr};
 };
 
 // With plan == true only the arena is sized (no pointer is touched).
@@ -31,6 +27,13 @@ slora_status linear_bwd_run(const LinearDesc& L, const slora_tokens* tok, const 
                             const void* X_out, const float* XA, const void* dY_ctx,
                             const void* dY_out, void* dX_ctx, void* dX_out, float* dA, float* dB,
                             Arena& ar, bool plan, cudaStream_t st);
+
+// The backward with the layer input as 8-bit checkpoints (bf16 path).
+slora_status linear_bwd_act8_run(const LinearDesc& L, const slora_tokens* tok,
+                                 const slora_act8& X_ctx, const slora_act8& X_out,
+                                 const float* XA, const void* dY_ctx, const void* dY_out,
+                                 void* dX_ctx, void* dX_out, float* dA, float* dB, Arena& ar,
+                                 bool plan, cudaStream_t st);
 
 struct FfnDesc {
   int dt;

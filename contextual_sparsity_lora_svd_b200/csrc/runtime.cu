@@ -6,6 +6,7 @@
 #include "common.cuh"
 #include "estimator.cuh"
 #include "gemm_tc.cuh"
+#include "lora_grad.cuh"
 #include "lora_pack.cuh"
 #include "qk_rotary.cuh"
 #include "skinny.cuh"
@@ -286,14 +287,17 @@ extern "C" slora_status slora_device_error(int clear) {
   const slora_status e = attn_check_error(clear != 0);
   const std::string fifth = e != SLORA_OK ? g_error : std::string();
   const slora_status f = qk_check_error(clear != 0);
+  const std::string sixth = f != SLORA_OK ? g_error : std::string();
+  const slora_status g = rank_check_error(clear != 0);
   if (a != SLORA_OK) g_error = first;
   else if (b != SLORA_OK) g_error = second;
   else if (c != SLORA_OK) g_error = third;
   else if (d != SLORA_OK) g_error = fourth;
   else if (e != SLORA_OK) g_error = fifth;
-  for (slora_status st : {a, b, c, d, e})
+  else if (f != SLORA_OK) g_error = sixth;
+  for (slora_status st : {a, b, c, d, e, f})
     if (st != SLORA_OK) return st;
-  return f;
+  return g;
 }
 
 extern "C" slora_status slora_set_wait_budget(int64_t cycles) {

@@ -645,8 +645,8 @@ slora_status slora_rmsnorm_bwd_act8(slora_dtype dt, int64_t T, int64_t d, const 
  * slora_linear_bwd_act8 — slora_linear_bwd whose layer input is a checkpoint:
  * X_ctx (and X_out, for SLORA_SLICE_IN_COLS) of the same shapes, read as codes
  * by the dA contraction itself.  SLORA_BF16 only.  The rank-r operands dY B and
- * XA_save enter the sums at full fp32 precision (three bf16 terms), so dA and
- * dB are exact to fp32 rounding for the values that the checkpoint holds.
+ * XA_save enter the sums in fp32, so dA and dB are exact to fp32 rounding for
+ * the values that the checkpoint holds.
  */
 slora_status slora_linear_bwd_act8(slora_dtype dt, const slora_tokens* tok, int64_t k, int64_t n,
                                    const void* W, const void* A, const void* B, int r_lora,
