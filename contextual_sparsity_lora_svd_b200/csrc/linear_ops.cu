@@ -1147,10 +1147,10 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
 
 // The backward from 8-bit checkpoints: dX as above, on the same GEMMs; the
 // rank-r contractions on the kernels of lora_grad.cu, which read the
-// checkpoint's codes and keep dY B and X A^T in fp32.  Per call: one launch
-// for dY B (both row kinds), one for dA and dB; the part of a gradient that
-// belongs to the selected channels lands in a buffer of its own and is added
-// onto them.
+// checkpoint's codes and take dY B and X A^T to fp32 precision.  Per call: one
+// launch for dY B (both row kinds), one for dA and dB; the part of a gradient
+// that belongs to the selected channels lands in a buffer of its own and is
+// added onto them.
 slora_status linear_bwd_act8_run(const LinearDesc& L0, const slora_tokens* tok,
                                  const slora_act8& X_ctx, const slora_act8& X_out,
                                  const float* XA, const void* dY_ctx, const void* dY_out,
@@ -1173,7 +1173,6 @@ slora_status linear_bwd_act8_run(const LinearDesc& L0, const slora_tokens* tok,
   int4* ctiles = ar.take<int4>(size_t(std::max<int64_t>(nct, 1)));
   int4* otiles = ar.take<int4>(size_t(std::max<int64_t>(nott, 1)));
   int4* ptiles = none ? ar.take<int4>(size_t((T + 127) / 128)) : nullptr;
-  float* dYB = ar.take<float>(size_t(T) * r);
   // s dY B in bf16, the GEMMs' LoRA operand: full rows, or compact by row kind
   void* dYBb = outr ? nullptr : bf(T, lr);
   void* dYBbC = outr ? bf(TC, lr) : nullptr;
@@ -1187,29 +1186,38 @@ slora_status linear_bwd_act8_run(const LinearDesc& L0, const slora_tokens* tok,
   void* rsB1 = outr ? ar.take<__nv_bfloat16>(size_t(skinny_rsplit_elems(n))) : nullptr;
   const void* dYc = dYpad ? dYpad : dY_ctx;
   const int64_t lddc = dYpad ? ldi : ni;
+  // terms of dY B and of XA: full rows, or by row kind in compact order
+  const bool in_cols = !none && !outr;
+  auto terms = [&](int64_t M) {
+    return static_cast<void*>(ar.take<__nv_bfloat16>(size_t(rank_terms_elems(M, r))));
+  };
+  void* tP = in_cols ? terms(TC) : terms(T);
+  void* tPo = in_cols ? terms(TO) : nullptr;
+  void* tX = outr ? terms(TO) : terms(T);
+  void* tXc = outr ? terms(TC) : nullptr;
 
   RankSum sums[kRankSums];
   int nsums = 0;
-  auto add_sum = [&](int64_t M, int64_t K, const float* P, const int32_t* map, float* out,
-                     int64_t ldo, int trans) -> RankSum& {
+  auto add_sum = [&](int64_t M, int64_t K, const void* t, float* out, int64_t ldo,
+                     int trans) -> RankSum& {
     RankSum& j = sums[nsums++];
-    j.M = M; j.K = K; j.P = P; j.ldp = r; j.map = map; j.out = out; j.ldo = ldo; j.trans = trans;
+    j.M = M; j.K = K; j.terms = t; j.out = out; j.ldo = ldo; j.trans = trans;
     return j;
   };
-  if (none || outr) add_sum(T, k, dYB, nullptr, dA, k, 1).X8 = X_ctx;
-  else add_sum(TO, k, dYB, out_rows, dA, k, 1).X8 = X_out;
+  if (in_cols) add_sum(TO, k, tPo, dA, k, 1).X8 = X_out;
+  else add_sum(T, k, tP, dA, k, 1).X8 = X_ctx;
   {
-    RankSum& j = outr ? add_sum(TO, n, XA, out_rows, dB, r, 0) : add_sum(T, n, XA, nullptr, dB, r, 0);
+    RankSum& j = add_sum(outr ? TO : T, n, tX, dB, r, 0);
     j.X = outr ? dY_out : dY_ctx;
     j.ld = n;
   }
   const bool sliced = !none && TC > 0 && ni > 0;
   if (sliced && outr) {
-    RankSum& j = add_sum(TC, ni, XA, ctx_rows, SG, r, 0);
+    RankSum& j = add_sum(TC, ni, tXc, SG, r, 0);
     j.X = dYc;
     j.ld = lddc;
   } else if (sliced) {
-    add_sum(TC, ni, dYB, ctx_rows, SG, ni, 1).X8 = X_ctx;
+    add_sum(TC, ni, tP, SG, ni, 1).X8 = X_ctx;
   }
   float* part = ar.take<float>(size_t(rank_sums_part(sums, nsums, r)));
   const int64_t ncnt = rank_sums_counters(sums, nsums, r);
@@ -1219,19 +1227,43 @@ slora_status linear_bwd_act8_run(const LinearDesc& L0, const slora_tokens* tok,
 
   SLORA_TRY(launch_rowmaps(tok, ti, ctx_rows, out_rows, st, ctiles, otiles, cnt, ncnt));
   if (dYpad) SLORA_TRY(gather_pad(dY_ctx, ni, nullptr, TC, ni, dYpad, ldi, st, TC));
-  {  // dY B, one bf16 term of B (B is bf16: exact)
-    const SkPrep jobs[2] = {{rkv(L.B, kBF16, r, 1, outr ? L.idx : nullptr, n), r, outr ? ni : n, rsB0},
-                            {rkv(L.B, kBF16, r, 1), r, n, rsB1}};
-    SLORA_TRY(prep_r_batch(jobs, outr ? 2 : 1, st));
+  {  // B in one bf16 term (exact), XA in three
+    SkPrep jobs[4];
+    int nj = 0;
+    auto prep = [&](const SkR& R, int64_t I, void* rs) {
+      jobs[nj].R = R; jobs[nj].c = r; jobs[nj].I = I; jobs[nj].rs = rs;
+      ++nj;
+    };
+    auto xa = [&](const int32_t* map) {
+      SkR R = rkv(XA, kF32, r, 1, map);
+      R.terms = 0;
+      return R;
+    };
+    prep(rkv(L.B, kBF16, r, 1, outr ? L.idx : nullptr, n), outr ? ni : n, rsB0);
+    prep(xa(outr ? out_rows : nullptr), outr ? TO : T, tX);
+    if (outr) {
+      prep(rkv(L.B, kBF16, r, 1), n, rsB1);
+      prep(xa(ctx_rows), TC, tXc);
+    }
+    SLORA_TRY(prep_r_batch(jobs, nj, st));
     RankRows rows[2];
-    rows[0].Y = outr ? dYc : dY_ctx; rows[0].ld = outr ? lddc : n;
-    rows[0].M = outr ? TC : T; rows[0].K = outr ? ni : n; rows[0].R = rsB0;
-    rows[0].out1 = dYB; rows[0].ld1 = r; rows[0].map1 = outr ? ctx_rows : nullptr;
-    rows[0].out2 = outr ? dYBbC : dYBb; rows[0].ld2 = lr;
-    rows[1].Y = dY_out; rows[1].ld = n; rows[1].M = TO; rows[1].K = n; rows[1].R = rsB1;
-    rows[1].out1 = dYB; rows[1].ld1 = r; rows[1].map1 = out_rows;
-    rows[1].out2 = dYBbO; rows[1].ld2 = lr;
-    SLORA_TRY(rank_rows(rows, outr ? 2 : 1, r, s, st));
+    RankRows &rc = rows[0], &ro = rows[1];
+    rc.R = rsB0; rc.terms = tP; rc.ldo = lr;
+    if (none) {
+      rc.Y = dY_ctx; rc.ld = n; rc.M = T; rc.K = n; rc.ldt = rank_terms_ld(T); rc.out = dYBb;
+    } else if (outr) {  // compact rows of dY; dA sums over the full rows
+      rc.Y = dYc; rc.ld = lddc; rc.M = TC; rc.K = ni; rc.out = dYBbC;
+      rc.map = ctx_rows; rc.map_terms = true; rc.ldt = rank_terms_ld(T);
+      ro = rc;
+      ro.Y = dY_out; ro.ld = n; ro.M = TO; ro.K = n; ro.R = rsB1; ro.out = dYBbO;
+      ro.map = out_rows;
+    } else {  // full rows of dY; dA sums over each kind's compact rows
+      rc.Y = dY_ctx; rc.ld = n; rc.M = TC; rc.K = n; rc.out = dYBb;
+      rc.map = ctx_rows; rc.map_y = rc.map_out = true; rc.ldt = rank_terms_ld(TC);
+      ro = rc;
+      ro.M = TO; ro.map = out_rows; ro.terms = tPo; ro.ldt = rank_terms_ld(TO);
+    }
+    SLORA_TRY(rank_rows(rows, none ? 1 : 2, r, s, st));
   }
   if (none) {
     SLORA_TRY(make_plain_tiles(ptiles, T, st));

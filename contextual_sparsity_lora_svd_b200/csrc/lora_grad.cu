@@ -8,25 +8,30 @@
 // memory.  The channel order inside a reduction is free, so lane t of a quad
 // takes 8 consecutive channels (one 16-byte load a row, the same 8 channels of
 // B's transposed copy), two k-steps of fragments.  A block owns 16 rows, its
-// eight warps take every eighth 32-channel group and are summed in order in
-// shared memory: no partial sums leave the block.
+// sixteen warps take every sixteenth 32-channel group and are summed in order
+// in shared memory: no partial sums leave the block.  p is written as the
+// GEMM's LoRA operand (bf16) and as the three bf16 terms that rank_sums reads.
 //
 // rank_sums: tcgen05.mma with 128 channels as M, the tokens as the reduction and
 // N = 48: 16 rank columns in three bf16 terms (an fp32 operand to 2^-24), so the
-// sums are those of fp32 operands.  Legacy mma.sync took 21 us for 4096 x 4096
-// codes at r = 16, packed fp32 FMAs 30 us.  X lies in shared memory as it does
-// in global memory, a token's 128 channels in a row (an M-major operand, 128-byte
-// swizzle): bf16 rows are copied there asynchronously; codes are copied to a
-// ring beside it and expanded by the thread that asked for them (a byte permute
-// pairs two codes, two logic operations and an addition make them bf16, a
-// product applies the step: all exact).  The same eight warps split the token's P
-// row into its terms.  A stage is 64 tokens, three stages are on their way; a
-// ninth warp issues the products.  The stages take turns on four accumulators:
-// the tensor core truncates each addition, and four short chains added in fp32
-// are off by a quarter of one long one.  Blocks that share channels leave partial
-// sums that the last to arrive adds in order: the result does not depend on
-// timing.  Every wait is bounded; on expiry the block raises a device flag
-// (slora_device_error: SLORA_ERR_TIMEOUT) and leaves after its own work ended.
+// sums are those of fp32 operands.  For 4096 x 4096 codes at r = 16, legacy
+// mma.sync took 21 us and packed fp32 FMAs 30 us.  X lies in shared memory as
+// it does in global memory, a token's 128 channels in a row (an M-major operand,
+// 128-byte swizzle): bf16 rows and the rank operand's terms come by TMA; codes
+// come by TMA into a ring and eight warps expand them into the operand (a byte
+// permute pairs two codes, two logic operations and an addition make them bf16,
+// a product applies the step: all exact).  A stage is 64 tokens, four are in
+// flight.  The stages take turns on four accumulators: the tensor core truncates
+// each addition, and four short chains added in fp32 are off by a quarter of one
+// long one.  Blocks that share channels leave partial sums that the last to
+// arrive adds in order: the result does not depend on timing.  Every wait is
+// bounded; on expiry the block raises a device flag (slora_device_error:
+// SLORA_ERR_TIMEOUT) and leaves after its own copies and products ended.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
 #include <algorithm>
 
 #include "act8_dev.cuh"
@@ -38,8 +43,8 @@ __device__ int g_rank_error = 0;
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kCols = 16;  // rank columns of a block (more: further blocks)
+constexpr int kCols = 16;   // rank columns of a block (more: further blocks)
+constexpr int kTerms = 3;   // bf16 terms of an fp32 rank operand
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -51,44 +56,51 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 }
 
 // ------------------------------------------------------------------- rows
+constexpr int kRowWarps = 16;
+
 struct RowsJob {
   const __nv_bfloat16* Y;
   const __nv_bfloat16* R;  // [cols rounded up to 16][K64]
   long long ld, M, K, K64;
-  float* out1;
-  long long ld1;
-  const int32_t* map1;
-  __nv_bfloat16* out2;
-  long long ld2;
+  const int32_t* map;
+  int map_y, map_terms, map_out;
+  __nv_bfloat16* terms;  // [kTerms][cp][ldt]
+  long long ldt;
+  __nv_bfloat16* out;
+  long long ldo;
 };
 struct RowsParams {
   RowsJob job[2];
   int blocks0;  // 16-row blocks of job 0
-  int cols;
-  float s2;
+  int cols, cp;
+  float s;
 };
 
-__global__ void __launch_bounds__(kWarps * 32) rank_rows_kernel(const __grid_constant__ RowsParams P) {
-  __shared__ float red[kWarps][16][kCols + 1];
+__global__ void __launch_bounds__(kRowWarps * 32, 2)
+    rank_rows_kernel(const __grid_constant__ RowsParams P) {
+  __shared__ float red[kRowWarps][16][kCols + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const bool second = int(blockIdx.x) >= P.blocks0;
   const RowsJob& j = P.job[second ? 1 : 0];
   const long long m0 = (long long)(int(blockIdx.x) - (second ? P.blocks0 : 0)) * 16;
   const int q0 = blockIdx.y * kCols;
   const bool on0 = m0 + g < j.M, on1 = m0 + g + 8 < j.M;
-  const __nv_bfloat16* y0 = j.Y + (m0 + g) * j.ld;
-  const __nv_bfloat16* y1 = y0 + 8 * j.ld;
+  auto row = [&](long long m, bool on, int mapped) -> long long {
+    return !on ? 0 : (mapped ? (long long)j.map[m] : m);
+  };
+  const __nv_bfloat16* y0 = j.Y + row(m0 + g, on0, j.map_y) * j.ld;
+  const __nv_bfloat16* y1 = j.Y + row(m0 + g + 8, on1, j.map_y) * j.ld;
   const __nv_bfloat16* r0 = j.R + (q0 + g) * j.K64;
   const __nv_bfloat16* r1 = r0 + 8 * j.K64;
   float acc[2][4] = {};
   const uint4 none = make_uint4(0, 0, 0, 0);
-  // four groups of 32 channels in flight; every 8-channel load lies inside the
-  // row's whole 16-byte units or is left out
-  for (long long c0 = warp * 32; c0 < j.K; c0 += kWarps * 32 * 4) {
-    uint4 a[4], b[4], r[4], s[4];
+  constexpr int kDeep = 3;  // groups of 32 channels in flight
+  // every 8-channel load lies inside the row's whole 16-byte units or is left out
+  for (long long c0 = warp * 32; c0 < j.K; c0 += kRowWarps * 32 * kDeep) {
+    uint4 a[kDeep], b[kDeep], r[kDeep], s[kDeep];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const long long c = c0 + i * kWarps * 32 + 8 * t;
+    for (int i = 0; i < kDeep; ++i) {
+      const long long c = c0 + i * kRowWarps * 32 + 8 * t;
       const bool on = c < j.K;
       a[i] = on && on0 ? *reinterpret_cast<const uint4*>(y0 + c) : none;
       b[i] = on && on1 ? *reinterpret_cast<const uint4*>(y1 + c) : none;
@@ -96,7 +108,7 @@ __global__ void __launch_bounds__(kWarps * 32) rank_rows_kernel(const __grid_con
       s[i] = on ? __ldg(reinterpret_cast<const uint4*>(r1 + c)) : none;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kDeep; ++i) {
       mma_bf16(acc[0], a[i].x, b[i].x, a[i].y, b[i].y, r[i].x, r[i].y);
       mma_bf16(acc[1], a[i].x, b[i].x, a[i].y, b[i].y, s[i].x, s[i].y);
       mma_bf16(acc[0], a[i].z, b[i].z, a[i].w, b[i].w, r[i].z, r[i].w);
@@ -108,43 +120,49 @@ __global__ void __launch_bounds__(kWarps * 32) rank_rows_kernel(const __grid_con
 #pragma unroll
     for (int e = 0; e < 4; ++e) red[warp][g + 8 * (e >> 1)][n * 8 + 2 * t + (e & 1)] = acc[n][e];
   __syncthreads();
-  const int row = threadIdx.x / kCols, q = threadIdx.x % kCols;  // 256 threads: one value each
-  const long long m = m0 + row;
+  if (threadIdx.x >= 256) return;
+  // a thread a value: the row runs fastest, as in the terms' rows
+  const int mr = threadIdx.x % 16, q = threadIdx.x / 16;
+  const long long m = m0 + mr;
   if (m >= j.M || q0 + q >= P.cols) return;
   float v = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) v += red[w][row][q];
-  j.out1[(j.map1 ? (long long)j.map1[m] : m) * j.ld1 + q0 + q] = v;
-  j.out2[m * j.ld2 + q0 + q] = __float2bfloat16_rn(P.s2 * v);
+  for (int w = 0; w < kRowWarps; ++w) v += red[w][mr][q];
+  j.out[row(m, true, j.map_out) * j.ldo + q0 + q] = __float2bfloat16_rn(P.s * v);
+  __nv_bfloat16* o = j.terms + (q0 + q) * j.ldt + row(m, true, j.map_terms);
+#pragma unroll
+  for (int k = 0; k < kTerms; ++k) {
+    const __nv_bfloat16 h = __float2bfloat16_rn(v);
+    v -= __bfloat162float(h);
+    o[(long long)k * P.cp * j.ldt] = h;
+  }
 }
 
 // ------------------------------------------------------------------- sums
 constexpr int kCh = 128;            // channels of a block (M)
 constexpr int kTok = 64;            // tokens of a stage
-constexpr int kTerms = 3;           // bf16 terms of an fp32 rank operand
 constexpr int kAcc = 4;             // accumulators the stages take turns on
 constexpr int kTile = kCh * kCols;  // outputs of a block
-constexpr int kFetch = 3;           // stages on their way beside the current one (bf16: 2)
-constexpr int kABytes = kTok * kCh * 2;              // 16 KB: two 64-channel halves
-constexpr int kBBytes = kTerms * kCols * kTok * 2;   // 6 KB
-constexpr int kPBytes = kTok * kCols * 4;            // 4 KB: raw P rows
-constexpr int kXBytes = kTok * kCh;                  // 8 KB: raw codes
-// Operand slots: bf16 rows arrive in them, codes are expanded into them.
-constexpr int kSlotsB16 = 4, kSlots8 = 2;
-constexpr int kSumSmem = 1024 + kSlotsB16 * (kABytes + kBBytes) + (kFetch + 1) * kPBytes;  // 105 KB
-static_assert(kSlots8 * (kABytes + kBBytes) + (kFetch + 1) * kXBytes <= kSlotsB16 * (kABytes + kBBytes),
+constexpr int kRing = 4;            // stages in flight
+constexpr int kSlots8 = 2;          // operand slots that codes are expanded into
+constexpr int kXWarps = 8;          // warps that expand codes
+constexpr int kSumThreads = kXWarps * 32 + 64;  // and the products' warp, the copies' warp
+constexpr int kABytes = kTok * kCh * 2;             // 16 KB: two 64-channel halves
+constexpr int kBBytes = kTerms * kCols * kTok * 2;  // 6 KB
+constexpr int kXBytes = kTok * kCh;                 // 8 KB of codes
+// bf16: a ring of (X, P) operands; codes: a ring of (codes, P) and the slots.
+constexpr int kSumSmem = 1024 + kRing * (kABytes + kBBytes);  // 89 KB
+static_assert(kRing * (kXBytes + kBBytes) + kSlots8 * kABytes <= kRing * (kABytes + kBBytes),
               "codes' layout inside the bf16 layout's memory");
 constexpr int kTmemCols = 256;  // kAcc * 64, of which 48 each are used
 constexpr long long kWaitBudget = 2000000000LL;  // ~1 s of SM clocks per wait
 
-struct SumJob {
-  const uint8_t* X;       // codes, or bf16 values
+struct alignas(64) SumJob {
+  CUtensorMap xmap;       // codes: 128 x 64 boxes; bf16: 64 x 64, 128-byte swizzle
+  CUtensorMap pmap;       // the terms of P^T, 64 tokens x 16 columns, 128-byte swizzle
   const uint8_t* scales;  // null: bf16
-  long long ld;           // elements of a row
+  long long ld8;          // scale bytes of a row
   long long M, K;
-  const float* P;
-  long long ldp;
-  const int32_t* map;
   float* out;
   long long ldo;
   int trans, nsplit, blocks;  // blocks: channel blocks * splits
@@ -153,7 +171,7 @@ struct SumJob {
 };
 struct SumParams {
   SumJob job[kRankSums];
-  int n, cols, tiles;  // tiles: output tiles of one column slice
+  int n, cols, cp, tiles;  // tiles: output tiles of one column slice
   float scale;
   float* part;
   unsigned* counters;
@@ -227,20 +245,17 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool on) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(on ? 16 : 0)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-                 "r"(on ? 4 : 0)
-                 : "memory");
+__device__ __forceinline__ void mbar_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(bytes)
+               : "memory");
 }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* m, uint64_t* bar, int x,
+                                         int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(su32(bar)), "r"(x), "r"(y)
+      : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
@@ -253,9 +268,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "r"(a));
   return v;
-}
-__device__ __forceinline__ void sts16(uint32_t a, __nv_bfloat16 v) {
-  asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(__bfloat16_as_ushort(v)) : "memory");
 }
 // Byte offset of 16-byte unit u (0 .. 15: 8 channels each) of token t in an X
 // slot: two halves of 64 channels, 128-byte rows, unit index XOR row mod 8.
@@ -274,150 +286,24 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, __nv_bfloat162 step) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// The eight producer warps' work on one (channel block, split).
-template <bool kCodes>
-__device__ __forceinline__ bool sum_produce(const SumJob& j, long long ch0, int q0, int cols,
-                                            long long m0, int stages, uint8_t* smem,
-                                            uint64_t* full, uint64_t* empty,
-                                            volatile int* abort, int tid) {
-  constexpr int kSlots = kCodes ? kSlots8 : kSlotsB16;
-  // bf16 rows arrive in their operand slot: one stage fewer, so that a copy
-  // waits for products issued two stages ago
-  constexpr int kAhead = kCodes ? kFetch : kFetch - 1;
-  const uint32_t sA = su32(smem), sB = sA + kSlots * kABytes;
-  const uint32_t sX = sB + kSlots * kBBytes;  // codes
-  const uint32_t sP = sA + kSumSmem - 1024 - (kFetch + 1) * kPBytes;
-  const int lane = tid & 31;
-  // this thread's share of P: token tid / 4, columns q0 + 4 (tid % 4) ...
-  const int pt = tid >> 2, pq = 4 * (tid & 3);
-  const bool vec = q0 + kCols <= cols && j.ldp % 4 == 0;
-  auto row_of = [&](int st) -> long long {  // its row of P in stage st, or -1
-    const long long m = m0 + (long long)st * kTok + pt;
-    if (st >= stages || m >= j.M) return -1;
-    return j.map ? (long long)j.map[m] : m;
-  };
-  auto slot_free = [&](int st) {  // the products of the slot's last stage are done
-    return st < kSlots || mbar_wait(&empty[st % kSlots], uint32_t(st / kSlots - 1) & 1u, abort);
-  };
-  auto fetch = [&](int st, long long prow) {
-    if (st < stages) {
-      const long long mb = m0 + (long long)st * kTok;
-      if constexpr (kCodes) {
-        const uint32_t dst = sX + (st % (kFetch + 1)) * kXBytes + tid * 16;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int id = tid + 256 * i, t = id >> 3;
-          const long long ch = ch0 + 16 * (id & 7);
-          const bool on = mb + t < j.M && ch < j.ld;
-          cp_async<16>(dst + 4096 * i, j.X + (on ? (mb + t) * j.ld + ch : 0), on);
-        }
-      } else {
-        const uint32_t dst = sA + (st % kSlots) * kABytes;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int id = tid + 256 * i, t = id >> 4, u = id & 15;
-          const long long ch = ch0 + 8 * u;
-          const bool on = mb + t < j.M && ch < j.ld;
-          cp_async<16>(dst + x_at(t, u), j.X + (on ? ((mb + t) * j.ld + ch) * 2 : 0), on);
-        }
-      }
-      const uint32_t dp = sP + (st % (kFetch + 1)) * kPBytes + tid * 16;
-      const float* src = j.P + (prow >= 0 ? prow * j.ldp + q0 + pq : 0);
-      if (vec) {
-        cp_async<16>(dp, src, prow >= 0);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool on = prow >= 0 && q0 + pq + e < cols;
-          cp_async<4>(dp + 4 * e, on ? src + e : j.P, on);
-        }
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  // scale bytes of this thread's two code chunks in stage st
-  auto bytes_of = [&](int st, uint32_t (&b)[2]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int id = tid + 256 * i;
-      const long long m = m0 + (long long)st * kTok + (id >> 3), ch = ch0 + 16 * (id & 7);
-      b[i] = st < stages && m < j.M && ch < j.ld ? j.scales[(m * j.ld + ch) >> 5] : 7u;
-    }
-  };
-  uint32_t byte[kAhead][2];
-  long long prow[kAhead + 1];
-#pragma unroll
-  for (int st = 0; st <= kAhead; ++st) prow[st] = row_of(st);
-#pragma unroll
-  for (int st = 0; st < kAhead; ++st) {
-    fetch(st, prow[st]);
-    if constexpr (kCodes) bytes_of(st, byte[st]);
-  }
-  long long next_row = prow[kAhead];
-  bool ok = true;
-  for (int st = 0; st < stages; ++st) {
-    if constexpr (!kCodes) {
-      if (!slot_free(st + kAhead < stages ? st + kAhead : 0)) { ok = false; break; }
-    }
-    fetch(st + kAhead, next_row);
-    next_row = row_of(st + kAhead + 1);
-    uint32_t nb[2] = {7u, 7u};
-    if constexpr (kCodes) bytes_of(st + kAhead, nb);
-    cp_wait<kAhead>();  // stage st of this thread has arrived
-    if constexpr (kCodes) {
-      if (!slot_free(st)) { ok = false; break; }
-      const uint32_t src = sX + (st % (kFetch + 1)) * kXBytes + tid * 16;
-      const uint32_t dst = sA + (st % kSlots) * kABytes;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int id = tid + 256 * i, t = id >> 3, u = 2 * (id & 7);
-        const uint4 w = lds128(src + 4096 * i);
-        const uint32_t b = byte[0][i];
-        const uint32_t e = b == 255u ? 0x7fff7fffu : ((b - 6u) << 7) * 0x10001u;
-        const __nv_bfloat162 step = act8_as_bf162(e);
-        sts128(dst + x_at(t, u), make_uint4(code_pair<0>(w.x, step), code_pair<2>(w.x, step),
-                                            code_pair<0>(w.y, step), code_pair<2>(w.y, step)));
-        sts128(dst + x_at(t, u + 1), make_uint4(code_pair<0>(w.z, step), code_pair<2>(w.z, step),
-                                                code_pair<0>(w.w, step), code_pair<2>(w.w, step)));
-      }
-#pragma unroll
-      for (int f = 0; f + 1 < kAhead; ++f) {
-        byte[f][0] = byte[f + 1][0];
-        byte[f][1] = byte[f + 1][1];
-      }
-      byte[kAhead - 1][0] = nb[0];
-      byte[kAhead - 1][1] = nb[1];
-    }
-    {  // the three terms of this thread's four P values, transposed: row (term, column), token
-      const uint4 w = lds128(sP + (st % (kFetch + 1)) * kPBytes + tid * 16);
-      const uint32_t dst = sB + (st % kSlots) * kBBytes;
-      const float v[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z),
-                          __uint_as_float(w.w)};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float rest = v[e];
-#pragma unroll
-        for (int s = 0; s < kTerms; ++s) {
-          const __nv_bfloat16 h = __float2bfloat16_rn(rest);
-          rest -= __bfloat162float(h);
-          const int row = s * kCols + pq + e;
-          sts16(dst + row * 128 + (((pt >> 3) ^ (row & 7)) << 4) + (pt & 7) * 2, h);
-        }
-      }
-    }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&full[st % kSlots]);
-  }
-  cp_wait<0>();
-  return ok;
+// 16 codes of a token, two 16-byte units of the operand slot (they differ in the
+// lowest bit of the swizzled unit index).
+__device__ __forceinline__ void expand16(uint32_t dst, const uint4& w, uint32_t byte) {
+  const __nv_bfloat162 step =
+      act8_as_bf162(byte == 255u ? 0x7fff7fffu : (byte - 6u) * 0x800080u);
+  sts128(dst, make_uint4(code_pair<0>(w.x, step), code_pair<2>(w.x, step),
+                         code_pair<0>(w.y, step), code_pair<2>(w.y, step)));
+  sts128(dst ^ 16u, make_uint4(code_pair<0>(w.z, step), code_pair<2>(w.z, step),
+                               code_pair<0>(w.w, step), code_pair<2>(w.w, step)));
 }
 
-__global__ void __launch_bounds__(kWarps * 32 + 32, 2) rank_sums_kernel(const __grid_constant__ SumParams P) {
+__global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_constant__ SumParams P) {
   extern __shared__ uint8_t s_raw[];
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[kSlotsB16], empty[kSlotsB16], done;
+  // copied: a ring place's copies have landed; ready: its X operand is complete
+  // (codes); empty: its products are done
+  __shared__ uint64_t copied[kRing], ready[kRing], empty[kRing], done;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ unsigned s_last;
@@ -432,15 +318,16 @@ __global__ void __launch_bounds__(kWarps * 32 + 32, 2) rank_sums_kernel(const __
   const int stages = int(max(0ll, min((long long)j.stages, (j.M - m0 + kTok - 1) / kTok)));
   const bool codes = j.scales != nullptr;
   if (tid == 0) {
-    for (int i = 0; i < kSlotsB16; ++i) {
-      mbar_init(&full[i], kWarps);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&copied[i], 1);
+      mbar_init(&ready[i], kXWarps);
       mbar_init(&empty[i], 1);
     }
     mbar_init(&done, 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kWarps) {
+  if (warp == kXWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      su32(&s_tmem)),
                  "n"(kTmemCols)
@@ -452,27 +339,58 @@ __global__ void __launch_bounds__(kWarps * 32 + 32, 2) rank_sums_kernel(const __
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tbase = s_tmem;
   volatile int* abort = &s_abort;
+  const uint32_t sB = su32(smem), sX = sB + kRing * kBBytes;  // sX: operands, or codes
+  const uint32_t sA = sX + kRing * kXBytes;                   // codes' operand slots
+  // the products of stage st (which used its ring place and operand slot) are done
+  auto products_done = [&](int st) {
+    return st < 0 || mbar_wait(&empty[st % kRing], uint32_t(st / kRing) & 1u, abort);
+  };
 
-  if (warp < kWarps) {
-    if (codes)
-      sum_produce<true>(j, ch0, q0, P.cols, m0, stages, smem, full, empty, abort, tid);
-    else
-      sum_produce<false>(j, ch0, q0, P.cols, m0, stages, smem, full, empty, abort, tid);
-  } else if (lane == 0) {
-    const int slots = codes ? kSlots8 : kSlotsB16;
-    const uint32_t sA = su32(smem), sB = sA + slots * kABytes;
-    for (int st = 0; st < stages; ++st) {
-      const int slot = st % slots;
-      if (!mbar_wait(&full[slot], uint32_t(st / slots) & 1u, abort)) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t d = tbase + uint32_t(st % kAcc) * 64u;
+  if (warp == kXWarps + 1) {
+    // ------------------------------------------------------------ copies
+    if (lane == 0) {
+      int issued = 0;
+      for (int st = 0; st < stages; ++st, ++issued) {
+        const int place = st % kRing;
+        if (!products_done(st - kRing)) break;
+        const int m = int(m0) + st * kTok;
+        mbar_expect(&copied[place], kBBytes + (codes ? kXBytes : kABytes));
 #pragma unroll
-      for (int k = 0; k < kTok / 16; ++k)
-        mma_1sm(d, sdesc(sA + slot * kABytes + k * 2048, kTok * 128, 1024),
-                sdesc(sB + slot * kBBytes + k * 32, 16, 1024), st >= kAcc || k > 0 ? 1u : 0u);
-      mma_commit(&empty[slot]);
+        for (int s = 0; s < kTerms; ++s)
+          tma_load(sB + place * kBBytes + s * kCols * 128, &j.pmap, &copied[place], m,
+                   s * P.cp + q0);
+        if (codes) {
+          tma_load(sX + place * kXBytes, &j.xmap, &copied[place], int(ch0), m);
+        } else {
+          tma_load(sX + place * kABytes, &j.xmap, &copied[place], int(ch0), m);
+          tma_load(sX + place * kABytes + kTok * 128, &j.xmap, &copied[place], int(ch0) + 64, m);
+        }
+      }
+      // the copies land before the block may leave (normally long since read)
+      for (int st = max(0, issued - kRing); st < issued; ++st) {
+        const long long t0 = clock64();
+        while (!mbar_try(&copied[st % kRing], uint32_t(st / kRing) & 1u) &&
+               clock64() - t0 < kWaitBudget) {
+        }
+      }
     }
-    if (stages > 0) {
+  } else if (warp == kXWarps) {
+    // ---------------------------------------------------------- products
+    if (lane == 0 && stages > 0) {
+      for (int st = 0; st < stages; ++st) {
+        const int place = st % kRing;
+        if (!mbar_wait(&copied[place], uint32_t(st / kRing) & 1u, abort)) break;
+        if (codes && !mbar_wait(&ready[place], uint32_t(st / kRing) & 1u, abort)) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t a = codes ? sA + (st % kSlots8) * kABytes : sX + place * kABytes;
+        const uint32_t b = sB + place * kBBytes;
+        const uint32_t d = tbase + uint32_t(st % kAcc) * 64u;
+#pragma unroll
+        for (int k = 0; k < kTok / 16; ++k)
+          mma_1sm(d, sdesc(a + k * 2048, kTok * 128, 1024), sdesc(b + k * 32, 16, 1024),
+                  st >= kAcc || k > 0 ? 1u : 0u);
+        mma_commit(&empty[place]);
+      }
       mma_commit(&done);
       // nothing of this block may be in flight when it leaves, aborted or not
       const long long t0 = clock64();
@@ -482,6 +400,37 @@ __global__ void __launch_bounds__(kWarps * 32 + 32, 2) rank_sums_kernel(const __
         s_abort = 1;
         atomicExch(&g_rank_error, 1);
       }
+    }
+  } else if (codes) {
+    // --------------------------------------------------------- expansion
+    // this thread: 16 channels (unit tid % 8) of tokens tid / 8 and tid / 8 + 32
+    const int xt = tid >> 3, xu = tid & 7;
+    const long long ch = ch0 + 16 * xu;
+    const bool inside = ch < j.ld8 * kActBlock;  // rows are whole blocks
+    const uint8_t* sc = j.scales + (inside ? (m0 + xt) * j.ld8 + (ch >> 5) : 0);
+    const int rows = int(min((long long)stages * kTok, j.M - m0));
+    auto byte_of = [&](int at) -> uint32_t {  // of the split's token xt + at
+      return inside && at + xt < rows ? sc[at * j.ld8] : 7u;
+    };
+    const uint32_t d0 = x_at(xt, 2 * xu), d1 = x_at(xt + 32, 2 * xu);
+    uint32_t b0[2] = {byte_of(0), byte_of(kTok)}, b1[2] = {byte_of(32), byte_of(kTok + 32)};
+    for (int st = 0; st < stages; ++st) {
+      const int place = st % kRing;
+      const uint32_t n0 = byte_of((st + 2) * kTok), n1 = byte_of((st + 2) * kTok + 32);
+      if (!mbar_wait(&copied[place], uint32_t(st / kRing) & 1u, abort)) break;
+      const uint4 w0 = lds128(sX + place * kXBytes + tid * 16);
+      const uint4 w1 = lds128(sX + place * kXBytes + tid * 16 + 4096);
+      if (!products_done(st - kSlots8)) break;
+      const uint32_t dst = sA + (st % kSlots8) * kABytes;
+      expand16(dst + d0, w0, b0[0]);
+      expand16(dst + d1, w1, b1[0]);
+      b0[0] = b0[1];
+      b1[0] = b1[1];
+      b0[1] = n0;
+      b1[1] = n1;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ready[place]);
     }
   }
   __syncthreads();
@@ -520,7 +469,7 @@ __global__ void __launch_bounds__(kWarps * 32 + 32, 2) rank_sums_kernel(const __
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (warp == kWarps) {
+  if (warp == kXWarps) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase),
                  "n"(kTmemCols)
@@ -558,52 +507,104 @@ __global__ void __launch_bounds__(kWarps * 32 + 32, 2) rank_sums_kernel(const __
 
 int slices(int cols) { return (cols + kCols - 1) / kCols; }
 int64_t channel_blocks(const RankSum& j) { return (j.K + kCh - 1) / kCh; }
-// Splits of each job over the tokens: two blocks an SM over the launch, shared
-// in proportion to the jobs' sizes, none without a stage, at most 32 (the last
-// block of a tile adds them).
+// Splits of each job over the tokens: the fewest stages a block for which the
+// launch is one wave of two blocks an SM (a second wave would double it), at
+// most 32 splits (the last block of a tile adds them).
 void plan_splits(const RankSum* jobs, int n, int cols, int* nsplit, int* per) {
-  double total = 0.0;
-  for (int i = 0; i < n; ++i) total += double(jobs[i].M) * double(jobs[i].K);
+  int64_t stages[kRankSums], nch[kRankSums], most = 1;
   for (int i = 0; i < n; ++i) {
-    const int64_t nch = std::max<int64_t>(channel_blocks(jobs[i]), 1);
-    const int64_t stages = std::max<int64_t>((jobs[i].M + kTok - 1) / kTok, 1);
-    const double share = total > 0.0 ? double(jobs[i].M) * double(jobs[i].K) / total : 0.0;
-    int64_t want = int64_t(2.0 * num_sms() * share / double(nch * slices(cols)) + 0.5);
-    want = std::max<int64_t>(1, std::min<int64_t>({want, stages, 32}));
-    const int64_t each = (stages + want - 1) / want;
-    nsplit[i] = int((stages + each - 1) / each);
-    per[i] = int(each);
+    stages[i] = std::max<int64_t>((jobs[i].M + kTok - 1) / kTok, 1);
+    nch[i] = channel_blocks(jobs[i]) * slices(cols);
+    most = std::max(most, stages[i]);
+  }
+  auto splits = [&](int i, int64_t each) { return (stages[i] + each - 1) / each; };
+  auto fits = [&](int64_t each) {
+    int64_t blocks = 0;
+    for (int i = 0; i < n; ++i) {
+      if (splits(i, each) > 32) return false;
+      blocks += nch[i] * splits(i, each);
+    }
+    return blocks <= 2 * num_sms();
+  };
+  int64_t lo = 1, hi = most;  // `most` is one split each: taken even where it does not fit
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (fits(mid)) hi = mid;
+    else lo = mid + 1;
+  }
+  for (int i = 0; i < n; ++i) {
+    const int64_t k = std::min<int64_t>(splits(i, lo), 32);
+    per[i] = int((stages[i] + k - 1) / k);
+    nsplit[i] = int((stages[i] + per[i] - 1) / per[i]);
   }
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+
+// 2-D tensor map with zero fill outside [rows x cols].
+slora_status encode(CUtensorMap* m, CUtensorMapDataType type, int es, const void* ptr,
+                    int64_t rows, int64_t cols, int64_t ld, int box_x, int box_y,
+                    CUtensorMapSwizzle swz) {
+  std::call_once(g_encode_once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  if (!g_encode) SLORA_FAIL(SLORA_ERR_CUDA, "cuTensorMapEncodeTiled entry point not available");
+  cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+  cuuint64_t strides[1] = {cuuint64_t(ld) * es};
+  cuuint32_t box[2] = {cuuint32_t(box_x), cuuint32_t(box_y)}, one[2] = {1, 1};
+  const CUresult r = g_encode(m, type, 2, const_cast<void*>(ptr), dims, strides, box, one,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    SLORA_FAIL(SLORA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) rows=%lld cols=%lld ld=%lld",
+               int(r), (long long)rows, (long long)cols, (long long)ld);
+  return SLORA_OK;
+}
+
+int64_t padded_cols(int cols) { return int64_t(slices(cols)) * kCols; }
+
 }  // namespace
 
-slora_status rank_rows(const RankRows* jobs, int n, int cols, float s2, cudaStream_t st) {
+int64_t rank_terms_ld(int64_t M) { return (std::max<int64_t>(M, 1) + 63) / 64 * 64; }
+int64_t rank_terms_elems(int64_t M, int cols) {
+  return kTerms * padded_cols(cols) * rank_terms_ld(M);
+}
+
+slora_status rank_rows(const RankRows* jobs, int n, int cols, float s, cudaStream_t st) {
   if (n < 1 || n > 2) SLORA_FAIL(SLORA_ERR_SHAPE, "rank_rows: %d jobs", n);
   RowsParams p{};
   int64_t blocks[2] = {0, 0};
   double bytes = 0.0;
   for (int i = 0; i < n; ++i) {
-    const RankRows& s = jobs[i];
+    const RankRows& r = jobs[i];
     RowsJob& j = p.job[i];
-    j.Y = static_cast<const __nv_bfloat16*>(s.Y);
-    j.R = static_cast<const __nv_bfloat16*>(s.R);
-    j.ld = s.ld; j.M = s.M; j.K = s.K;
-    j.K64 = (std::max<int64_t>(s.K, 1) + 63) / 64 * 64;
-    j.out1 = s.out1; j.ld1 = s.ld1; j.map1 = s.map1;
-    j.out2 = static_cast<__nv_bfloat16*>(s.out2); j.ld2 = s.ld2;
-    blocks[i] = (s.M + 15) / 16;
-    bytes += double(s.M) * s.K * 2;
-    if (s.M > 0 && s.K > 0 && (!aligned16(s.Y) || s.ld % 8))
+    j.Y = static_cast<const __nv_bfloat16*>(r.Y);
+    j.R = static_cast<const __nv_bfloat16*>(r.R);
+    j.ld = r.ld; j.M = r.M; j.K = r.K;
+    j.K64 = (std::max<int64_t>(r.K, 1) + 63) / 64 * 64;
+    j.map = r.map; j.map_y = r.map_y; j.map_terms = r.map_terms; j.map_out = r.map_out;
+    j.terms = static_cast<__nv_bfloat16*>(r.terms); j.ldt = r.ldt;
+    j.out = static_cast<__nv_bfloat16*>(r.out); j.ldo = r.ldo;
+    blocks[i] = (r.M + 15) / 16;
+    bytes += double(r.M) * r.K * 2;
+    if (r.M > 0 && r.K > 0 && (!aligned16(r.Y) || r.ld % 8))
       SLORA_FAIL(SLORA_ERR_ALIGN, "rank_rows: rows are not whole 16-byte units");
   }
   if (blocks[0] + blocks[1] == 0) return SLORA_OK;
   p.blocks0 = int(blocks[0]);
   p.cols = cols;
-  p.s2 = s2;
+  p.cp = int(padded_cols(cols));
+  p.s = s;
   LaunchScope ls(kSkinny, bytes, st);
-  rank_rows_kernel<<<dim3(unsigned(blocks[0] + blocks[1]), unsigned(slices(cols))), kWarps * 32, 0,
-                     st>>>(p);
+  rank_rows_kernel<<<dim3(unsigned(blocks[0] + blocks[1]), unsigned(slices(cols))),
+                     kRowWarps * 32, 0, st>>>(p);
   SLORA_CHECK_LAUNCH();
   return SLORA_OK;
 }
@@ -635,11 +636,7 @@ slora_status rank_sums(const RankSum* jobs, int n, int cols, float scale, float*
     const RankSum& s = jobs[i];
     SumJob& j = p.job[i];
     const bool codes = s.X8.codes != nullptr;
-    j.X = codes ? reinterpret_cast<const uint8_t*>(s.X8.codes) : static_cast<const uint8_t*>(s.X);
-    j.scales = codes ? s.X8.scales : nullptr;
-    j.ld = codes ? act8_cols(s.K) : s.ld;
     j.M = s.M; j.K = s.K;
-    j.P = s.P; j.ldp = s.ldp; j.map = s.map;
     j.out = s.out; j.ldo = s.ldo; j.trans = s.trans;
     j.nsplit = nsplit[i];
     j.stages = per[i];
@@ -648,12 +645,26 @@ slora_status rank_sums(const RankSum* jobs, int n, int cols, float scale, float*
     tiles += channel_blocks(s);
     blocks += j.blocks;
     bytes += double(s.M) * s.K * (codes ? 1.03125 : 2.0);
-    if (!codes && s.M > 0 && s.K > 0 && (!aligned16(s.X) || s.ld % 8))
-      SLORA_FAIL(SLORA_ERR_ALIGN, "rank_sums: rows are not whole 16-byte units");
+    if (s.M <= 0 || s.K <= 0) continue;  // no stage: its outputs are zeros
+    if (codes) {
+      j.scales = s.X8.scales;
+      j.ld8 = act8_cols(s.K) / kActBlock;
+      SLORA_TRY(encode(&j.xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, s.X8.codes, s.M, act8_cols(s.K),
+                       act8_cols(s.K), kCh, kTok, CU_TENSOR_MAP_SWIZZLE_NONE));
+    } else {
+      if (!aligned16(s.X) || s.ld % 8)
+        SLORA_FAIL(SLORA_ERR_ALIGN, "rank_sums: rows are not whole 16-byte units");
+      SLORA_TRY(encode(&j.xmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, s.X, s.M, s.K, s.ld, 64, kTok,
+                       CU_TENSOR_MAP_SWIZZLE_128B));
+    }
+    SLORA_TRY(encode(&j.pmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, s.terms,
+                     kTerms * padded_cols(cols), s.M, rank_terms_ld(s.M), kTok, kCols,
+                     CU_TENSOR_MAP_SWIZZLE_128B));
   }
   if (blocks == 0) return SLORA_OK;
   p.n = n;
   p.cols = cols;
+  p.cp = int(padded_cols(cols));
   p.tiles = int(tiles);
   p.scale = scale;
   p.part = part;
@@ -661,8 +672,7 @@ slora_status rank_sums(const RankSum* jobs, int n, int cols, float scale, float*
   SLORA_CUDA(cudaFuncSetAttribute(rank_sums_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   kSumSmem));
   LaunchScope ls(kSkinny, bytes * slices(cols), st);
-  rank_sums_kernel<<<dim3(unsigned(blocks), unsigned(slices(cols))), kWarps * 32 + 32, kSumSmem,
-                     st>>>(p);
+  rank_sums_kernel<<<dim3(unsigned(blocks), unsigned(slices(cols))), kSumThreads, kSumSmem, st>>>(p);
   SLORA_CHECK_LAUNCH();
   return SLORA_OK;
 }

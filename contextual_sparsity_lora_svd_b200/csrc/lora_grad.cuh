@@ -7,34 +7,39 @@
 
 namespace slora {
 
+// An fp32 rank operand P [M x cols] as rank_sums reads it: three bf16 terms,
+// transposed, [3][cols rounded up to 16][rank_terms_ld(M)] (what prep_r_batch
+// makes of an fp32 operand; columns past M and rows past cols are not read).
+int64_t rank_terms_ld(int64_t M);
+int64_t rank_terms_elems(int64_t M, int cols);
+
 // Rows of a rank projection: p[m, q] = sum over c < K of Y(m, c) R(c, q), q <
 // cols, for m < M.  Y bf16 with 16-byte aligned rows whose columns past K, up
 // to a multiple of 8, are zero; R split by prep_r_batch into one bf16 term.
-// Written to out1 (fp32, row map1 ? map1[m] : m, ld1) and, scaled by s2, to
-// out2 (bf16, row m, ld2).
+// Written as terms (column m) and, scaled by s and in bf16, to out (row m).
+// With map_*, map[m] stands for m: in the row of Y, the terms' column, out's row.
 struct RankRows {
   const void* Y = nullptr;
   int64_t ld = 0, M = 0, K = 0;
   const void* R = nullptr;
-  float* out1 = nullptr;
-  int64_t ld1 = 0;
-  const int32_t* map1 = nullptr;
-  void* out2 = nullptr;
-  int64_t ld2 = 0;
+  const int32_t* map = nullptr;
+  bool map_y = false, map_terms = false, map_out = false;
+  void* terms = nullptr;
+  int64_t ldt = 0;
+  void* out = nullptr;
+  int64_t ldo = 0;
 };
 // Up to two of them in one launch.
-slora_status rank_rows(const RankRows* jobs, int n, int cols, float s2, cudaStream_t st);
+slora_status rank_rows(const RankRows* jobs, int n, int cols, float s, cudaStream_t st);
 
-// Sum over tokens: v[c, q] = scale * sum over m < M of X(m, c) P(map ? map[m] : m, q)
-// for c < K, q < cols, P fp32 [.. x ldp], X bf16 (16-byte aligned rows of ld,
-// a multiple of 8) or a checkpoint.  Written to out[q * ldo + c] (trans) or out[c * ldo + q].
+// Sum over tokens: v[c, q] = scale * sum over m < M of X(m, c) P(m, q) for c < K,
+// q < cols, P given as its terms, X bf16 (16-byte aligned rows of ld, a multiple
+// of 8) or a checkpoint.  Written to out[q * ldo + c] (trans) or out[c * ldo + q].
 struct RankSum {
   const void* X = nullptr;
   slora_act8 X8 = {nullptr, nullptr};  // codes: the checkpoint, else X
   int64_t ld = 0, M = 0, K = 0;
-  const float* P = nullptr;
-  int64_t ldp = 0;
-  const int32_t* map = nullptr;
+  const void* terms = nullptr;
   float* out = nullptr;
   int64_t ldo = 0;
   int trans = 0;
