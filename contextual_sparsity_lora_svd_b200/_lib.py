@@ -10,6 +10,7 @@ computes any part of the method; a missing library raises at import time.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -422,9 +423,11 @@ ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
 ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
 
 
+@functools.lru_cache(maxsize=64)
 def rotary(layout="half", dims=0, base=ROPE_BASE, scaling="none", factor=1.0, orig_len=0, low=0.0,
            high=0.0, mscale=0.0) -> Rotary:
-    """How q and k are rotated (slora_rotary); dims 0: the whole head."""
+    """How q and k are rotated (slora_rotary); dims 0: the whole head.  Equal
+    arguments give the same struct: it is not to be changed."""
     return Rotary(ROTARY_LAYOUTS[layout], ROTARY_SCALINGS[scaling], int(dims), int(orig_len),
                   float(base), float(factor), float(low), float(high), float(mscale))
 
@@ -432,6 +435,8 @@ def rotary(layout="half", dims=0, base=ROPE_BASE, scaling="none", factor=1.0, or
 def _rows(t, what):
     """(address, row stride) of a 2-D tensor whose rows are contiguous."""
     st = t.stride()
+    if len(st) == 2 and st[1] == 1 and st[0] > 1:
+        return t.data_ptr(), st[0]
     n = t.shape
     if len(st) != 2 or (st[1] != 1 and n[1] > 1):
         raise ValueError(f"{what}: a 2-D tensor with contiguous rows is needed")
@@ -444,6 +449,11 @@ def _whole(t, what):
     return t.data_ptr()
 
 
+def _same(t, what, dt):
+    if t.dtype != dt:
+        raise TypeError(f"{what} is {t.dtype}, the rows are {dt}")
+
+
 def qk_rows(heads, X=None, g=None, Y=None, dY=None, dX=None, dg=None, idx=None, X_ctx=None,
             X_out=None, dX_ctx=None, dX_out=None) -> QkRows:
     """The rows of q or k for slora_qk_rotary_fwd / _bwd: dense (X, Y, dX may
@@ -451,44 +461,43 @@ def qk_rows(heads, X=None, g=None, Y=None, dY=None, dX=None, dg=None, idx=None, 
     contiguous).  The struct keeps its tensors alive; a program that calls more
     than once on the same buffers builds it once."""
     r = QkRows(heads)
-    dts = set()
+    first = X if X is not None else Y if Y is not None else dX
+    if first is None:
+        first = next(t for t in (X_ctx, X_out, dX_ctx, dX_out, dY) if t is not None)
+    dt = first.dtype
+    r.dt = _DTYPES.get(dt)
+    if r.dt is None:
+        raise TypeError("the rows are bf16 or fp32 tensors")
     if X is not None:
         r.X, r.ldx = _rows(X, "X")
-        dts.add(X.dtype)
     if Y is not None:
         r.Y, r.ldy = _rows(Y, "Y")
-        dts.add(Y.dtype)
+        _same(Y, "Y", dt)
     if dX is not None:
         r.dX, r.lddx = _rows(dX, "dX")
-        dts.add(dX.dtype)
+        _same(dX, "dX", dt)
     if g is not None:
         r.g = _whole(g, "g")
-        dts.add(g.dtype)
+        _same(g, "g", dt)
     r.gdt = F32
     if dY is not None:
         r.dY, r.lddy = _rows(dY, "dY")
         r.gdt = dtype_code(dY)
+    r.scratch = dg is not None or idx is not None
     if dg is not None:
         r.dg = _whole(dg, "dg")
         if dg.dtype != torch.float32:
             raise TypeError("dg is an fp32 tensor")
-    r.scratch = dg is not None
     if idx is not None:
         if idx.dtype != torch.int32:
             raise TypeError("idx is an int32 tensor")
-        r.scratch = True
         r.n_idx = idx.numel()
         for name, t in (("X_ctx", X_ctx), ("X_out", X_out), ("dX_ctx", dX_ctx), ("dX_out", dX_out)):
             if t is not None:
                 setattr(r, name, _whole(t, name))
-                dts.add(t.dtype)
+                _same(t, name, dt)
         # an empty list is still a list: its address, never read, may be null
         r.idx = _whole(idx, "idx") or r.X_out or r.dX_out or r.Y or r.dY
-    if len(dts) != 1:
-        raise TypeError(f"the rows and the gain have one dtype, not {dts}")
-    r.dt = _DTYPES.get(dts.pop())
-    if r.dt is None:
-        raise TypeError("the rows are bf16 or fp32 tensors")
     r.tensors = (X, g, Y, dY, dX, dg, idx, X_ctx, X_out, dX_ctx, dX_out)
     return r
 
@@ -496,8 +505,15 @@ def qk_rows(heads, X=None, g=None, Y=None, dY=None, dX=None, dg=None, idx=None, 
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
+@functools.lru_cache(maxsize=64)
+def _whole_sequences(batch, seq):
+    """Tokens of `batch` sequences for calls that do not split them."""
+    return make_tokens(batch, seq, [seq] * batch)
+
+
 def _qk(fn, head, batch, seq, head_dim, q, k, rotary_, pos, eps, ctx_len, ws, stream):
-    tok, keep = make_tokens(batch, seq, [seq] * batch if ctx_len is None else ctx_len)
+    tok, keep = (_whole_sequences(batch, seq) if ctx_len is None
+                 else make_tokens(batch, seq, ctx_len))
     if pos is not None and (pos.dtype != torch.int32 or pos.numel() != batch * seq
                             or not pos.is_contiguous()):
         raise TypeError("pos is a contiguous int32 tensor with one position a row")
@@ -551,12 +567,12 @@ def act8_empty(T, d, device="cuda"):
 def act8(codes, scales, T, d) -> Act8:
     """The C struct of a checkpoint of [T x d] activations."""
     nb = (d + ACT8_BLOCK - 1) // ACT8_BLOCK
-    if (codes.dtype != torch.int8 or scales.dtype != torch.uint8 or not codes.is_contiguous()
-            or not scales.is_contiguous() or codes.numel() != T * nb * ACT8_BLOCK
-            or scales.numel() != T * nb):
+    if (codes.dtype is not torch.int8 or scales.dtype is not torch.uint8
+            or codes.numel() != T * nb * ACT8_BLOCK or scales.numel() != T * nb
+            or not codes.is_contiguous() or not scales.is_contiguous()):
         raise ValueError(f"a checkpoint of {T} x {d} activations is contiguous int8 "
                          f"[{T} x {nb * ACT8_BLOCK}] and uint8 [{T} x {nb}]")
-    return Act8(ptr(codes), ptr(scales))
+    return Act8(codes.data_ptr() or None, scales.data_ptr() or None)
 
 
 def _ref(c):

@@ -13,9 +13,10 @@
 // in registers anyway, so no statistic is stored between the two.
 //
 // Angles: f_p / 2 pi is held in units of 2^-64 turn, so pos * f_p modulo one
-// turn is one wrapping 64-bit product, exact at every position, and
-// sin and cos take an argument in [-1, 1) half turns.  A product in fp32 is off
-// by 4e-3 rad at position 100000.
+// turn is one wrapping 64-bit product, exact at every position (a product in
+// fp32 is off by 4e-3 rad at position 100000).  Its top bits give the quadrant,
+// the rest an angle within pi / 4, whose Taylor sums to the 9th and 8th power
+// leave 2e-9 and 3e-8.
 //
 // Bound: memory.  Forward 2 + 2 bytes a channel, backward 2 + 4 + 2 (fp32 dy);
 // the arithmetic is close behind, so it runs on packed pairs of fp32 values
@@ -23,12 +24,14 @@
 // loads at V = 8), so the norm is a few shuffles and every value is read and
 // written once.  A warp owns one row at a time, or a share of its heads where
 // rows are few: it computes the row's hd / 2 sines and cosines once, spread
-// over its lanes, keeps each lane's in registers and walks the heads, loading
-// one head ahead.  Nothing in the loop waits for another warp.
+// over its lanes, keeps each lane's in registers and walks the heads, the next
+// ones on their way to shared memory.  Nothing in the loop waits for another
+// warp.
 //
 // Sliced rows: the inverse channel list lies in shared memory, and a context
-// row's compact channels are staged there with wide loads, gathered from (and
-// in the backward scattered back to) by channel, and stored with wide stores.
+// row's compact channels are copied there ahead of their turn, gathered from
+// (and in the backward scattered back to) by channel, and stored with wide
+// stores.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -65,8 +68,8 @@ struct QkParams {
   const int32_t* pos;
   const int32_t* ctx_off;  // sliced: context rows before sequence b, [batch + 1]
   int T, seq, hd, dims, units, tl;
-  int stage;  // sliced: elements of a warp's staged row (a multiple of 8)
-  float eps, mscale;
+  int stage;  // sliced: bytes of a warp's staged row (a multiple of 16)
+  float eps, mscale, inv_hd;
 };
 
 // Two fp32 values as one operand of the packed instructions.
@@ -216,21 +219,79 @@ __device__ __forceinline__ void members(const Raw<T, V>& ra, const Raw<T, V>& rb
   pack_all<V>(h, hi);
 }
 
-// One head's rows in flight (zeros where this lane has none).
-template <typename T, typename G, int V, bool kBwd>
-struct Item {
-  static constexpr int NU = units_per_lane<V>();
-  Raw<T, V> xa[NU], xb[NU];
-  Raw<G, V> ya[kBwd ? NU : 1], yb[kBwd ? NU : 1];
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+
+// Cosine and sine of pos * turns (2^-64 turn each), times m.
+__device__ __forceinline__ void cos_sin(int pos, unsigned long long turns, float m, float& c,
+                                        float& s) {
+  const int top = int(((unsigned long long)(long long)pos * turns) >> 32);  // 2^-32 turn
+  const unsigned quad = (unsigned(top) + 0x20000000u) >> 30;                // nearest quarter turn
+  const int rest = int(unsigned(top) - (quad << 30));                       // within an eighth
+  const float a = float(rest) * 1.4629180792671596e-9f;                     // 2 pi / 2^32
+  const float z = a * a;
+  float sp = fmaf(z, 2.7557319223985893e-6f, -1.9841269841269841e-4f);  // 1/9!, -1/7!
+  sp = fmaf(z, sp, 8.3333333333333333e-3f);                             // 1/5!
+  sp = fmaf(z, sp, -1.6666666666666667e-1f);                            // -1/3!
+  sp = fmaf(a * z, sp, a);
+  float cp = fmaf(z, 2.4801587301587302e-5f, -1.3888888888888889e-3f);  // 1/8!, -1/6!
+  cp = fmaf(z, cp, 4.1666666666666667e-2f);                             // 1/4!
+  cp = fmaf(z, cp, -0.5f);
+  cp = fmaf(z, cp, 1.0f);
+  c = (quad & 1u) ? sp : cp;
+  s = (quad & 1u) ? cp : sp;
+  c *= ((quad + 1u) & 2u) ? -m : m;
+  s *= (quad & 2u) ? -m : m;
+}
+
+// Rows on their way to shared memory: kAhead items of a warp beside the one
+// that is computed, each lane's own 16-byte pieces (asynchronous copies need
+// 16-byte groups, V = 8; narrower rows load when their turn comes).
+template <bool kBwd, bool kSliced>
+constexpr int ahead() {
+  return kSliced ? 1 : (kBwd ? 2 : 3);
+}
+// 16-byte pieces of one lane and item: x (two groups of 8), then dy.
+template <typename T, typename G, bool kBwd>
+constexpr int pieces() {
+  return int(sizeof(T)) + (kBwd ? int(sizeof(G)) : 0);
+}
+template <typename T, typename G, int V, bool kBwd, bool kSliced>
+constexpr int ring_bytes() {  // of a warp
+  return V == 8 ? (ahead<kBwd, kSliced>() + 1) * pieces<T, G, kBwd>() * 512 : 0;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(on ? 16 : 0)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_but(void) {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Where an item is: this warp's round that starts at head hb of row t.
+struct Place {
+  int u, t, hb, h1;  // h1: the end of the unit's heads
+  int kind;          // sliced: compact context row of row t, or -1 - output row
+  bool first, more;  // first round of its unit; inside the warp's units
 };
 
 template <typename T, typename G, int V, bool kInter, bool kBwd, bool kSliced>
 __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
     qk_rotary_kernel(const __grid_constant__ QkParams P) {
   constexpr int NU = units_per_lane<V>(), NP = packs<V>();
-  // [warps][hd / 2] cosines and sines (the backward's dg at the end), then for
-  // sliced rows the inverse channel list and the warps' staged rows
-  extern __shared__ __align__(16) float2 smem[];
+  constexpr int kAhead = ahead<kBwd, kSliced>();
+  constexpr bool kRing = V == 8;
+  // [warps][hd / 2 cosines, hd / 2 sines] (the backward's dg at the end), the
+  // warps' rings, then for sliced rows the inverse channel list (byte offsets)
+  // and two staged rows a warp
+  extern __shared__ __align__(16) float smem[];
   __shared__ unsigned long long s_turns[kMaxHeadDim / 2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nwarps = blockDim.x >> 5;
   const bool second = int(blockIdx.x) >= P.part[0].blocks;
@@ -238,46 +299,55 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
   const int blk = int(blockIdx.x) - (second ? P.part[0].blocks : 0);
   const int hd = P.hd, dims = P.dims, np = hd / 2, U = P.units, tl = P.tl;
   const int heads = q.heads;
-  float2* tab = smem + warp * np;
+  float* tab = smem + warp * hd;
+  char* rings = reinterpret_cast<char*>(smem + (nwarps * hd + 3) / 4 * 4);  // 16-byte aligned
+  const uint32_t ring = uint32_t(__cvta_generic_to_shared(rings)) +
+                        warp * ring_bytes<T, G, V, kBwd, kSliced>() + lane * 16;
   uint16_t* s_inv = nullptr;
-  T* stage = nullptr;
+  char* stages = nullptr;
+  constexpr unsigned kSkipped = 65535u;  // in s_inv: a channel that is not computed
   if constexpr (kSliced) {
-    s_inv = reinterpret_cast<uint16_t*>(smem + (nwarps * np + 1) / 2 * 2);  // 16-byte aligned
-    stage = reinterpret_cast<T*>(s_inv + (heads * hd + 7) / 8 * 8) + warp * P.stage;
-    for (int i = tid; i < heads * hd; i += blockDim.x) s_inv[i] = uint16_t(q.inv[i]);  // -1: 65535
+    s_inv = reinterpret_cast<uint16_t*>(rings + nwarps * ring_bytes<T, G, V, kBwd, kSliced>());
+    stages = reinterpret_cast<char*>(s_inv + (heads * hd + 7) / 8 * 8) + warp * 2 * P.stage;
+    for (int i = tid; i < heads * hd; i += blockDim.x) {
+      const int at = q.inv[i];
+      s_inv[i] = at < 0 ? uint16_t(kSkipped) : uint16_t(2 * at);
+    }
   }
   for (int p = tid; p < dims / 2; p += blockDim.x) s_turns[p] = P.turns[p];
   __syncthreads();
 
-  // this lane's place: team `team` of the warp, units lt, lt + tl, ...
+  // this lane's place: team `team` of the warp, units lt, lt + tl, ...; group B
+  // lies `apart` channels behind group A
   const int lt = lane % tl, team = lane / tl, tpw = 32 / tl;
-  int offa[NU], offb[NU];
+  int offa[NU], apart[NU];
   bool act[NU];
   f2 glo[NU][NP], ghi[NU][NP];
   const bool norm = q.g != nullptr;
+  const bool reads_x = !kBwd || norm;
 #pragma unroll
   for (int j = 0; j < NU; ++j) {
     const int u = lt + j * tl, p0 = u * V;
     act[j] = u < U;
     if (kInter) {
       offa[j] = 2 * p0;
-      offb[j] = 2 * p0 + V;
+      apart[j] = V;
     } else if (p0 < dims / 2) {
       offa[j] = p0;
-      offb[j] = p0 + dims / 2;
+      apart[j] = dims / 2;
     } else {
-      offa[j] = p0 + dims / 2;            // dims + (p0 - dims / 2)
-      offb[j] = offa[j] + np - dims / 2;  // + half of the unrotated channels
+      offa[j] = p0 + dims / 2;   // dims + (p0 - dims / 2)
+      apart[j] = np - dims / 2;  // half of the unrotated channels
     }
     float a[V], b[V], l[V], h[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) a[i] = b[i] = 1.0f;
     if (norm && act[j]) {
-      const T* g = static_cast<const T*>(q.g);
+      const T* g = static_cast<const T*>(q.g) + offa[j];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        a[i] = to_f(g[offa[j] + i]);
-        b[i] = to_f(g[offb[j] + i]);
+        a[i] = to_f(g[i]);
+        b[i] = to_f(g[apart[j] + i]);
       }
     }
     Pairs<V, kInter>::split(a, b, l, h);
@@ -294,71 +364,98 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
   f2 cs[NU][NP], sn[NU][NP];
   const f2 minus1 = pack2(-1.0f, -1.0f);
 
-  // compact context row of row t, or -1 - its output row
-  auto kind_of = [&](int t) {
-    const int b = t / P.seq, i = t - b * P.seq;
-    const int o0 = P.ctx_off[b], o1 = P.ctx_off[b + 1];
-    return i < o1 - o0 ? o0 + i : -1 - (t - o1);
+  auto x_of = [&](const Place& w, int h) -> const T* {  // a head that is held at full width
+    if constexpr (kSliced)
+      return static_cast<const T*>(q.Xo) + ((long long)(-1 - w.kind) * heads + h) * hd;
+    else
+      return static_cast<const T*>(q.X) + (w.t * q.ldx + h * hd);
   };
-  // the rows of one head that global memory holds at full width
-  auto load = [&](int t, int h, bool valid, int kind, Item<T, G, V, kBwd>& it) {
+  auto y_of = [&](const Place& w, int h) {
+    return static_cast<const G*>(q.dY) + (w.t * q.ldy + h * hd);
+  };
+  auto full_x = [&](const Place& w) { return reads_x && (!kSliced || w.kind < 0); };
+  // this lane's pieces of an item to ring place k (zeros where it has none)
+  auto fetch = [&](const Place& w, int k) {
+    if constexpr (kRing) {
+      const int h = w.hb + team;
+      const bool on = w.more && h < w.h1 && act[0];
+      const uint32_t dst = ring + k * pieces<T, G, kBwd>() * 512;
+      if (w.more && full_x(w)) {
+        const T* x = on ? x_of(w, h) + offa[0] : static_cast<const T*>(kSliced ? q.Xo : q.X);
 #pragma unroll
-    for (int j = 0; j < NU; ++j) {
-      const bool on = valid && act[j];
-      zero(it.xa[j]);
-      zero(it.xb[j]);
-      if (on && (!kBwd || norm) && (!kSliced || kind < 0)) {
-        const T* x = kSliced ? static_cast<const T*>(q.Xo) +
-                                   ((long long)(-1 - kind) * heads + h) * hd
-                             : static_cast<const T*>(q.X) + t * q.ldx + h * hd;
-        ld_vec(x + offa[j], it.xa[j]);
-        ld_vec(x + offb[j], it.xb[j]);
-      }
-      if constexpr (kBwd) {
-        zero(it.ya[j]);
-        zero(it.yb[j]);
-        if (on) {
-          const G* y = static_cast<const G*>(q.dY) + t * q.ldy + h * hd;
-          ld_vec(y + offa[j], it.ya[j]);
-          ld_vec(y + offb[j], it.yb[j]);
+        for (int i = 0; i < int(sizeof(T)) / 2; ++i) {
+          copy16(dst + i * 512, x + (on ? i * (16 / sizeof(T)) : 0), on);
+          copy16(dst + (int(sizeof(T)) / 2 + i) * 512,
+                 x + (on ? apart[0] + i * (16 / sizeof(T)) : 0), on);
         }
       }
+      if constexpr (kBwd) {
+        if (w.more) {
+          const G* y = on ? y_of(w, h) + offa[0] : static_cast<const G*>(q.dY);
+          const uint32_t dy = dst + int(sizeof(T)) * 512;
+#pragma unroll
+          for (int i = 0; i < int(sizeof(G)) / 2; ++i) {
+            copy16(dy + i * 512, y + (on ? i * (16 / sizeof(G)) : 0), on);
+            copy16(dy + (int(sizeof(G)) / 2 + i) * 512,
+                   y + (on ? apart[0] + i * (16 / sizeof(G)) : 0), on);
+          }
+        }
+      }
+    }
+    // one group an item, with the staged row that was asked for before it
+    if constexpr (kRing || kSliced) asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto from_ring = [&](auto& ra, auto& rb, uint32_t src) {
+    constexpr int N = int(sizeof(ra)) / 16;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      reinterpret_cast<uint4*>(ra.v)[i] = lds128(src + i * 512);
+      reinterpret_cast<uint4*>(rb.v)[i] = lds128(src + (N + i) * 512);
     }
   };
   // cosines and sines of a row, from the warp's lanes to each lane's pairs
   auto angles = [&](int pos) {
     __syncwarp();
     for (int p = lane; p < np; p += 32) {
-      float s = 0.0f, c = 1.0f;
-      if (p < dims / 2) {
-        const unsigned long long turn = (unsigned long long)(long long)pos * s_turns[p];
-        // the top 32 bits as a signed fraction: half turns in [-1, 1)
-        sincospif(float(int(turn >> 32)) * 4.656612873077393e-10f, &s, &c);
-        s *= P.mscale;
-        c *= P.mscale;
-      }
-      tab[p] = make_float2(c, s);
+      float c = 1.0f, s = 0.0f;
+      if (p < dims / 2) cos_sin(pos, s_turns[p], P.mscale, c, s);
+      tab[p] = c;
+      tab[np + p] = s;
     }
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
-      const int p0 = (lt + j * tl) * V;
-      float c[V], s[V];
+      const int p0 = act[j] ? (lt + j * tl) * V : 0;  // (a lane without a unit: any values)
+      Raw<float, V> c, s;
+      if constexpr (V == 8) {
+        ld_vec(tab + p0, c);
+        ld_vec(tab + np + p0, s);
+      } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float2 w = act[j] ? tab[p0 + i] : make_float2(1.0f, 0.0f);
-        c[i] = w.x;
-        s[i] = w.y;
+        for (int i = 0; i < V; ++i) {
+          c.v[i] = tab[p0 + i];
+          s.v[i] = tab[np + p0 + i];
+        }
       }
-      pack_all<V>(c, cs[j]);
-      pack_all<V>(s, sn[j]);
+      pack_all<V>(c.v, cs[j]);
+      pack_all<V>(s.v, sn[j]);
     }
   };
-  auto team_sum = [&](float v) {
-    for (int s = tl >> 1; s; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+  auto team_sum = [&](f2 v2) {
+    float a, b;
+    unpack2(v2, a, b);
+    float v = a + b;
+    for (int s = 1; s < tl; s <<= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
     return v;
   };
-  auto store = [&](int t, int h, int kind, int j, const f2 (&lo)[NP], const f2 (&hi)[NP]) {
+  // a context row's channels of one head: their byte offsets in the staged row
+  auto offsets = [&](int h, int j, Raw<uint16_t, V>& ia, Raw<uint16_t, V>& ib) {
+    const uint16_t* inv = s_inv + h * hd + offa[j];
+    ld_vec(inv, ia);
+    ld_vec(inv + apart[j], ib);
+  };
+  auto store = [&](const Place& w, char* stage, int j, const f2 (&lo)[NP], const f2 (&hi)[NP]) {
+    const int h = w.hb + team;
     float l[V], m[V], a[V], b[V];
     unpack_all<V>(lo, l);
     unpack_all<V>(hi, m);
@@ -370,40 +467,55 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
       rb.v[i] = from_f<T>(b[i]);
     }
     if constexpr (kSliced && kBwd) {
-      if (kind >= 0) {  // into the staged row, over this lane's own x
-        const uint16_t* inv = s_inv + h * hd;
+      if (w.kind >= 0) {  // into the staged row, over this lane's own x
+        Raw<uint16_t, V> ia, ib;
+        offsets(h, j, ia, ib);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const int ia = inv[offa[j] + i], ib = inv[offb[j] + i];
-          if (ia != 65535) stage[ia] = ra.v[i];
-          if (ib != 65535) stage[ib] = rb.v[i];
+          if (ia.v[i] != kSkipped) *reinterpret_cast<T*>(stage + ia.v[i]) = ra.v[i];
+          if (ib.v[i] != kSkipped) *reinterpret_cast<T*>(stage + ib.v[i]) = rb.v[i];
         }
         return;
       }
     }
-    T* o = kSliced && kBwd
-               ? static_cast<T*>(q.outo) + ((long long)(-1 - kind) * heads + h) * hd
-               : static_cast<T*>(q.out) + t * q.ldo + h * hd;
-    st_vec(o + offa[j], ra);
-    st_vec(o + offb[j], rb);
+    T* o = (kSliced && kBwd
+                ? static_cast<T*>(q.outo) + ((long long)(-1 - w.kind) * heads + h) * hd
+                : static_cast<T*>(q.out) + (w.t * q.ldo + h * hd)) +
+           offa[j];
+    st_vec(o, ra);
+    st_vec(o + apart[j], rb);
   };
-  auto compute = [&](int t, int h, bool valid, int kind, Item<T, G, V, kBwd>& it) {
+  auto compute = [&](const Place& w, int k, char* stage) {
+    const int h = w.hb + team;
+    const bool valid = h < w.h1;
+    const uint32_t src = ring + k * pieces<T, G, kBwd>() * 512;
     f2 xlo[NU][NP], xhi[NU][NP];
     f2 ss = 0ull;
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
-      if constexpr (kSliced) {
-        if (kind >= 0 && valid && act[j] && (!kBwd || norm)) {
-          const uint16_t* inv = s_inv + h * hd;
+      Raw<T, V> xa, xb;
+      if (kRing && full_x(w)) {
+        from_ring(xa, xb, src);
+      } else {
+        zero(xa);
+        zero(xb);
+        if (valid && act[j] && reads_x) {
+          if (full_x(w)) {
+            const T* x = x_of(w, h) + offa[j];
+            ld_vec(x, xa);
+            ld_vec(x + apart[j], xb);
+          } else if constexpr (kSliced) {
+            Raw<uint16_t, V> ia, ib;
+            offsets(h, j, ia, ib);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const int ia = inv[offa[j] + i], ib = inv[offb[j] + i];
-            if (ia != 65535) it.xa[j].v[i] = stage[ia];
-            if (ib != 65535) it.xb[j].v[i] = stage[ib];
+            for (int i = 0; i < V; ++i) {
+              if (ia.v[i] != kSkipped) xa.v[i] = *reinterpret_cast<const T*>(stage + ia.v[i]);
+              if (ib.v[i] != kSkipped) xb.v[i] = *reinterpret_cast<const T*>(stage + ib.v[i]);
+            }
           }
         }
       }
-      members<T, V, kInter>(it.xa[j], it.xb[j], xlo[j], xhi[j]);
+      members<T, V, kInter>(xa, xb, xlo[j], xhi[j]);
       if (norm) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
@@ -413,11 +525,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
       }
     }
     float rs = 1.0f;
-    if (norm) {
-      float a, b;
-      unpack2(ss, a, b);
-      rs = rsqrtf(team_sum(a + b) / float(hd) + P.eps);
-    }
+    if (norm) rs = rsqrtf(fmaf(team_sum(ss), P.inv_hd, P.eps));
     const f2 rs2 = pack2(rs, rs);
     if constexpr (!kBwd) {
 #pragma unroll
@@ -433,15 +541,27 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
           lo[i] = fma2(mul2(m, sn[j][i]), minus1, mul2(l, cs[j][i]));
           hi[i] = fma2(m, cs[j][i], mul2(l, sn[j][i]));
         }
-        if (valid && act[j]) store(t, h, kind, j, lo, hi);
+        if (valid && act[j]) store(w, stage, j, lo, hi);
       }
     } else {
       f2 dlo[NU][NP], dhi[NU][NP];  // dn = R^T dy, then g dn
       f2 dot = 0ull;                // sum of x g dn
 #pragma unroll
       for (int j = 0; j < NU; ++j) {
+        Raw<G, V> ya, yb;
+        if constexpr (kRing) {
+          from_ring(ya, yb, src + int(sizeof(T)) * 512);
+        } else {
+          zero(ya);
+          zero(yb);
+          if (valid && act[j]) {
+            const G* y = y_of(w, h) + offa[j];
+            ld_vec(y, ya);
+            ld_vec(y + apart[j], yb);
+          }
+        }
         f2 ylo[NP], yhi[NP];
-        members<G, V, kInter>(it.ya[j], it.yb[j], ylo, yhi);
+        members<G, V, kInter>(ya, yb, ylo, yhi);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           f2 l = fma2(yhi[i], sn[j][i], mul2(ylo[i], cs[j][i]));
@@ -459,9 +579,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
         }
       }
       if (norm) {
-        float a, b;
-        unpack2(dot, a, b);
-        const float coef = -(rs * rs * rs) * (team_sum(a + b) / float(hd));
+        const float coef = -(rs * rs * rs) * (team_sum(dot) * P.inv_hd);
         const f2 coef2 = pack2(coef, coef);
 #pragma unroll
         for (int j = 0; j < NU; ++j)
@@ -473,84 +591,101 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
       }
 #pragma unroll
       for (int j = 0; j < NU; ++j)
-        if (valid && act[j]) store(t, h, kind, j, dlo[j], dhi[j]);
+        if (valid && act[j]) store(w, stage, j, dlo[j], dhi[j]);
     }
   };
-  // a context row's compact channels to the stage, and back from it
-  auto stage_in = [&](int kind) {
-    const T* x = static_cast<const T*>(q.Xc) + (long long)kind * q.n_idx;
-    __syncwarp();
-    if (q.n_idx % 8 == 0) {
-      for (int i = lane * 8; i < q.n_idx; i += 256)
-        *reinterpret_cast<uint4*>(stage + i) = *reinterpret_cast<const uint4*>(x + i);
-    } else {
-      for (int i = lane; i < q.n_idx; i += 32) stage[i] = x[i];
-    }
-    __syncwarp();
-  };
-  auto stage_out = [&](int kind) {
-    T* x = static_cast<T*>(q.outc) + (long long)kind * q.n_idx;
-    __syncwarp();
-    if (q.n_idx % 8 == 0) {
-      for (int i = lane * 8; i < q.n_idx; i += 256)
-        *reinterpret_cast<uint4*>(x + i) = *reinterpret_cast<const uint4*>(stage + i);
-    } else {
-      for (int i = lane; i < q.n_idx; i += 32) x[i] = stage[i];
-    }
-    __syncwarp();
-  };
-  auto position = [&](int t) { return P.pos ? P.pos[t] : t % P.seq; };
 
   // unit u: share u % chunks of row u / chunks
   const int units = P.T * q.chunks, stride = q.blocks * nwarps;
-  int u = blk * nwarps + warp;
-  Item<T, G, V, kBwd> cur, nxt;
-  int t = 0, h0 = 0, h1 = 0, pos = 0, kind = -1;
-  if (u < units) {
-    t = u / q.chunks;
-    h0 = (u - t * q.chunks) * q.per_chunk;
-    h1 = min(heads, h0 + q.per_chunk);
-    pos = position(t);
-    if constexpr (kSliced) kind = kind_of(t);
-    load(t, h0 + team, h0 + team < h1, kind, cur);
-  }
-  while (u < units) {  // the same rounds for every lane of a warp
-    const int u2 = u + stride;
-    int t2 = 0, h02 = 0, h12 = 0, pos2 = 0, kind2 = -1;
-    if (u2 < units) {
-      t2 = u2 / q.chunks;
-      h02 = (u2 - t2 * q.chunks) * q.per_chunk;
-      h12 = min(heads, h02 + q.per_chunk);
-      pos2 = position(t2);
-      if constexpr (kSliced) kind2 = kind_of(t2);
-    }
+  auto enter = [&](Place& w) {  // the first round of unit w.u
+    w.more = w.u < units;
+    if (!w.more) return;
+    w.t = w.u / q.chunks;
+    w.hb = (w.u - w.t * q.chunks) * q.per_chunk;
+    w.h1 = min(heads, w.hb + q.per_chunk);
+    w.first = true;
+    w.kind = -1;
     if constexpr (kSliced) {
-      if (kind >= 0 && (!kBwd || norm)) stage_in(kind);
+      const int b = w.t / P.seq, i = w.t - b * P.seq;
+      const int o0 = P.ctx_off[b], o1 = P.ctx_off[b + 1];
+      w.kind = i < o1 - o0 ? o0 + i : -1 - (w.t - o1);
     }
-    angles(pos);
-    for (int hb = h0; hb < h1; hb += tpw) {
-      const int h = hb + team;
-      const bool more = hb + tpw < h1;
-      const int hn = more ? h + tpw : h02 + team;
-      load(more ? t : t2, hn, hn < (more ? h1 : h12), more ? kind : kind2, nxt);
-      compute(t, h, h < h1, kind, cur);
-      cur = nxt;
+  };
+  auto next = [&](Place& w) {
+    if (!w.more) return;
+    w.hb += tpw;
+    w.first = false;
+    if (w.hb < w.h1) return;
+    w.u += stride;
+    enter(w);
+  };
+  // Sliced: the staged row of the unit that `w` enters starts to arrive (its
+  // buffer's last unit is two units back).
+  int side = 0;  // buffer of the next row to arrive
+  auto fetch_row = [&](const Place& w) {
+    if constexpr (kSliced) {
+      if (!w.more || !w.first) return;
+      char* to = stages + side * P.stage;
+      side ^= 1;
+      if (w.kind < 0 || !reads_x) return;
+      const T* from = static_cast<const T*>(q.Xc) + (long long)w.kind * q.n_idx;
+      if (q.n_idx % 8 == 0) {
+        const uint32_t dst = uint32_t(__cvta_generic_to_shared(to));
+        for (int i = lane * 8; i < q.n_idx; i += 256) copy16(dst + 2 * i, from + i, true);
+      } else {
+        for (int i = lane; i < q.n_idx; i += 32) reinterpret_cast<T*>(to)[i] = from[i];
+      }
     }
-    if constexpr (kSliced && kBwd) {
-      if (kind >= 0) stage_out(kind);
+  };
+  auto store_row = [&](const Place& w, const char* stage) {
+    T* to = static_cast<T*>(q.outc) + (long long)w.kind * q.n_idx;
+    __syncwarp();
+    if (q.n_idx % 8 == 0) {
+      for (int i = lane * 8; i < q.n_idx; i += 256)
+        *reinterpret_cast<uint4*>(to + i) = *reinterpret_cast<const uint4*>(stage + 2 * i);
+    } else {
+      for (int i = lane; i < q.n_idx; i += 32) to[i] = reinterpret_cast<const T*>(stage)[i];
     }
-    u = u2;
-    t = t2;
-    h0 = h02;
-    h1 = h12;
-    pos = pos2;
-    kind = kind2;
+    __syncwarp();
+  };
+
+  Place w, f;  // the item that is computed, and the one whose rows are asked for
+  w.u = blk * nwarps + warp;
+  enter(w);
+  f = w;
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    fetch_row(f);
+    fetch(f, k);
+    next(f);
   }
+  int k = 0, kf = kAhead;  // ring places
+  int now = 1;             // sliced: buffer of the unit that is computed (flipped as it starts)
+  while (w.more) {         // the same rounds for every lane of a warp
+    fetch_row(f);
+    fetch(f, kf);
+    next(f);
+    if constexpr (kRing || kSliced) copies_but<kAhead>();
+    if (w.first) {
+      now ^= 1;
+      angles(P.pos ? P.pos[w.t] : w.t % P.seq);  // (its barriers make the staged row visible)
+    }
+    char* stage = stages + now * P.stage;
+    compute(w, k, stage);
+    const Place was = w;
+    next(w);
+    if constexpr (kSliced && kBwd) {
+      if (was.kind >= 0 && (!w.more || w.first)) store_row(was, stage);
+    }
+    k = k == kAhead ? 0 : k + 1;
+    kf = kf == kAhead ? 0 : kf + 1;
+  }
+  copies_but<0>();
 
   if constexpr (kBwd) {
     if (!q.dgp) return;
     // this block's dg: the warp's teams by shuffles, then the warps in order
-    float* red = reinterpret_cast<float*>(smem) + warp * hd;  // over this warp's table
+    float* red = smem + warp * hd;  // over this warp's table
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
@@ -568,14 +703,14 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           red[offa[j] + i] = a[i];
-          red[offb[j] + i] = b[i];
+          red[offa[j] + apart[j] + i] = b[i];
         }
       }
     }
     __syncthreads();
     for (int c = tid; c < hd; c += blockDim.x) {
       float v = 0.0f;
-      for (int w = 0; w < nwarps; ++w) v += reinterpret_cast<const float*>(smem)[w * hd + c];
+      for (int k2 = 0; k2 < nwarps; ++k2) v += smem[k2 * hd + c];
       q.dgp[(long long)blk * hd + c] = v;
     }
   }
@@ -722,24 +857,38 @@ int vector_width(const QkDesc& D, bool backward) {
   return 1;
 }
 
-// Blocks an SM holds at once (registers: launch bounds of the kernel).
-int blocks_per_sm(bool backward) { return backward ? 2 : 3; }
-// Warps of a block and its shared memory: tables, and for sliced rows the
-// inverse channel list and a staged row a warp, within half an SM's memory as
-// long as that leaves a warp.
-void block_shape(const QkDesc& D, bool sliced, Geometry* g, int* stage) {
+constexpr int kUnits = 4;  // units a warp is given at least, where the rows' heads allow
+
+// Warps of a block, its shared memory (tables and rings, and for sliced rows the
+// inverse channel list and two staged rows a warp) and the blocks that an SM
+// holds of them: registers allow 16 warps backward and 24 forward (the kernel's
+// launch bounds), shared memory 220 KB.  Eight warps, or the smaller block that
+// keeps more warps resident.
+struct Shape {
+  int warps = 1, smem = 0, per_sm = 1, stage = 0;
+};
+Shape block_shape(const QkDesc& D, bool backward, bool sliced, int V) {
   int n = 0, ni = 0;
   for (int i = 0; i < D.nparts; ++i) {
     n = std::max(n, D.part[i].heads * D.head_dim);
     ni = std::max(ni, D.part[i].idx ? D.part[i].n_idx : 0);
   }
-  *stage = (ni + 7) / 8 * 8;
-  g->warps = kWarps;
-  for (;; g->warps /= 2) {
-    g->smem = (g->warps * D.head_dim * 4 + 15) / 16 * 16;
-    if (sliced) g->smem += (n + 7) / 8 * 16 + g->warps * *stage * 2;
-    if (!sliced || g->warps == 1 || g->smem <= 100 * 1024) return;
+  const int stage = (ni + 7) / 8 * 16;
+  // a warp's ring: one item more than is on its way, 512 bytes a piece
+  const int piece = dt_size(D.dt) + (backward ? dt_size(D.gdt) : 0);
+  const int ahead = sliced ? 1 : (backward ? 2 : 3);
+  const int ring = V == 8 ? (ahead + 1) * piece * 512 : 0;
+  Shape best;
+  for (int w = kWarps; w >= 1; w /= 2) {
+    Shape s;
+    s.warps = w;
+    s.stage = stage;
+    s.smem = (w * D.head_dim * 4 + 15) / 16 * 16 + w * ring;
+    if (sliced) s.smem += (n + 7) / 8 * 16 + w * 2 * stage;
+    s.per_sm = std::min((backward ? 16 : 24) / w, 220 * 1024 / s.smem);
+    if (w == kWarps || s.warps * s.per_sm > best.warps * best.per_sm) best = s;
   }
+  return best;
 }
 
 }  // namespace
@@ -827,7 +976,9 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
     sliced = sliced || D.part[i].idx;
     any_dg = any_dg || (backward && D.part[i].g && D.part[i].dg);
   }
-  const int max_blocks = num_sms() * blocks_per_sm(backward);
+  const int V = vector_width(D, backward);
+  const Shape shape = block_shape(D, backward, sliced, V);
+  const int max_blocks = num_sms() * std::max(shape.per_sm, 1);
   int32_t* inv[2] = {nullptr, nullptr};
   int32_t* ctx_off = nullptr;
   float* dgp = nullptr;
@@ -848,7 +999,6 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
     SLORA_CHECK_LAUNCH();
   }
 
-  const int V = vector_width(D, backward);
   QkParams P{};
   P.pos = D.pos;
   P.ctx_off = ctx_off;
@@ -858,13 +1008,16 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
   P.dims = D.rot.dims;
   P.eps = D.eps;
   P.mscale = D.rot.mscale;
+  P.inv_hd = 1.0f / float(hd);
   std::copy(D.rot.turns, D.rot.turns + kMaxHeadDim / 2, P.turns);
   P.units = hd / 2 / V;
   const int nu = V == 8 ? 1 : (V == 2 ? 2 : 4);
   P.tl = 1;
   while (P.tl < 32 && P.tl * nu < P.units) P.tl *= 2;
   Geometry g;
-  block_shape(D, sliced, &g, &P.stage);
+  g.warps = shape.warps;
+  g.smem = shape.smem;
+  P.stage = shape.stage;
   int heads = 0;
   for (int i = 0; i < D.nparts; ++i) heads += D.part[i].heads;
   g.grid = 0;
@@ -882,12 +1035,12 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
       q.out = s.Y; q.ldo = s.ldy;
     }
     // blocks in proportion to the heads; a row's heads in as many shares as
-    // give every warp about eight units, down to one round of a warp's teams
+    // give every warp about kUnits units, down to one round of a warp's teams
     // (sliced rows stay whole: their stage is a row)
     const int share = i == 0 ? std::max(1, int(int64_t(max_blocks) * s.heads / heads))
                              : std::max(1, max_blocks - P.part[0].blocks);
     const int rounds = (s.heads + 32 / P.tl - 1) / (32 / P.tl);
-    const int64_t want = int64_t(share) * g.warps * 8;
+    const int64_t want = int64_t(share) * g.warps * kUnits;
     q.chunks = s.idx ? 1 : int(std::min<int64_t>(rounds, (want + D.ti.T - 1) / D.ti.T));
     q.per_chunk = (rounds + q.chunks - 1) / q.chunks * (32 / P.tl);
     q.chunks = (s.heads + q.per_chunk - 1) / q.per_chunk;
