@@ -60,7 +60,7 @@ struct QkPart {
   long long ldy;
   float* dgp;  // [blocks of this part][hd] partial sums of dg, or null
   int heads, blocks;
-  int chunks, per_chunk;  // a row's heads in `chunks` shares of per_chunk
+  int lg_chunks, per_chunk;  // a row's heads in 2^lg_chunks shares of per_chunk
 };
 struct QkParams {
   QkPart part[2];
@@ -70,6 +70,7 @@ struct QkParams {
   int T, seq, hd, dims, units, tl;
   int stage;  // sliced: bytes of a warp's staged row (a multiple of 16)
   float eps, mscale, inv_hd;
+  unsigned seq_mul, seq_shift;  // t / seq = umulhi(t, seq_mul) >> seq_shift for t < 2^31, seq > 1
 };
 
 // Two fp32 values as one operand of the packed instructions.
@@ -204,19 +205,69 @@ __device__ __forceinline__ void zero(Raw<T, V>& r) {
 #pragma unroll
   for (int i = 0; i < V; ++i) r.v[i] = from_f<T>(0.0f);
 }
-// Raw groups of a unit to its packed first and second members.
+// Raw groups of a unit to its packed first and second members, and back.  bf16
+// goes by words: a word of a group is two neighbours of it (half layout) or one
+// pair (interleaved).
 template <typename T, int V, bool kInter>
 __device__ __forceinline__ void members(const Raw<T, V>& ra, const Raw<T, V>& rb,
                                         f2 (&lo)[packs<V>()], f2 (&hi)[packs<V>()]) {
-  float a[V], b[V], l[V], h[V];
+  if constexpr (std::is_same<T, __nv_bfloat16>::value && V > 1) {
+    const uint32_t* wa = reinterpret_cast<const uint32_t*>(ra.v);
+    const uint32_t* wb = reinterpret_cast<const uint32_t*>(rb.v);
+    auto first = [](uint32_t w) { return __uint_as_float(w << 16); };
+    auto last = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    a[i] = to_f(ra.v[i]);
-    b[i] = to_f(rb.v[i]);
+    for (int i = 0; i < V / 2; ++i) {
+      if constexpr (kInter) {
+        const uint32_t w0 = 2 * i < V / 2 ? wa[(2 * i) % (V / 2)] : wb[(2 * i) % (V / 2)];
+        const uint32_t w1 = 2 * i + 1 < V / 2 ? wa[(2 * i + 1) % (V / 2)] : wb[(2 * i + 1) % (V / 2)];
+        lo[i] = pack2(first(w0), first(w1));
+        hi[i] = pack2(last(w0), last(w1));
+      } else {
+        lo[i] = pack2(first(wa[i]), last(wa[i]));
+        hi[i] = pack2(first(wb[i]), last(wb[i]));
+      }
+    }
+  } else {
+    float a[V], b[V], l[V], h[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      a[i] = to_f(ra.v[i]);
+      b[i] = to_f(rb.v[i]);
+    }
+    Pairs<V, kInter>::split(a, b, l, h);
+    pack_all<V>(l, lo);
+    pack_all<V>(h, hi);
   }
-  Pairs<V, kInter>::split(a, b, l, h);
-  pack_all<V>(l, lo);
-  pack_all<V>(h, hi);
+}
+template <typename T, int V, bool kInter>
+__device__ __forceinline__ void groups(const f2 (&lo)[packs<V>()], const f2 (&hi)[packs<V>()],
+                                       Raw<T, V>& ra, Raw<T, V>& rb) {
+  float l[V], m[V];
+  unpack_all<V>(lo, l);
+  unpack_all<V>(hi, m);
+  if constexpr (std::is_same<T, __nv_bfloat16>::value && V > 1) {
+    __nv_bfloat162* wa = reinterpret_cast<__nv_bfloat162*>(ra.v);
+    __nv_bfloat162* wb = reinterpret_cast<__nv_bfloat162*>(rb.v);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      if constexpr (kInter) {
+        wa[i] = __floats2bfloat162_rn(l[i], m[i]);
+        wb[i] = __floats2bfloat162_rn(l[V / 2 + i], m[V / 2 + i]);
+      } else {
+        wa[i] = __floats2bfloat162_rn(l[2 * i], l[2 * i + 1]);
+        wb[i] = __floats2bfloat162_rn(m[2 * i], m[2 * i + 1]);
+      }
+    }
+  } else {
+    float a[V], b[V];
+    Pairs<V, kInter>::join(l, m, a, b);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      ra.v[i] = from_f<T>(a[i]);
+      rb.v[i] = from_f<T>(b[i]);
+    }
+  }
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -275,11 +326,16 @@ __device__ __forceinline__ void copies_but(void) {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Where an item is: this warp's round that starts at head hb of row t.
+// Where a warp is: row t of unit u, `left` rounds of the unit from this one on;
+// this team's head starts at channel e.  x, y, o: the row's elements.
+template <typename T, typename G>
 struct Place {
-  int u, t, hb, h1;  // h1: the end of the unit's heads
-  int kind;          // sliced: compact context row of row t, or -1 - output row
-  bool first, more;  // first round of its unit; inside the warp's units
+  int u, t, e, left;
+  int kind;  // sliced: compact context row of row t, or -1 - output row
+  bool first;
+  const T* x;
+  const G* y;
+  T* o;
 };
 
 template <typename T, typename G, int V, bool kInter, bool kBwd, bool kSliced>
@@ -295,10 +351,10 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
   __shared__ unsigned long long s_turns[kMaxHeadDim / 2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nwarps = blockDim.x >> 5;
   const bool second = int(blockIdx.x) >= P.part[0].blocks;
-  const QkPart& q = P.part[second ? 1 : 0];
+  const QkPart q = second ? P.part[1] : P.part[0];  // (in registers: read in every round)
   const int blk = int(blockIdx.x) - (second ? P.part[0].blocks : 0);
   const int hd = P.hd, dims = P.dims, np = hd / 2, U = P.units, tl = P.tl;
-  const int heads = q.heads;
+  const int heads = q.heads, n = heads * hd;
   float* tab = smem + warp * hd;
   char* rings = reinterpret_cast<char*>(smem + (nwarps * hd + 3) / 4 * 4);  // 16-byte aligned
   const uint32_t ring = uint32_t(__cvta_generic_to_shared(rings)) +
@@ -329,7 +385,9 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
   for (int j = 0; j < NU; ++j) {
     const int u = lt + j * tl, p0 = u * V;
     act[j] = u < U;
-    if (kInter) {
+    if (!act[j]) {
+      offa[j] = apart[j] = 0;
+    } else if (kInter) {
       offa[j] = 2 * p0;
       apart[j] = V;
     } else if (p0 < dims / 2) {
@@ -364,40 +422,33 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
   f2 cs[NU][NP], sn[NU][NP];
   const f2 minus1 = pack2(-1.0f, -1.0f);
 
-  auto x_of = [&](const Place& w, int h) -> const T* {  // a head that is held at full width
-    if constexpr (kSliced)
-      return static_cast<const T*>(q.Xo) + ((long long)(-1 - w.kind) * heads + h) * hd;
-    else
-      return static_cast<const T*>(q.X) + (w.t * q.ldx + h * hd);
-  };
-  auto y_of = [&](const Place& w, int h) {
-    return static_cast<const G*>(q.dY) + (w.t * q.ldy + h * hd);
-  };
-  auto full_x = [&](const Place& w) { return reads_x && (!kSliced || w.kind < 0); };
+  using At = Place<T, G>;
+  auto full_x = [&](const At& w) { return reads_x && (!kSliced || w.kind < 0); };
+  const int units = P.T << q.lg_chunks, stride = q.blocks * nwarps, step = tpw * hd;
   // this lane's pieces of an item to ring place k (zeros where it has none)
-  auto fetch = [&](const Place& w, int k) {
+  auto fetch = [&](const At& w, int k) {
     if constexpr (kRing) {
-      const int h = w.hb + team;
-      const bool on = w.more && h < w.h1 && act[0];
-      const uint32_t dst = ring + k * pieces<T, G, kBwd>() * 512;
-      if (w.more && full_x(w)) {
-        const T* x = on ? x_of(w, h) + offa[0] : static_cast<const T*>(kSliced ? q.Xo : q.X);
+      if (w.u < units) {
+        const bool on = w.e < n && act[0];
+        const int e = min(w.e, n - hd) + offa[0];  // inside the row either way
+        const uint32_t dst = ring + k * pieces<T, G, kBwd>() * 512;
+        if (full_x(w)) {
+          const T* x = w.x + e;
+          const T* x2 = x + apart[0];
 #pragma unroll
-        for (int i = 0; i < int(sizeof(T)) / 2; ++i) {
-          copy16(dst + i * 512, x + (on ? i * (16 / sizeof(T)) : 0), on);
-          copy16(dst + (int(sizeof(T)) / 2 + i) * 512,
-                 x + (on ? apart[0] + i * (16 / sizeof(T)) : 0), on);
+          for (int i = 0; i < int(sizeof(T)) / 2; ++i) {
+            copy16(dst + i * 512, x + i * (16 / sizeof(T)), on);
+            copy16(dst + (int(sizeof(T)) / 2 + i) * 512, x2 + i * (16 / sizeof(T)), on);
+          }
         }
-      }
-      if constexpr (kBwd) {
-        if (w.more) {
-          const G* y = on ? y_of(w, h) + offa[0] : static_cast<const G*>(q.dY);
+        if constexpr (kBwd) {
+          const G* y = w.y + e;
+          const G* y2 = y + apart[0];
           const uint32_t dy = dst + int(sizeof(T)) * 512;
 #pragma unroll
           for (int i = 0; i < int(sizeof(G)) / 2; ++i) {
-            copy16(dy + i * 512, y + (on ? i * (16 / sizeof(G)) : 0), on);
-            copy16(dy + (int(sizeof(G)) / 2 + i) * 512,
-                   y + (on ? apart[0] + i * (16 / sizeof(G)) : 0), on);
+            copy16(dy + i * 512, y + i * (16 / sizeof(G)), on);
+            copy16(dy + (int(sizeof(G)) / 2 + i) * 512, y2 + i * (16 / sizeof(G)), on);
           }
         }
       }
@@ -441,35 +492,41 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
       pack_all<V>(s.v, sn[j]);
     }
   };
-  auto team_sum = [&](f2 v2) {
+  // sums over a team, two at once (v2's and w2's halves added first)
+  auto team_sums = [&](f2 v2, f2 w2, float& v, float& w) {
     float a, b;
     unpack2(v2, a, b);
-    float v = a + b;
-    for (int s = 1; s < tl; s <<= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-    return v;
+    v = a + b;
+    if constexpr (kBwd) {
+      unpack2(w2, a, b);
+      w = a + b;
+    }
+    auto add = [&](int s) {
+      const float x = __shfl_xor_sync(0xffffffffu, v, s);
+      if constexpr (kBwd) w += __shfl_xor_sync(0xffffffffu, w, s);
+      v += x;
+    };
+    if (tl == 8) {  // heads of 128 channels
+      add(1);
+      add(2);
+      add(4);
+    } else {
+      for (int s = 1; s < tl; s <<= 1) add(s);
+    }
   };
   // a context row's channels of one head: their byte offsets in the staged row
-  auto offsets = [&](int h, int j, Raw<uint16_t, V>& ia, Raw<uint16_t, V>& ib) {
-    const uint16_t* inv = s_inv + h * hd + offa[j];
+  auto offsets = [&](int e, int j, Raw<uint16_t, V>& ia, Raw<uint16_t, V>& ib) {
+    const uint16_t* inv = s_inv + e + offa[j];
     ld_vec(inv, ia);
     ld_vec(inv + apart[j], ib);
   };
-  auto store = [&](const Place& w, char* stage, int j, const f2 (&lo)[NP], const f2 (&hi)[NP]) {
-    const int h = w.hb + team;
-    float l[V], m[V], a[V], b[V];
-    unpack_all<V>(lo, l);
-    unpack_all<V>(hi, m);
-    Pairs<V, kInter>::join(l, m, a, b);
+  auto store = [&](const At& w, char* stage, int j, const f2 (&lo)[NP], const f2 (&hi)[NP]) {
     Raw<T, V> ra, rb;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      ra.v[i] = from_f<T>(a[i]);
-      rb.v[i] = from_f<T>(b[i]);
-    }
+    groups<T, V, kInter>(lo, hi, ra, rb);
     if constexpr (kSliced && kBwd) {
       if (w.kind >= 0) {  // into the staged row, over this lane's own x
         Raw<uint16_t, V> ia, ib;
-        offsets(h, j, ia, ib);
+        offsets(w.e, j, ia, ib);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           if (ia.v[i] != kSkipped) *reinterpret_cast<T*>(stage + ia.v[i]) = ra.v[i];
@@ -478,16 +535,12 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
         return;
       }
     }
-    T* o = (kSliced && kBwd
-                ? static_cast<T*>(q.outo) + ((long long)(-1 - w.kind) * heads + h) * hd
-                : static_cast<T*>(q.out) + (w.t * q.ldo + h * hd)) +
-           offa[j];
+    T* o = w.o + (w.e + offa[j]);
     st_vec(o, ra);
     st_vec(o + apart[j], rb);
   };
-  auto compute = [&](const Place& w, int k, char* stage) {
-    const int h = w.hb + team;
-    const bool valid = h < w.h1;
+  auto compute = [&](const At& w, int k, char* stage) {
+    const bool valid = w.e < n;
     const uint32_t src = ring + k * pieces<T, G, kBwd>() * 512;
     f2 xlo[NU][NP], xhi[NU][NP];
     f2 ss = 0ull;
@@ -501,12 +554,12 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
         zero(xb);
         if (valid && act[j] && reads_x) {
           if (full_x(w)) {
-            const T* x = x_of(w, h) + offa[j];
+            const T* x = w.x + (w.e + offa[j]);
             ld_vec(x, xa);
             ld_vec(x + apart[j], xb);
           } else if constexpr (kSliced) {
             Raw<uint16_t, V> ia, ib;
-            offsets(h, j, ia, ib);
+            offsets(w.e, j, ia, ib);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
               if (ia.v[i] != kSkipped) xa.v[i] = *reinterpret_cast<const T*>(stage + ia.v[i]);
@@ -524,10 +577,14 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
         }
       }
     }
-    float rs = 1.0f;
-    if (norm) rs = rsqrtf(fmaf(team_sum(ss), P.inv_hd, P.eps));
-    const f2 rs2 = pack2(rs, rs);
     if constexpr (!kBwd) {
+      f2 rs2 = 0ull;
+      if (norm) {
+        float sum, none;
+        team_sums(ss, 0ull, sum, none);
+        const float rs = rsqrtf(fmaf(sum, P.inv_hd, P.eps));
+        rs2 = pack2(rs, rs);
+      }
 #pragma unroll
       for (int j = 0; j < NU; ++j) {
         f2 lo[NP], hi[NP];
@@ -544,7 +601,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
         if (valid && act[j]) store(w, stage, j, lo, hi);
       }
     } else {
-      f2 dlo[NU][NP], dhi[NU][NP];  // dn = R^T dy, then g dn
+      f2 dlo[NU][NP], dhi[NU][NP];  // dn = R^T dy
       f2 dot = 0ull;                // sum of x g dn
 #pragma unroll
       for (int j = 0; j < NU; ++j) {
@@ -555,7 +612,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
           zero(ya);
           zero(yb);
           if (valid && act[j]) {
-            const G* y = y_of(w, h) + offa[j];
+            const G* y = w.y + (w.e + offa[j]);
             ld_vec(y, ya);
             ld_vec(y + apart[j], yb);
           }
@@ -564,29 +621,29 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
         members<G, V, kInter>(ya, yb, ylo, yhi);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          f2 l = fma2(yhi[i], sn[j][i], mul2(ylo[i], cs[j][i]));
-          f2 m = fma2(mul2(ylo[i], sn[j][i]), minus1, mul2(yhi[i], cs[j][i]));
+          dlo[j][i] = fma2(yhi[i], sn[j][i], mul2(ylo[i], cs[j][i]));
+          dhi[j][i] = fma2(mul2(ylo[i], sn[j][i]), minus1, mul2(yhi[i], cs[j][i]));
           if (norm) {
-            dglo[j][i] = fma2(l, mul2(xlo[j][i], rs2), dglo[j][i]);
-            dghi[j][i] = fma2(m, mul2(xhi[j][i], rs2), dghi[j][i]);
-            l = mul2(l, glo[j][i]);
-            m = mul2(m, ghi[j][i]);
-            dot = fma2(xlo[j][i], l, dot);
-            dot = fma2(xhi[j][i], m, dot);
+            dot = fma2(mul2(xlo[j][i], glo[j][i]), dlo[j][i], dot);
+            dot = fma2(mul2(xhi[j][i], ghi[j][i]), dhi[j][i], dot);
           }
-          dlo[j][i] = l;
-          dhi[j][i] = m;
         }
       }
       if (norm) {
-        const float coef = -(rs * rs * rs) * (team_sum(dot) * P.inv_hd);
-        const f2 coef2 = pack2(coef, coef);
+        float sum, proj;
+        team_sums(ss, dot, sum, proj);
+        const float rs = rsqrtf(fmaf(sum, P.inv_hd, P.eps));
+        const float coef = -(rs * rs) * (proj * P.inv_hd);  // of x r
+        const f2 rs2 = pack2(rs, rs), coef2 = pack2(coef, coef);
 #pragma unroll
         for (int j = 0; j < NU; ++j)
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
-            dlo[j][i] = fma2(dlo[j][i], rs2, mul2(xlo[j][i], coef2));
-            dhi[j][i] = fma2(dhi[j][i], rs2, mul2(xhi[j][i], coef2));
+            const f2 xl = mul2(xlo[j][i], rs2), xh = mul2(xhi[j][i], rs2);
+            dglo[j][i] = fma2(dlo[j][i], xl, dglo[j][i]);
+            dghi[j][i] = fma2(dhi[j][i], xh, dghi[j][i]);
+            dlo[j][i] = fma2(mul2(dlo[j][i], glo[j][i]), rs2, mul2(xl, coef2));
+            dhi[j][i] = fma2(mul2(dhi[j][i], ghi[j][i]), rs2, mul2(xh, coef2));
           }
       }
 #pragma unroll
@@ -595,36 +652,43 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
     }
   };
 
-  // unit u: share u % chunks of row u / chunks
-  const int units = P.T * q.chunks, stride = q.blocks * nwarps;
-  auto enter = [&](Place& w) {  // the first round of unit w.u
-    w.more = w.u < units;
-    if (!w.more) return;
-    w.t = w.u / q.chunks;
-    w.hb = (w.u - w.t * q.chunks) * q.per_chunk;
-    w.h1 = min(heads, w.hb + q.per_chunk);
+  auto sequence_of = [&](int t) {
+    return P.seq == 1 ? t : int(__umulhi(unsigned(t), P.seq_mul) >> P.seq_shift);
+  };
+  // unit u: share u % chunks of row u / chunks (a power of two of them)
+  auto enter = [&](At& w, bool in, bool out) {  // the first round of unit w.u
+    if (w.u >= units) return;
+    w.t = w.u >> q.lg_chunks;
+    const int h0 = (w.u & ((1 << q.lg_chunks) - 1)) * q.per_chunk;
+    w.e = (h0 + team) * hd;
+    w.left = (min(heads - h0, q.per_chunk) + tpw - 1) / tpw;
     w.first = true;
-    w.kind = -1;
     if constexpr (kSliced) {
-      const int b = w.t / P.seq, i = w.t - b * P.seq;
+      const int b = sequence_of(w.t), i = w.t - b * P.seq;
       const int o0 = P.ctx_off[b], o1 = P.ctx_off[b + 1];
       w.kind = i < o1 - o0 ? o0 + i : -1 - (w.t - o1);
+      const long long full = w.kind < 0 ? (long long)(-1 - w.kind) * n : 0;
+      w.x = static_cast<const T*>(q.Xo) + full;
+      w.o = kBwd ? static_cast<T*>(q.outo) + full : static_cast<T*>(q.out) + w.t * q.ldo;
+    } else {
+      if (in) w.x = static_cast<const T*>(q.X) + w.t * q.ldx;
+      if (out) w.o = static_cast<T*>(q.out) + w.t * q.ldo;
     }
+    if (kBwd && in) w.y = static_cast<const G*>(q.dY) + w.t * q.ldy;
   };
-  auto next = [&](Place& w) {
-    if (!w.more) return;
-    w.hb += tpw;
+  auto next = [&](At& w, bool in, bool out) {
     w.first = false;
-    if (w.hb < w.h1) return;
+    w.e += step;
+    if (--w.left > 0) return;
     w.u += stride;
-    enter(w);
+    enter(w, in, out);
   };
   // Sliced: the staged row of the unit that `w` enters starts to arrive (its
   // buffer's last unit is two units back).
   int side = 0;  // buffer of the next row to arrive
-  auto fetch_row = [&](const Place& w) {
+  auto fetch_row = [&](const At& w) {
     if constexpr (kSliced) {
-      if (!w.more || !w.first) return;
+      if (w.u >= units || !w.first) return;
       char* to = stages + side * P.stage;
       side ^= 1;
       if (w.kind < 0 || !reads_x) return;
@@ -637,7 +701,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
       }
     }
   };
-  auto store_row = [&](const Place& w, const char* stage) {
+  auto store_row = [&](const At& w, const char* stage) {
     T* to = static_cast<T*>(q.outc) + (long long)w.kind * q.n_idx;
     __syncwarp();
     if (q.n_idx % 8 == 0) {
@@ -649,36 +713,44 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
     __syncwarp();
   };
 
-  Place w, f;  // the item that is computed, and the one whose rows are asked for
-  w.u = blk * nwarps + warp;
-  enter(w);
-  f = w;
+  // w: the item that is computed; f: the one whose rows are asked for (rows that
+  // are not copied ahead are w's own)
+  constexpr bool kIn = !kRing;
+  At w, f;
+  w.u = f.u = blk * nwarps + warp;
+  w.kind = f.kind = -1;
+  w.left = f.left = 0;
+  enter(w, kIn, true);
+  enter(f, true, false);
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) {
     fetch_row(f);
     fetch(f, k);
-    next(f);
+    if (f.u < units) next(f, true, false);
   }
-  int k = 0, kf = kAhead;  // ring places
-  int now = 1;             // sliced: buffer of the unit that is computed (flipped as it starts)
-  while (w.more) {         // the same rounds for every lane of a warp
-    fetch_row(f);
-    fetch(f, kf);
-    next(f);
-    if constexpr (kRing || kSliced) copies_but<kAhead>();
-    if (w.first) {
-      now ^= 1;
-      angles(P.pos ? P.pos[w.t] : w.t % P.seq);  // (its barriers make the staged row visible)
+  int now = 1;  // sliced: buffer of the unit that is computed (flipped as it starts)
+  while (w.u < units) {  // the same rounds for every lane of a warp
+#pragma unroll
+    for (int k = 0; k <= kAhead; ++k) {  // ring places
+      if (w.u >= units) break;
+      fetch_row(f);
+      fetch(f, (k + kAhead) % (kAhead + 1));
+      if (f.u < units) next(f, true, false);
+      if constexpr (kRing || kSliced) copies_but<kAhead>();
+      if (w.first) {
+        now ^= 1;
+        int pos;
+        if (P.pos) pos = P.pos[w.t];
+        else pos = w.t - sequence_of(w.t) * P.seq;
+        angles(pos);  // (its barriers make the staged row visible)
+      }
+      char* stage = stages + now * P.stage;
+      compute(w, k, stage);
+      if constexpr (kSliced && kBwd) {
+        if (w.kind >= 0 && w.left == 1) store_row(w, stage);
+      }
+      next(w, kIn, true);
     }
-    char* stage = stages + now * P.stage;
-    compute(w, k, stage);
-    const Place was = w;
-    next(w);
-    if constexpr (kSliced && kBwd) {
-      if (was.kind >= 0 && (!w.more || w.first)) store_row(was, stage);
-    }
-    k = k == kAhead ? 0 : k + 1;
-    kf = kf == kAhead ? 0 : kf + 1;
   }
   copies_but<0>();
 
@@ -857,7 +929,7 @@ int vector_width(const QkDesc& D, bool backward) {
   return 1;
 }
 
-constexpr int kUnits = 4;  // units a warp is given at least, where the rows' heads allow
+constexpr double kAngles = 0.6;  // a unit's angles, in rounds (about 150 of 245 instructions)
 
 // Warps of a block, its shared memory (tables and rings, and for sliced rows the
 // inverse channel list and two staged rows a warp) and the blocks that an SM
@@ -1009,6 +1081,12 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
   P.eps = D.eps;
   P.mscale = D.rot.mscale;
   P.inv_hd = 1.0f / float(hd);
+  if (P.seq > 1) {
+    unsigned l = 1;
+    while ((uint64_t(1) << l) < uint64_t(P.seq)) ++l;
+    P.seq_shift = l - 1;
+    P.seq_mul = unsigned(((uint64_t(1) << (31 + l)) + uint64_t(P.seq) - 1) / uint64_t(P.seq));
+  }
   std::copy(D.rot.turns, D.rot.turns + kMaxHeadDim / 2, P.turns);
   P.units = hd / 2 / V;
   const int nu = V == 8 ? 1 : (V == 2 ? 2 : 4);
@@ -1018,8 +1096,13 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
   g.warps = shape.warps;
   g.smem = shape.smem;
   P.stage = shape.stage;
-  int heads = 0;
-  for (int i = 0; i < D.nparts; ++i) heads += D.part[i].heads;
+  auto rounds_of = [&](int i, int lg) {  // of a share of part i's heads in 2^lg shares
+    const int all = (D.part[i].heads + 32 / P.tl - 1) / (32 / P.tl);
+    return (all + (1 << lg) - 1) >> lg;
+  };
+  auto work = [&](int i) { return rounds_of(i, 0) + kAngles; };
+  double total = 0.0;
+  for (int i = 0; i < D.nparts; ++i) total += work(i);
   g.grid = 0;
   double bytes = 0.0;
   const double es = D.dt == kF32 ? 4 : 2, gs = D.gdt == kF32 ? 4 : 2;
@@ -1034,17 +1117,22 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
     } else {
       q.out = s.Y; q.ldo = s.ldy;
     }
-    // blocks in proportion to the heads; a row's heads in as many shares as
-    // give every warp about kUnits units, down to one round of a warp's teams
-    // (sliced rows stay whole: their stage is a row)
-    const int share = i == 0 ? std::max(1, int(int64_t(max_blocks) * s.heads / heads))
+    // blocks in proportion to the parts' work on a row
+    const int share = i == 0 ? std::max(1, int(max_blocks * work(i) / total))
                              : std::max(1, max_blocks - P.part[0].blocks);
-    const int rounds = (s.heads + 32 / P.tl - 1) / (32 / P.tl);
-    const int64_t want = int64_t(share) * g.warps * kUnits;
-    q.chunks = s.idx ? 1 : int(std::min<int64_t>(rounds, (want + D.ti.T - 1) / D.ti.T));
-    q.per_chunk = (rounds + q.chunks - 1) / q.chunks * (32 / P.tl);
-    q.chunks = (s.heads + q.per_chunk - 1) / q.per_chunk;
-    q.blocks = int(std::min<int64_t>(share, (D.ti.T * q.chunks + g.warps - 1) / g.warps));
+    // a row's heads in the number of shares (a power of two, none empty) whose
+    // slowest warp has the least to do: units a warp, times rounds a unit and
+    // the unit's angles (sliced rows stay whole: their stage is a row)
+    const int rounds = rounds_of(i, 0), warps = share * g.warps;
+    auto cost = [&](int lg) {
+      const int64_t units = D.ti.T << lg;
+      return double((units + warps - 1) / warps) * (rounds_of(i, lg) + kAngles);
+    };
+    q.lg_chunks = 0;
+    for (int lg = 1; !s.idx && lg <= 6 && ((1 << lg) - 1) * rounds_of(i, lg) < rounds; ++lg)
+      if (cost(lg) < cost(q.lg_chunks)) q.lg_chunks = lg;
+    q.per_chunk = rounds_of(i, q.lg_chunks) * (32 / P.tl);
+    q.blocks = int(std::min<int64_t>(share, ((D.ti.T << q.lg_chunks) + g.warps - 1) / g.warps));
     if (any_dg && s.g && s.dg) q.dgp = dgp + int64_t(g.grid) * hd;
     g.grid += q.blocks;
     const double n = double(D.ti.T) * s.heads * hd;
