@@ -316,10 +316,18 @@ template <typename T, typename G, int V, bool kBwd, bool kSliced>
 constexpr int ring_bytes() {  // of a warp
   return V == 8 ? (ahead<kBwd, kSliced>() + 1) * pieces<T, G, kBwd>() * 512 : 0;
 }
+// kHalf: half of a 32-byte sector whose other half the lane copies next; through
+// L1, so that the sector is fetched once.
+template <bool kHalf>
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(on ? 16 : 0)
-               : "memory");
+  if constexpr (kHalf)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(on ? 16 : 0)
+                 : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(on ? 16 : 0)
+                 : "memory");
 }
 template <int N>
 __device__ __forceinline__ void copies_but(void) {
@@ -437,8 +445,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
           const T* x2 = x + apart[0];
 #pragma unroll
           for (int i = 0; i < int(sizeof(T)) / 2; ++i) {
-            copy16(dst + i * 512, x + i * (16 / sizeof(T)), on);
-            copy16(dst + (int(sizeof(T)) / 2 + i) * 512, x2 + i * (16 / sizeof(T)), on);
+            copy16<sizeof(T) == 4>(dst + i * 512, x + i * (16 / sizeof(T)), on);
+            copy16<sizeof(T) == 4>(dst + (int(sizeof(T)) / 2 + i) * 512, x2 + i * (16 / sizeof(T)), on);
           }
         }
         if constexpr (kBwd) {
@@ -447,8 +455,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
           const uint32_t dy = dst + int(sizeof(T)) * 512;
 #pragma unroll
           for (int i = 0; i < int(sizeof(G)) / 2; ++i) {
-            copy16(dy + i * 512, y + i * (16 / sizeof(G)), on);
-            copy16(dy + (int(sizeof(G)) / 2 + i) * 512, y2 + i * (16 / sizeof(G)), on);
+            copy16<sizeof(G) == 4>(dy + i * 512, y + i * (16 / sizeof(G)), on);
+            copy16<sizeof(G) == 4>(dy + (int(sizeof(G)) / 2 + i) * 512, y2 + i * (16 / sizeof(G)), on);
           }
         }
       }
@@ -695,7 +703,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
       const T* from = static_cast<const T*>(q.Xc) + (long long)w.kind * q.n_idx;
       if (q.n_idx % 8 == 0) {
         const uint32_t dst = uint32_t(__cvta_generic_to_shared(to));
-        for (int i = lane * 8; i < q.n_idx; i += 256) copy16(dst + 2 * i, from + i, true);
+        for (int i = lane * 8; i < q.n_idx; i += 256) copy16<false>(dst + 2 * i, from + i, true);
       } else {
         for (int i = lane; i < q.n_idx; i += 32) reinterpret_cast<T*>(to)[i] = from[i];
       }
