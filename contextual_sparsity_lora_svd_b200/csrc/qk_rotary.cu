@@ -68,7 +68,7 @@ struct QkParams {
   const int32_t* pos;
   const int32_t* ctx_off;  // sliced: context rows before sequence b, [batch + 1]
   int T, seq, hd, dims, units, tl;
-  int stage;  // sliced: bytes of a warp's staged row (a multiple of 16)
+  int stage;  // sliced: elements of a warp's staged row, a multiple of 8; the last 8 stay zero
   float eps, mscale, inv_hd;
   unsigned seq_mul, seq_shift;  // t / seq = umulhi(t, seq_mul) >> seq_shift for t < 2^31, seq > 1
 };
@@ -353,8 +353,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
   constexpr int kAhead = ahead<kBwd, kSliced>();
   constexpr bool kRing = V == 8;
   // [warps][hd / 2 cosines, hd / 2 sines] (the backward's dg at the end), the
-  // warps' rings, then for sliced rows the inverse channel list (byte offsets)
-  // and two staged rows a warp
+  // warps' rings, then for sliced rows the inverse channel list (a channel that
+  // is not computed: the staged rows' zero) and two staged rows a warp
   extern __shared__ __align__(16) float smem[];
   __shared__ unsigned long long s_turns[kMaxHeadDim / 2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nwarps = blockDim.x >> 5;
@@ -368,15 +368,16 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
   const uint32_t ring = uint32_t(__cvta_generic_to_shared(rings)) +
                         warp * ring_bytes<T, G, V, kBwd, kSliced>() + lane * 16;
   uint16_t* s_inv = nullptr;
-  char* stages = nullptr;
-  constexpr unsigned kSkipped = 65535u;  // in s_inv: a channel that is not computed
+  T* stages = nullptr;
+  const unsigned skipped = P.stage - 8;
   if constexpr (kSliced) {
     s_inv = reinterpret_cast<uint16_t*>(rings + nwarps * ring_bytes<T, G, V, kBwd, kSliced>());
-    stages = reinterpret_cast<char*>(s_inv + (heads * hd + 7) / 8 * 8) + warp * 2 * P.stage;
-    for (int i = tid; i < heads * hd; i += blockDim.x) {
+    stages = reinterpret_cast<T*>(s_inv + (n + 7) / 8 * 8) + warp * 2 * P.stage;
+    for (int i = tid; i < n; i += blockDim.x) {
       const int at = q.inv[i];
-      s_inv[i] = at < 0 ? uint16_t(kSkipped) : uint16_t(2 * at);
+      s_inv[i] = uint16_t(at < 0 ? skipped : unsigned(at));
     }
+    if (lane < 16) stages[(lane >> 3) * P.stage + skipped + (lane & 7)] = from_f<T>(0.0f);
   }
   for (int p = tid; p < dims / 2; p += blockDim.x) s_turns[p] = P.turns[p];
   __syncthreads();
@@ -522,13 +523,13 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
       for (int s = 1; s < tl; s <<= 1) add(s);
     }
   };
-  // a context row's channels of one head: their byte offsets in the staged row
+  // a context row's channels of one head: their places in the staged row
   auto offsets = [&](int e, int j, Raw<uint16_t, V>& ia, Raw<uint16_t, V>& ib) {
     const uint16_t* inv = s_inv + e + offa[j];
     ld_vec(inv, ia);
     ld_vec(inv + apart[j], ib);
   };
-  auto store = [&](const At& w, char* stage, int j, const f2 (&lo)[NP], const f2 (&hi)[NP]) {
+  auto store = [&](const At& w, T* stage, int j, const f2 (&lo)[NP], const f2 (&hi)[NP]) {
     Raw<T, V> ra, rb;
     groups<T, V, kInter>(lo, hi, ra, rb);
     if constexpr (kSliced && kBwd) {
@@ -537,8 +538,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
         offsets(w.e, j, ia, ib);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          if (ia.v[i] != kSkipped) *reinterpret_cast<T*>(stage + ia.v[i]) = ra.v[i];
-          if (ib.v[i] != kSkipped) *reinterpret_cast<T*>(stage + ib.v[i]) = rb.v[i];
+          if (ia.v[i] != skipped) stage[ia.v[i]] = ra.v[i];
+          if (ib.v[i] != skipped) stage[ib.v[i]] = rb.v[i];
         }
         return;
       }
@@ -547,36 +548,49 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
     st_vec(o, ra);
     st_vec(o + apart[j], rb);
   };
-  auto compute = [&](const At& w, int k, char* stage) {
+  auto compute = [&](const At& w, int k, T* stage) {
     const bool valid = w.e < n;
     const uint32_t src = ring + k * pieces<T, G, kBwd>() * 512;
     f2 xlo[NU][NP], xhi[NU][NP];
     f2 ss = 0ull;
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
-      Raw<T, V> xa, xb;
-      if (kRing && full_x(w)) {
-        from_ring(xa, xb, src);
+      if (kSliced && w.kind >= 0) {
+        // gathered from the staged row, its zero where a channel is not computed
+        float a[V], b[V], l[V], h[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) a[i] = b[i] = 0.0f;
+        if (reads_x) {
+          Raw<uint16_t, V> ia, ib;
+          offsets(min(w.e, n - hd), j, ia, ib);  // (a team without a head: the last one's)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            a[i] = to_f(stage[ia.v[i]]);
+            b[i] = to_f(stage[ib.v[i]]);
+          }
+          if (!valid || !act[j]) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) a[i] = b[i] = 0.0f;
+          }
+        }
+        Pairs<V, kInter>::split(a, b, l, h);
+        pack_all<V>(l, xlo[j]);
+        pack_all<V>(h, xhi[j]);
       } else {
-        zero(xa);
-        zero(xb);
-        if (valid && act[j] && reads_x) {
-          if (full_x(w)) {
+        Raw<T, V> xa, xb;
+        if (kRing && reads_x) {
+          from_ring(xa, xb, src);
+        } else {
+          zero(xa);
+          zero(xb);
+          if (valid && act[j] && reads_x) {
             const T* x = w.x + (w.e + offa[j]);
             ld_vec(x, xa);
             ld_vec(x + apart[j], xb);
-          } else if constexpr (kSliced) {
-            Raw<uint16_t, V> ia, ib;
-            offsets(w.e, j, ia, ib);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-              if (ia.v[i] != kSkipped) xa.v[i] = *reinterpret_cast<const T*>(stage + ia.v[i]);
-              if (ib.v[i] != kSkipped) xb.v[i] = *reinterpret_cast<const T*>(stage + ib.v[i]);
-            }
           }
         }
+        members<T, V, kInter>(xa, xb, xlo[j], xhi[j]);
       }
-      members<T, V, kInter>(xa, xb, xlo[j], xhi[j]);
       if (norm) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
@@ -697,7 +711,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
   auto fetch_row = [&](const At& w) {
     if constexpr (kSliced) {
       if (w.u >= units || !w.first) return;
-      char* to = stages + side * P.stage;
+      T* to = stages + side * P.stage;
       side ^= 1;
       if (w.kind < 0 || !reads_x) return;
       const T* from = static_cast<const T*>(q.Xc) + (long long)w.kind * q.n_idx;
@@ -705,18 +719,18 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
         const uint32_t dst = uint32_t(__cvta_generic_to_shared(to));
         for (int i = lane * 8; i < q.n_idx; i += 256) copy16<false>(dst + 2 * i, from + i, true);
       } else {
-        for (int i = lane; i < q.n_idx; i += 32) reinterpret_cast<T*>(to)[i] = from[i];
+        for (int i = lane; i < q.n_idx; i += 32) to[i] = from[i];
       }
     }
   };
-  auto store_row = [&](const At& w, const char* stage) {
+  auto store_row = [&](const At& w, const T* stage) {
     T* to = static_cast<T*>(q.outc) + (long long)w.kind * q.n_idx;
     __syncwarp();
     if (q.n_idx % 8 == 0) {
       for (int i = lane * 8; i < q.n_idx; i += 256)
-        *reinterpret_cast<uint4*>(to + i) = *reinterpret_cast<const uint4*>(stage + 2 * i);
+        *reinterpret_cast<uint4*>(to + i) = *reinterpret_cast<const uint4*>(stage + i);
     } else {
-      for (int i = lane; i < q.n_idx; i += 32) to[i] = reinterpret_cast<const T*>(stage)[i];
+      for (int i = lane; i < q.n_idx; i += 32) to[i] = stage[i];
     }
     __syncwarp();
   };
@@ -752,7 +766,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
         else pos = w.t - sequence_of(w.t) * P.seq;
         angles(pos);  // (its barriers make the staged row visible)
       }
-      char* stage = stages + now * P.stage;
+      T* stage = kSliced ? stages + now * P.stage : nullptr;
       compute(w, k, stage);
       if constexpr (kSliced && kBwd) {
         if (w.kind >= 0 && w.left == 1) store_row(w, stage);
@@ -953,7 +967,7 @@ Shape block_shape(const QkDesc& D, bool backward, bool sliced, int V) {
     n = std::max(n, D.part[i].heads * D.head_dim);
     ni = std::max(ni, D.part[i].idx ? D.part[i].n_idx : 0);
   }
-  const int stage = (ni + 7) / 8 * 16;
+  const int stage = (ni + 7) / 8 * 8 + 8;
   // a warp's ring: one item more than is on its way, 512 bytes a piece
   const int piece = dt_size(D.dt) + (backward ? dt_size(D.gdt) : 0);
   const int ahead = sliced ? 1 : (backward ? 2 : 3);
@@ -964,7 +978,7 @@ Shape block_shape(const QkDesc& D, bool backward, bool sliced, int V) {
     s.warps = w;
     s.stage = stage;
     s.smem = (w * D.head_dim * 4 + 15) / 16 * 16 + w * ring;
-    if (sliced) s.smem += (n + 7) / 8 * 16 + w * 2 * stage;
+    if (sliced) s.smem += (n + 7) / 8 * 16 + w * 2 * stage * 2;
     s.per_sm = std::min((backward ? 16 : 24) / w, 220 * 1024 / s.smem);
     if (w == kWarps || s.warps * s.per_sm > best.warps * best.per_sm) best = s;
   }
