@@ -170,11 +170,11 @@ struct Pairs {
   }
 };
 
-// Units a lane owns: V = 8 covers 256 channels with 16 lanes; narrower
-// vectors need two or four units on 32 lanes.
+// Units a lane owns: V = 8 covers 256 channels with 16 lanes, V = 4 with 32;
+// narrower vectors need two or four units a lane.
 template <int V>
 constexpr int units_per_lane() {
-  return V == 8 ? 1 : (V == 2 ? 2 : 4);
+  return V >= 4 ? 1 : (V == 2 ? 2 : 4);
 }
 // Packed pairs of a unit (V = 1: the second value of the one is zero).
 template <int V>
@@ -270,14 +270,6 @@ __device__ __forceinline__ void groups(const f2 (&lo)[packs<V>()], const f2 (&hi
   }
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
-
 // Cosine and sine of pos * turns (2^-64 turn each), times m.
 __device__ __forceinline__ void cos_sin(int pos, unsigned long long turns, float m, float& c,
                                         float& s) {
@@ -301,33 +293,55 @@ __device__ __forceinline__ void cos_sin(int pos, unsigned long long turns, float
 }
 
 // Rows on their way to shared memory: kAhead items of a warp beside the one
-// that is computed, each lane's own 16-byte pieces (asynchronous copies need
-// 16-byte groups, V = 8; narrower rows load when their turn comes).
+// that is computed, each lane's own pieces of up to 16 bytes (an asynchronous
+// copy has at least 4: V > 1; single channels load when their turn comes).
 template <bool kBwd, bool kSliced>
 constexpr int ahead() {
   return kSliced ? 1 : (kBwd ? 2 : 3);
 }
-// 16-byte pieces of one lane and item: x (two groups of 8), then dy.
-template <typename T, typename G, bool kBwd>
-constexpr int pieces() {
-  return int(sizeof(T)) + (kBwd ? int(sizeof(G)) : 0);
+template <typename T, int V>
+constexpr int piece_bytes() {
+  return V * int(sizeof(T)) < 16 ? V * int(sizeof(T)) : 16;
+}
+template <typename T, int V>
+constexpr int group_pieces() {
+  return V * int(sizeof(T)) / piece_bytes<T, V>();
+}
+// Bytes of x (or dy) of one lane and item, and of a warp's ring.
+template <typename T, int V>
+constexpr int item_bytes() {
+  return 2 * units_per_lane<V>() * V * int(sizeof(T));
 }
 template <typename T, typename G, int V, bool kBwd, bool kSliced>
-constexpr int ring_bytes() {  // of a warp
-  return V == 8 ? (ahead<kBwd, kSliced>() + 1) * pieces<T, G, kBwd>() * 512 : 0;
+constexpr int ring_bytes() {
+  return V == 1 ? 0
+                : (ahead<kBwd, kSliced>() + 1) * 32 *
+                      (item_bytes<T, V>() + (kBwd ? item_bytes<G, V>() : 0));
 }
-// kHalf: half of a 32-byte sector whose other half the lane copies next; through
-// L1, so that the sector is fetched once.
-template <bool kHalf>
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
-  if constexpr (kHalf)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(on ? 16 : 0)
-                 : "memory");
-  else
+// kThrough: part of a 32-byte sector whose other part the lane copies next;
+// through L1, so that the sector is fetched once (as pieces below 16 bytes are).
+template <int BYTES, bool kThrough>
+__device__ __forceinline__ void copy_piece(uint32_t dst, const void* src, bool on) {
+  if constexpr (BYTES == 16 && !kThrough)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(on ? 16 : 0)
                  : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src),
+                 "n"(BYTES), "r"(on ? BYTES : 0)
+                 : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void read_piece(void* to, uint32_t src) {
+  uint32_t* w = static_cast<uint32_t*>(to);
+  if constexpr (BYTES == 16)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(src));
+  else if constexpr (BYTES == 8)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(src));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(src));
 }
 template <int N>
 __device__ __forceinline__ void copies_but(void) {
@@ -351,7 +365,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
     qk_rotary_kernel(const __grid_constant__ QkParams P) {
   constexpr int NU = units_per_lane<V>(), NP = packs<V>();
   constexpr int kAhead = ahead<kBwd, kSliced>();
-  constexpr bool kRing = V == 8;
+  constexpr bool kRing = V > 1;
   // [warps][hd / 2 cosines, hd / 2 sines] (the backward's dg at the end), the
   // warps' rings, then for sliced rows the inverse channel list (a channel that
   // is not computed: the staged rows' zero) and two staged rows a warp
@@ -366,7 +380,9 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
   float* tab = smem + warp * hd;
   char* rings = reinterpret_cast<char*>(smem + (nwarps * hd + 3) / 4 * 4);  // 16-byte aligned
   const uint32_t ring = uint32_t(__cvta_generic_to_shared(rings)) +
-                        warp * ring_bytes<T, G, V, kBwd, kSliced>() + lane * 16;
+                        warp * ring_bytes<T, G, V, kBwd, kSliced>();
+  constexpr int kXBytes = 32 * item_bytes<T, V>();  // of a warp's item: x, then dy
+  constexpr int kItemBytes = kXBytes + (kBwd ? 32 * item_bytes<G, V>() : 0);
   uint16_t* s_inv = nullptr;
   T* stages = nullptr;
   const unsigned skipped = P.stage - 8;
@@ -434,44 +450,50 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
   using At = Place<T, G>;
   auto full_x = [&](const At& w) { return reads_x && (!kSliced || w.kind < 0); };
   const int units = P.T << q.lg_chunks, stride = q.blocks * nwarps, step = tpw * hd;
-  // this lane's pieces of an item to ring place k (zeros where it has none)
+  // this lane's pieces of one tensor's row from channel e, zeros where it has
+  // none: [unit][group][piece][lane]
+  auto fetch_rows = [&](auto* row, int e, bool valid, uint32_t dst) {
+    using R = typename std::remove_cv<typename std::remove_pointer<decltype(row)>::type>::type;
+    constexpr int PB = piece_bytes<R, V>(), PG = group_pieces<R, V>();
+    constexpr bool kThrough = PG > 1 || kInter;
+    dst += lane * PB;
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      const bool on = valid && act[j];
+      const auto* a = row + (e + offa[j]);
+      const auto* b = a + apart[j];
+#pragma unroll
+      for (int i = 0; i < PG; ++i) {
+        copy_piece<PB, kThrough>(dst + ((2 * j) * PG + i) * 32 * PB, a + i * (PB / sizeof(R)), on);
+        copy_piece<PB, kThrough>(dst + ((2 * j + 1) * PG + i) * 32 * PB, b + i * (PB / sizeof(R)),
+                                 on);
+      }
+    }
+  };
+  auto from_ring = [&](auto& ra, auto& rb, int j, uint32_t src) {
+    using R = typename std::remove_reference<decltype(ra.v[0])>::type;
+    constexpr int PB = piece_bytes<R, V>(), PG = group_pieces<R, V>();
+    src += lane * PB;
+#pragma unroll
+    for (int i = 0; i < PG; ++i) {
+      read_piece<PB>(reinterpret_cast<char*>(ra.v) + i * PB, src + ((2 * j) * PG + i) * 32 * PB);
+      read_piece<PB>(reinterpret_cast<char*>(rb.v) + i * PB,
+                     src + ((2 * j + 1) * PG + i) * 32 * PB);
+    }
+  };
+  // an item's rows to ring place k
   auto fetch = [&](const At& w, int k) {
     if constexpr (kRing) {
       if (w.u < units) {
-        const bool on = w.e < n && act[0];
-        const int e = min(w.e, n - hd) + offa[0];  // inside the row either way
-        const uint32_t dst = ring + k * pieces<T, G, kBwd>() * 512;
-        if (full_x(w)) {
-          const T* x = w.x + e;
-          const T* x2 = x + apart[0];
-#pragma unroll
-          for (int i = 0; i < int(sizeof(T)) / 2; ++i) {
-            copy16<sizeof(T) == 4>(dst + i * 512, x + i * (16 / sizeof(T)), on);
-            copy16<sizeof(T) == 4>(dst + (int(sizeof(T)) / 2 + i) * 512, x2 + i * (16 / sizeof(T)), on);
-          }
-        }
-        if constexpr (kBwd) {
-          const G* y = w.y + e;
-          const G* y2 = y + apart[0];
-          const uint32_t dy = dst + int(sizeof(T)) * 512;
-#pragma unroll
-          for (int i = 0; i < int(sizeof(G)) / 2; ++i) {
-            copy16<sizeof(G) == 4>(dy + i * 512, y + i * (16 / sizeof(G)), on);
-            copy16<sizeof(G) == 4>(dy + (int(sizeof(G)) / 2 + i) * 512, y2 + i * (16 / sizeof(G)), on);
-          }
-        }
+        const bool valid = w.e < n;
+        const int e = min(w.e, n - hd);  // inside the row either way
+        const uint32_t dst = ring + k * kItemBytes;
+        if (full_x(w)) fetch_rows(w.x, e, valid, dst);
+        if constexpr (kBwd) fetch_rows(w.y, e, valid, dst + kXBytes);
       }
     }
     // one group an item, with the staged row that was asked for before it
     if constexpr (kRing || kSliced) asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  auto from_ring = [&](auto& ra, auto& rb, uint32_t src) {
-    constexpr int N = int(sizeof(ra)) / 16;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      reinterpret_cast<uint4*>(ra.v)[i] = lds128(src + i * 512);
-      reinterpret_cast<uint4*>(rb.v)[i] = lds128(src + (N + i) * 512);
-    }
   };
   // cosines and sines of a row, from the warp's lanes to each lane's pairs
   auto angles = [&](int pos) {
@@ -487,7 +509,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
     for (int j = 0; j < NU; ++j) {
       const int p0 = act[j] ? (lt + j * tl) * V : 0;  // (a lane without a unit: any values)
       Raw<float, V> c, s;
-      if constexpr (V == 8) {
+      if constexpr (V >= 4) {
         ld_vec(tab + p0, c);
         ld_vec(tab + np + p0, s);
       } else {
@@ -550,7 +572,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
   };
   auto compute = [&](const At& w, int k, T* stage) {
     const bool valid = w.e < n;
-    const uint32_t src = ring + k * pieces<T, G, kBwd>() * 512;
+    const uint32_t src = ring + k * kItemBytes;
     f2 xlo[NU][NP], xhi[NU][NP];
     f2 ss = 0ull;
 #pragma unroll
@@ -579,7 +601,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
       } else {
         Raw<T, V> xa, xb;
         if (kRing && reads_x) {
-          from_ring(xa, xb, src);
+          from_ring(xa, xb, j, src);
         } else {
           zero(xa);
           zero(xb);
@@ -629,7 +651,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
       for (int j = 0; j < NU; ++j) {
         Raw<G, V> ya, yb;
         if constexpr (kRing) {
-          from_ring(ya, yb, src + int(sizeof(T)) * 512);
+          from_ring(ya, yb, j, src + kXBytes);
         } else {
           zero(ya);
           zero(yb);
@@ -717,7 +739,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
       const T* from = static_cast<const T*>(q.Xc) + (long long)w.kind * q.n_idx;
       if (q.n_idx % 8 == 0) {
         const uint32_t dst = uint32_t(__cvta_generic_to_shared(to));
-        for (int i = lane * 8; i < q.n_idx; i += 256) copy16<false>(dst + 2 * i, from + i, true);
+        for (int i = lane * 8; i < q.n_idx; i += 256) copy_piece<16, false>(dst + 2 * i, from + i, true);
       } else {
         for (int i = lane; i < q.n_idx; i += 32) to[i] = from[i];
       }
@@ -926,6 +948,9 @@ slora_status launch_v(int V, bool inter, bool sliced, const QkParams& P,
   if (V == 8)
     return inter ? launch_s<T, G, 8, true, kBwd>(sliced, P, g, st)
                  : launch_s<T, G, 8, false, kBwd>(sliced, P, g, st);
+  if (V == 4)
+    return inter ? launch_s<T, G, 4, true, kBwd>(sliced, P, g, st)
+                 : launch_s<T, G, 4, false, kBwd>(sliced, P, g, st);
   if (V == 2)
     return inter ? launch_s<T, G, 2, true, kBwd>(sliced, P, g, st)
                  : launch_s<T, G, 2, false, kBwd>(sliced, P, g, st);
@@ -934,10 +959,11 @@ slora_status launch_v(int V, bool inter, bool sliced, const QkParams& P,
 }
 
 // The widest vector (in channels of one group) that every row of the call
-// takes: 16-byte accesses at 8, pairs at 2.  A unit may not straddle the
-// members of a pair, so in the half layout the width divides both halves.
+// takes.  A unit may not straddle the members of a pair, so in the half layout
+// the width divides both halves.  (16 + 4 heads of 96 channels, 24 of them
+// rotated, 8192 rows: forward 38 us with single loads of 2, 28 us at 4.)
 int vector_width(const QkDesc& D, bool backward) {
-  for (int V : {8, 2}) {
+  for (int V : {8, 4, 2}) {
     bool ok = D.rot.inter ? D.head_dim % (2 * V) == 0
                           : (D.rot.dims / 2) % V == 0 && (D.head_dim / 2 - D.rot.dims / 2) % V == 0;
     for (int i = 0; i < D.nparts && ok; ++i) {
@@ -968,10 +994,10 @@ Shape block_shape(const QkDesc& D, bool backward, bool sliced, int V) {
     ni = std::max(ni, D.part[i].idx ? D.part[i].n_idx : 0);
   }
   const int stage = (ni + 7) / 8 * 8 + 8;
-  // a warp's ring: one item more than is on its way, 512 bytes a piece
-  const int piece = dt_size(D.dt) + (backward ? dt_size(D.gdt) : 0);
-  const int ahead = sliced ? 1 : (backward ? 2 : 3);
-  const int ring = V == 8 ? (ahead + 1) * piece * 512 : 0;
+  // a warp's ring (ring_bytes): one item more than is on its way
+  const int pair = 2 * (dt_size(D.dt) + (backward ? dt_size(D.gdt) : 0));
+  const int items = sliced ? 2 : (backward ? 3 : 4);
+  const int ring = V == 1 ? 0 : items * 32 * std::max(V, 4) * pair;
   Shape best;
   for (int w = kWarps; w >= 1; w /= 2) {
     Shape s;
@@ -1111,7 +1137,7 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
   }
   std::copy(D.rot.turns, D.rot.turns + kMaxHeadDim / 2, P.turns);
   P.units = hd / 2 / V;
-  const int nu = V == 8 ? 1 : (V == 2 ? 2 : 4);
+  const int nu = V >= 4 ? 1 : (V == 2 ? 2 : 4);
   P.tl = 1;
   while (P.tl < 32 && P.tl * nu < P.units) P.tl *= 2;
   Geometry g;

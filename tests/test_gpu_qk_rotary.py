@@ -133,7 +133,7 @@ def test_norm_of_either_tensor(L, norm):
     run_case(L, norm=norm, hd=128)
 
 
-@pytest.mark.parametrize("pad", [8, 2, 1, 64])
+@pytest.mark.parametrize("pad", [8, 4, 2, 1, 64])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 def test_strided_rows(L, pad, layout):
     run_case(L, pad=pad, layout=layout, hd=64)
