@@ -28,10 +28,13 @@
 // ones on their way to shared memory.  Nothing in the loop waits for another
 // warp.
 //
-// Sliced rows: the inverse channel list lies in shared memory, and a context
-// row's compact channels are copied there ahead of their turn, gathered from
-// (and in the backward scattered back to) by channel, and stored with wide
-// stores.
+// Sliced rows: the inverse channel list lies in shared memory; a context row's
+// compact channels are staged there, gathered from (and in the backward
+// scattered back to) by channel, and stored with wide stores.  An output row's
+// heads pass through the same stage, two ahead.  The next row is asked into L2
+// meanwhile: a second stage a warp would cost more resident warps than it
+// hides (a forward and backward of 64 heads x 4096 rows at half the channels:
+// 131 us with two stages, 147 us with a full-width row a warp).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -68,7 +71,7 @@ struct QkParams {
   const int32_t* pos;
   const int32_t* ctx_off;  // sliced: context rows before sequence b, [batch + 1]
   int T, seq, hd, dims, units, tl;
-  int stage;  // sliced: elements of a warp's staged row, a multiple of 8; the last 8 stay zero
+  int stage;  // sliced: elements of a warp's stage, a multiple of 8; the last 8 stay zero
   float eps, mscale, inv_hd;
   unsigned seq_mul, seq_shift;  // t / seq = umulhi(t, seq_mul) >> seq_shift for t < 2^31, seq > 1
 };
@@ -295,9 +298,10 @@ __device__ __forceinline__ void cos_sin(int pos, unsigned long long turns, float
 // Rows on their way to shared memory: kAhead items of a warp beside the one
 // that is computed, each lane's own pieces of up to 16 bytes (an asynchronous
 // copy has at least 4: V > 1; single channels load when their turn comes).
+// Sliced rows: dy alone.
 template <bool kBwd, bool kSliced>
 constexpr int ahead() {
-  return kSliced ? 1 : (kBwd ? 2 : 3);
+  return kBwd ? (kSliced ? 1 : 2) : 3;
 }
 template <typename T, int V>
 constexpr int piece_bytes() {
@@ -316,7 +320,7 @@ template <typename T, typename G, int V, bool kBwd, bool kSliced>
 constexpr int ring_bytes() {
   return V == 1 ? 0
                 : (ahead<kBwd, kSliced>() + 1) * 32 *
-                      (item_bytes<T, V>() + (kBwd ? item_bytes<G, V>() : 0));
+                      ((kSliced ? 0 : item_bytes<T, V>()) + (kBwd ? item_bytes<G, V>() : 0));
 }
 // kThrough: part of a 32-byte sector whose other part the lane copies next;
 // through L1, so that the sector is fetched once (as pieces below 16 bytes are).
@@ -365,10 +369,11 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
     qk_rotary_kernel(const __grid_constant__ QkParams P) {
   constexpr int NU = units_per_lane<V>(), NP = packs<V>();
   constexpr int kAhead = ahead<kBwd, kSliced>();
-  constexpr bool kRing = V > 1;
+  constexpr bool kRingX = V > 1 && !kSliced, kRingY = V > 1 && kBwd, kRing = kRingX || kRingY;
+  constexpr bool kThroughStage = V > 1 && kSliced;  // output rows' x
   // [warps][hd / 2 cosines, hd / 2 sines] (the backward's dg at the end), the
   // warps' rings, then for sliced rows the inverse channel list (a channel that
-  // is not computed: the staged rows' zero) and two staged rows a warp
+  // is not computed: the stage's zero) and a stage a warp
   extern __shared__ __align__(16) float smem[];
   __shared__ unsigned long long s_turns[kMaxHeadDim / 2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nwarps = blockDim.x >> 5;
@@ -381,19 +386,20 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
   char* rings = reinterpret_cast<char*>(smem + (nwarps * hd + 3) / 4 * 4);  // 16-byte aligned
   const uint32_t ring = uint32_t(__cvta_generic_to_shared(rings)) +
                         warp * ring_bytes<T, G, V, kBwd, kSliced>();
-  constexpr int kXBytes = 32 * item_bytes<T, V>();  // of a warp's item: x, then dy
-  constexpr int kItemBytes = kXBytes + (kBwd ? 32 * item_bytes<G, V>() : 0);
+  // of a warp's item: x, then dy
+  constexpr int kXBytes = 32 * item_bytes<T, V>(), kYBytes = kBwd ? 32 * item_bytes<G, V>() : 0;
+  constexpr int kYAt = kRingX ? kXBytes : 0, kItemBytes = kYAt + kYBytes;
   uint16_t* s_inv = nullptr;
-  T* stages = nullptr;
+  T* stage = nullptr;
   const unsigned skipped = P.stage - 8;
   if constexpr (kSliced) {
     s_inv = reinterpret_cast<uint16_t*>(rings + nwarps * ring_bytes<T, G, V, kBwd, kSliced>());
-    stages = reinterpret_cast<T*>(s_inv + (n + 7) / 8 * 8) + warp * 2 * P.stage;
+    stage = reinterpret_cast<T*>(s_inv + (n + 7) / 8 * 8) + warp * P.stage;
     for (int i = tid; i < n; i += blockDim.x) {
       const int at = q.inv[i];
       s_inv[i] = uint16_t(at < 0 ? skipped : unsigned(at));
     }
-    if (lane < 16) stages[(lane >> 3) * P.stage + skipped + (lane & 7)] = from_f<T>(0.0f);
+    if (lane < 8) stage[skipped + lane] = from_f<T>(0.0f);
   }
   for (int p = tid; p < dims / 2; p += blockDim.x) s_turns[p] = P.turns[p];
   __syncthreads();
@@ -448,7 +454,6 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
   const f2 minus1 = pack2(-1.0f, -1.0f);
 
   using At = Place<T, G>;
-  auto full_x = [&](const At& w) { return reads_x && (!kSliced || w.kind < 0); };
   const int units = P.T << q.lg_chunks, stride = q.blocks * nwarps, step = tpw * hd;
   // this lane's pieces of one tensor's row from channel e, zeros where it has
   // none: [unit][group][piece][lane]
@@ -488,12 +493,11 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
         const bool valid = w.e < n;
         const int e = min(w.e, n - hd);  // inside the row either way
         const uint32_t dst = ring + k * kItemBytes;
-        if (full_x(w)) fetch_rows(w.x, e, valid, dst);
-        if constexpr (kBwd) fetch_rows(w.y, e, valid, dst + kXBytes);
+        if (kRingX && reads_x) fetch_rows(w.x, e, valid, dst);
+        if constexpr (kRingY) fetch_rows(w.y, e, valid, dst + kYAt);
       }
     }
-    // one group an item, with the staged row that was asked for before it
-    if constexpr (kRing || kSliced) asm volatile("cp.async.commit_group;" ::: "memory");
+    if constexpr (kRing) asm volatile("cp.async.commit_group;" ::: "memory");  // one an item
   };
   // cosines and sines of a row, from the warp's lanes to each lane's pairs
   auto angles = [&](int pos) {
@@ -551,7 +555,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
     ld_vec(inv, ia);
     ld_vec(inv + apart[j], ib);
   };
-  auto store = [&](const At& w, T* stage, int j, const f2 (&lo)[NP], const f2 (&hi)[NP]) {
+  auto store = [&](const At& w, int j, const f2 (&lo)[NP], const f2 (&hi)[NP]) {
     Raw<T, V> ra, rb;
     groups<T, V, kInter>(lo, hi, ra, rb);
     if constexpr (kSliced && kBwd) {
@@ -570,7 +574,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
     st_vec(o, ra);
     st_vec(o + apart[j], rb);
   };
-  auto compute = [&](const At& w, int k, T* stage) {
+  auto compute = [&](const At& w, int k, int sx) {  // sx: the stage's place of an output row's x
     const bool valid = w.e < n;
     const uint32_t src = ring + k * kItemBytes;
     f2 xlo[NU][NP], xhi[NU][NP];
@@ -600,8 +604,10 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
         pack_all<V>(h, xhi[j]);
       } else {
         Raw<T, V> xa, xb;
-        if (kRing && reads_x) {
+        if (kRingX && reads_x) {
           from_ring(xa, xb, j, src);
+        } else if (kThroughStage && reads_x) {
+          from_ring(xa, xb, j, uint32_t(__cvta_generic_to_shared(stage)) + sx * kXBytes);
         } else {
           zero(xa);
           zero(xb);
@@ -642,7 +648,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
           lo[i] = fma2(mul2(m, sn[j][i]), minus1, mul2(l, cs[j][i]));
           hi[i] = fma2(m, cs[j][i], mul2(l, sn[j][i]));
         }
-        if (valid && act[j]) store(w, stage, j, lo, hi);
+        if (valid && act[j]) store(w, j, lo, hi);
       }
     } else {
       f2 dlo[NU][NP], dhi[NU][NP];  // dn = R^T dy
@@ -650,8 +656,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
 #pragma unroll
       for (int j = 0; j < NU; ++j) {
         Raw<G, V> ya, yb;
-        if constexpr (kRing) {
-          from_ring(ya, yb, j, src + kXBytes);
+        if constexpr (kRingY) {
+          from_ring(ya, yb, j, src + kYAt);
         } else {
           zero(ya);
           zero(yb);
@@ -692,7 +698,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
       }
 #pragma unroll
       for (int j = 0; j < NU; ++j)
-        if (valid && act[j]) store(w, stage, j, dlo[j], dhi[j]);
+        if (valid && act[j]) store(w, j, dlo[j], dhi[j]);
     }
   };
 
@@ -727,71 +733,103 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
     w.u += stride;
     enter(w, in, out);
   };
-  // Sliced: the staged row of the unit that `w` enters starts to arrive (its
-  // buffer's last unit is two units back).
-  int side = 0;  // buffer of the next row to arrive
-  auto fetch_row = [&](const At& w) {
-    if constexpr (kSliced) {
-      if (w.u >= units || !w.first) return;
-      T* to = stages + side * P.stage;
-      side ^= 1;
-      if (w.kind < 0 || !reads_x) return;
-      const T* from = static_cast<const T*>(q.Xc) + (long long)w.kind * q.n_idx;
-      if (q.n_idx % 8 == 0) {
-        const uint32_t dst = uint32_t(__cvta_generic_to_shared(to));
-        for (int i = lane * 8; i < q.n_idx; i += 256) copy_piece<16, false>(dst + 2 * i, from + i, true);
-      } else {
-        for (int i = lane; i < q.n_idx; i += 32) to[i] = from[i];
-      }
-    }
-  };
-  auto store_row = [&](const At& w, const T* stage) {
-    T* to = static_cast<T*>(q.outc) + (long long)w.kind * q.n_idx;
+  // Sliced: a context row's compact channels to the stage, and back from it
+  auto copy_row = [&](T* to, const T* from) {
     __syncwarp();
     if (q.n_idx % 8 == 0) {
+#pragma unroll 4
       for (int i = lane * 8; i < q.n_idx; i += 256)
-        *reinterpret_cast<uint4*>(to + i) = *reinterpret_cast<const uint4*>(stage + i);
+        *reinterpret_cast<uint4*>(to + i) = *reinterpret_cast<const uint4*>(from + i);
     } else {
-      for (int i = lane; i < q.n_idx; i += 32) to[i] = stage[i];
+      for (int i = lane; i < q.n_idx; i += 32) to[i] = from[i];
     }
     __syncwarp();
+  };
+  // ... the x of round `ahead` of an output row to the stage's place sx
+  auto ask_ahead = [&](const At& w, int ahead, int sx) {
+    if constexpr (kThroughStage) {
+      if (w.left > ahead) {
+        const int e = w.e + ahead * step;
+        fetch_rows(w.x, min(e, n - hd), e < n,
+                   uint32_t(__cvta_generic_to_shared(stage)) + sx * kXBytes);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+  // ... and the x of this warp's next unit on its way to L2
+  auto ask_for_next = [&](const At& w) {
+    At then = w;
+    then.u += stride;
+    if (!reads_x || then.u >= units) return;
+    enter(then, true, false);
+    const bool ctx = then.kind >= 0;
+    const char* from = ctx ? static_cast<const char*>(q.Xc) +
+                                 (long long)then.kind * q.n_idx * int(sizeof(T))
+                           : reinterpret_cast<const char*>(then.x);
+    const int bytes = (ctx ? q.n_idx : n) * int(sizeof(T));
+    for (int i = lane * 128; i < bytes; i += 32 * 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
   };
 
   // w: the item that is computed; f: the one whose rows are asked for (rows that
   // are not copied ahead are w's own)
-  constexpr bool kIn = !kRing;
+  constexpr bool kIn = !kRingX || (kBwd && !kRingY);
   At w, f;
   w.u = f.u = blk * nwarps + warp;
   w.kind = f.kind = -1;
   w.left = f.left = 0;
   enter(w, kIn, true);
   enter(f, true, false);
+  if constexpr (kRing) {
 #pragma unroll
-  for (int k = 0; k < kAhead; ++k) {
-    fetch_row(f);
-    fetch(f, k);
-    if (f.u < units) next(f, true, false);
+    for (int k = 0; k < kAhead; ++k) {
+      fetch(f, k);
+      if (f.u < units) next(f, true, false);
+    }
   }
-  int now = 1;  // sliced: buffer of the unit that is computed (flipped as it starts)
-  while (w.u < units) {  // the same rounds for every lane of a warp
+  int sx = 0;              // the stage's place of this round
+  while (w.u < units) {    // the same rounds for every lane of a warp
 #pragma unroll
     for (int k = 0; k <= kAhead; ++k) {  // ring places
       if (w.u >= units) break;
-      fetch_row(f);
-      fetch(f, (k + kAhead) % (kAhead + 1));
-      if (f.u < units) next(f, true, false);
-      if constexpr (kRing || kSliced) copies_but<kAhead>();
+      if constexpr (kRing) {
+        fetch(f, (k + kAhead) % (kAhead + 1));
+        if (f.u < units) next(f, true, false);
+      }
+      if constexpr (kSliced) {
+        if (w.first) {
+          ask_for_next(w);
+          if (w.kind >= 0 && reads_x)
+            copy_row(stage, static_cast<const T*>(q.Xc) + (long long)w.kind * q.n_idx);
+        }
+        if (w.kind < 0 && reads_x) {
+          if (w.first) {
+            __syncwarp();  // the last row's channels have been read
+            sx = 0;
+            ask_ahead(w, 0, 0);
+            ask_ahead(w, 1, 1);
+          }
+          ask_ahead(w, 2, sx == 0 ? 2 : sx - 1);
+        }
+      }
+      // this item's copies, those of its x behind two rounds of the stage's
+      if constexpr (kThroughStage) {
+        if (w.kind < 0 && reads_x) copies_but<2>();
+        else copies_but<kRing ? kAhead : 0>();
+      } else if constexpr (kRing) {
+        copies_but<kAhead>();
+      }
       if (w.first) {
-        now ^= 1;
         int pos;
         if (P.pos) pos = P.pos[w.t];
         else pos = w.t - sequence_of(w.t) * P.seq;
-        angles(pos);  // (its barriers make the staged row visible)
+        angles(pos);
       }
-      T* stage = kSliced ? stages + now * P.stage : nullptr;
-      compute(w, k, stage);
+      compute(w, k, sx);
+      sx = sx == 2 ? 0 : sx + 1;
       if constexpr (kSliced && kBwd) {
-        if (w.kind >= 0 && w.left == 1) store_row(w, stage);
+        if (w.kind >= 0 && w.left == 1)
+          copy_row(static_cast<T*>(q.outc) + (long long)w.kind * q.n_idx, stage);
       }
       next(w, kIn, true);
     }
@@ -980,9 +1018,9 @@ int vector_width(const QkDesc& D, bool backward) {
 constexpr double kAngles = 0.6;  // a unit's angles, in rounds (about 150 of 245 instructions)
 
 // Warps of a block, its shared memory (tables and rings, and for sliced rows the
-// inverse channel list and two staged rows a warp) and the blocks that an SM
+// inverse channel list and a stage a warp) and the blocks that an SM
 // holds of them: registers allow 16 warps backward and 24 forward (the kernel's
-// launch bounds), shared memory 220 KB.  Eight warps, or the smaller block that
+// launch bounds), shared memory 226 KB with 2 KB of a block's own.  Eight warps, or the smaller block that
 // keeps more warps resident.
 struct Shape {
   int warps = 1, smem = 0, per_sm = 1, stage = 0;
@@ -993,10 +1031,11 @@ Shape block_shape(const QkDesc& D, bool backward, bool sliced, int V) {
     n = std::max(n, D.part[i].heads * D.head_dim);
     ni = std::max(ni, D.part[i].idx ? D.part[i].n_idx : 0);
   }
-  const int stage = (ni + 7) / 8 * 8 + 8;
+  // a staged row, or three items of an output row's x
+  const int stage = std::max((ni + 7) / 8 * 8, V == 1 ? 0 : 3 * 32 * 2 * std::max(V, 4)) + 8;
   // a warp's ring (ring_bytes): one item more than is on its way
-  const int pair = 2 * (dt_size(D.dt) + (backward ? dt_size(D.gdt) : 0));
-  const int items = sliced ? 2 : (backward ? 3 : 4);
+  const int pair = 2 * ((sliced ? 0 : dt_size(D.dt)) + (backward ? dt_size(D.gdt) : 0));
+  const int items = backward ? (sliced ? 2 : 3) : 4;
   const int ring = V == 1 ? 0 : items * 32 * std::max(V, 4) * pair;
   Shape best;
   for (int w = kWarps; w >= 1; w /= 2) {
@@ -1004,8 +1043,8 @@ Shape block_shape(const QkDesc& D, bool backward, bool sliced, int V) {
     s.warps = w;
     s.stage = stage;
     s.smem = (w * D.head_dim * 4 + 15) / 16 * 16 + w * ring;
-    if (sliced) s.smem += (n + 7) / 8 * 16 + w * 2 * stage * 2;
-    s.per_sm = std::min((backward ? 16 : 24) / w, 220 * 1024 / s.smem);
+    if (sliced) s.smem += (n + 7) / 8 * 16 + w * stage * 2;
+    s.per_sm = std::min((backward ? 16 : 24) / w, 226 * 1024 / (s.smem + 2048));
     if (w == kWarps || s.warps * s.per_sm > best.warps * best.per_sm) best = s;
   }
   return best;
