@@ -71,6 +71,7 @@ struct QkParams {
   const int32_t* pos;
   const int32_t* ctx_off;  // sliced: context rows before sequence b, [batch + 1]
   int T, seq, hd, dims, units, tl;
+  int TC, batch, batch_pow;  // sliced: context rows, sequences, a power of two not above them
   int stage;  // sliced: elements of a warp's stage, a multiple of 8; the last 8 stay zero
   float eps, mscale, inv_hd;
   unsigned seq_mul, seq_shift;  // t / seq = umulhi(t, seq_mul) >> seq_shift for t < 2^31, seq > 1
@@ -714,9 +715,20 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
     w.left = (min(heads - h0, q.per_chunk) + tpw - 1) / tpw;
     w.first = true;
     if constexpr (kSliced) {
-      const int b = sequence_of(w.t), i = w.t - b * P.seq;
+      // the context rows first, the output rows, which cost less, behind them:
+      // a warp's last unit is a light one
+      const bool ctx = w.u < P.TC;
+      const int at = ctx ? w.u : w.u - P.TC;
+      // its sequence: the last one with at most `at` such rows before it
+      int b = 0;
+      for (int s = P.batch_pow; s; s >>= 1)
+        if (b + s < P.batch) {
+          const int before = P.ctx_off[b + s];
+          if ((ctx ? before : (b + s) * P.seq - before) <= at) b += s;
+        }
       const int o0 = P.ctx_off[b], o1 = P.ctx_off[b + 1];
-      w.kind = i < o1 - o0 ? o0 + i : -1 - (w.t - o1);
+      w.kind = ctx ? at : -1 - at;
+      w.t = ctx ? b * P.seq + (at - o0) : at + o1;
       const long long full = w.kind < 0 ? (long long)(-1 - w.kind) * n : 0;
       w.x = static_cast<const T*>(q.Xo) + full;
       w.o = kBwd ? static_cast<T*>(q.outo) + full : static_cast<T*>(q.out) + w.t * q.ldo;
@@ -1163,6 +1175,10 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
   P.ctx_off = ctx_off;
   P.T = int(D.ti.T);
   P.seq = D.ti.seq;
+  P.TC = int(D.ti.T_C);
+  P.batch = D.ti.batch;
+  P.batch_pow = 1;
+  while (2 * P.batch_pow <= P.batch) P.batch_pow *= 2;
   P.hd = hd;
   P.dims = D.rot.dims;
   P.eps = D.eps;
