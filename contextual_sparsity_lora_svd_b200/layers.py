@@ -349,13 +349,21 @@ class DecoderStack(_Runner):
     dense).  X [T x d] is the stack input, dY [T x d] the gradient of its
     output.  After step(): `y` is the output, `dX` the input gradient,
     `grads[l]` layer l's LoRA gradients (views of `gflat`), `idx_qk[l]` /
-    `idx_ffn[l]` (first `k_ffn[l]` entries) the channel sets used."""
+    `idx_ffn[l]` (first `k_ffn[l]` entries) the channel sets used.
+
+    `rotary` (L.rotary(...)) chooses another rotation than half pairs of the whole
+    head at unscaled angles; `rope_base` is then unused.  `qk_norm`: every q and
+    k head is RMS-normalised before the rotation with the frozen gains gq, gk
+    (bf16 [head_dim]) of its layer's dict.  `act8`: what only the backward reads
+    of the inputs of both norms and of the q, k and v linears is kept as 8-bit
+    checkpoints, 1.03 bytes a value in place of 2, and the bf16 tensors x, h and
+    n1 hold the last layer's; the forward's numbers do not change."""
 
     GRAD_ORDER = ("q", "k", "v", "o")
 
     def __init__(self, layers, d, heads, kv_heads, head_dim, d_ff, r_svd, r_lora, scale, batch,
                  seq, ctx_len, qk_sparsity, ffn_sparsity, X, dY, rope_base=10000.0,
-                 eps=1e-5):
+                 eps=1e-5, rotary=None, qk_norm=False, act8=False):
         H, KV, hd = heads, kv_heads, head_dim
         nq, nkv, T = H * hd, KV * hd, batch * seq
         tok, tok_keep = L.make_tokens(batch, seq, ctx_len)
@@ -369,14 +377,62 @@ class DecoderStack(_Runner):
         nl = len(layers)
         self.nl = nl
         # ---- saved activations, per layer
-        self.x = [X] + [bf(T, d) for _ in range(nl - 1)]
+        if act8:  # x, h and n1 live for one layer's forward; their checkpoints stay
+            xs, n1s, hs = bf(T, d), bf(T, d), bf(T, d)
+            self.x = [X] + [xs] * (nl - 1)
+        else:
+            self.x = [X] + [bf(T, d) for _ in range(nl - 1)]
         self.y = bf(T, d)
         sv = []
         for _ in range(nl):
-            sv.append(dict(n1=bf(T, d), r1=f32(T), Qr=bf(T, nq), Kr=bf(T, nkv), V=bf(T, nkv),
-                           O=bf(T, nq), lse=f32(batch, H, seq), XAq=f32(T, r), XAk=f32(T, r),
-                           XAv=f32(T, r), XAo=f32(T, r), h=bf(T, d), n2=bf(T, d), r2=f32(T)))
+            sv.append(dict(n1=n1s if act8 else bf(T, d), r1=f32(T), Qr=bf(T, nq), Kr=bf(T, nkv),
+                           V=bf(T, nkv), O=bf(T, nq), lse=f32(batch, H, seq), XAq=f32(T, r),
+                           XAk=f32(T, r), XAv=f32(T, r), XAo=f32(T, r),
+                           h=hs if act8 else bf(T, d), n2=bf(T, d), r2=f32(T)))
+            if act8:
+                # layer 0 reads X, which the caller keeps
+                sv[-1].update({k: L.act8_empty(T, d) for k in ("x8", "n18", "h8")[len(sv) == 1:]})
         self.saved = sv
+
+        def ck(pair):  # the C struct of a checkpoint, kept alive
+            c = L.act8(*pair, T, d)
+            self._keep.append(c)
+            return ctypes.byref(c)
+
+        def norm_fwd(Xin, A, g, Hout, N, rstd, H8, N8):
+            args = [L.BF16, T, d, L.c_f32(eps), L.ptr(Xin), L.ptr(A), L.ptr(g), L.ptr(Hout),
+                    L.ptr(N), L.ptr(rstd)]
+            if act8:
+                return _Call("slora_rmsnorm_fwd_act8", args + [ck(H8) if H8 else None,
+                                                               ck(N8) if N8 else None])
+            return _Call("slora_rmsnorm_fwd", args)
+
+        def norm_bwd(Hin, H8, rstd, g, dN0, dN1, dN2, dRes, dXo):
+            tail = [L.ptr(rstd), L.ptr(g), L.ptr(dN0), L.ptr(dN1), L.ptr(dN2), L.ptr(dRes),
+                    L.ptr(dXo)]
+            if H8:
+                return _Call("slora_rmsnorm_bwd_act8", [L.BF16, T, d, ck(H8)] + tail)
+            return _Call("slora_rmsnorm_bwd", [L.BF16, T, d, L.ptr(Hin)] + tail)
+
+        def lin_bwd(base, side, S_, XA, dYc, dYo, dXn, dA, dB):  # of q, k or v: reads n1
+            tail = [L.ptr(XA), L.ptr(dYc), L.ptr(dYo), L.ptr(dXn), None, L.ptr(dA), L.ptr(dB)]
+            if act8:
+                return _Call("slora_linear_bwd_act8", base + side + [ck(S_["n18"]), None] + tail)
+            return _Call("slora_linear_bwd", base + side + [L.ptr(S_["n1"]), None] + tail)
+
+        # rotation by slora_qk_rotary_* where the packed form does not reach
+        turn = qk_norm or rotary is not None
+        rot = rotary or L.rotary(base=rope_base)
+
+        def qk_turn(name, heads, g, R, dR, **rows):  # (forward, backward) of q or k
+            fwd = L.qk_rows(heads, g=g, Y=R, **{k: v for k, v in rows.items() if k[0] != "d"})
+            back = L.qk_rows(heads, g=g, dY=dR, **rows)
+            self._keep += [fwd, back, rot]
+            head = [ctypes.byref(tok), hd, L.c_f32(eps), ctypes.byref(rot), None]
+            return (_Call("slora_qk_rotary_fwd", [L.BF16] + head + [ctypes.byref(fwd), None]),
+                    _Call("slora_qk_rotary_bwd",
+                          [L.BF16, L.F32] + head + [ctypes.byref(back), None]))
+
         # ---- scratch shared by the layers
         a_out, f_out = bf(T, d), bf(T, d)
         dn2, dh, dxq, dxk, dxv = bf(T, d), bf(T, d), bf(T, d), bf(T, d), bf(T, d)
@@ -409,15 +465,9 @@ class DecoderStack(_Runner):
             G = self.grads[l]
             # -- input normalisation (the first layer reads X; later ones add
             # the previous FFN output to the previous residual)
-            if l == 0:
-                calls.append(_Call("slora_rmsnorm_fwd", [L.BF16, T, d, L.c_f32(eps), L.ptr(X),
-                                                         None, L.ptr(w["g1"]), None,
-                                                         L.ptr(S_["n1"]), L.ptr(S_["r1"])]))
-            else:
-                calls.append(_Call("slora_rmsnorm_fwd",
-                                   [L.BF16, T, d, L.c_f32(eps), L.ptr(sv[l - 1]["h"]),
-                                    L.ptr(f_out), L.ptr(w["g1"]), L.ptr(self.x[l]),
-                                    L.ptr(S_["n1"]), L.ptr(S_["r1"])]))
+            first = (X, None, None) if l == 0 else (sv[l - 1]["h"], f_out, self.x[l])
+            calls.append(norm_fwd(first[0], first[1], w["g1"], first[2], S_["n1"], S_["r1"],
+                                  S_.get("x8"), S_.get("n18")))
             n1 = S_["n1"]
             # -- q/k channel selection
             sq = float(qk_sparsity[l])
@@ -461,11 +511,12 @@ class DecoderStack(_Runner):
                                                          float(rope_base), L.ptr(ii), ni,
                                                          L.ptr(dR), None, L.ptr(dYc),
                                                          L.ptr(dYo)])
-                    back = _Call("slora_linear_bwd", base + [L.SLICE_OUT_ROWS, L.ptr(ii), ni,
-                                                             L.ptr(n1), None, L.ptr(XA),
-                                                             L.ptr(dYc), L.ptr(dYo), L.ptr(dXn),
-                                                             None, L.ptr(G["dA" + nm]),
-                                                             L.ptr(G["dB" + nm])])
+                    back = lin_bwd(base, [L.SLICE_OUT_ROWS, L.ptr(ii), ni], S_, XA, dYc, dYo, dXn,
+                                   G["dA" + nm], G["dB" + nm])
+                    if turn:
+                        rope, unrope = qk_turn(nm, n // hd, w.get("g" + nm) if qk_norm else None,
+                                               R, dR, idx=ii, X_ctx=Yc, X_out=Yo, dX_ctx=dYc,
+                                               dX_out=dYo)
                 else:
                     Y, dYd = bf(T, n), bf(T, n)
                     self._keep += [Y, dYd]
@@ -477,19 +528,18 @@ class DecoderStack(_Runner):
                     unrope = _Call("slora_rope_unpack", [L.BF16, ctypes.byref(tok), n, hd,
                                                          float(rope_base), None, 0, L.ptr(dR),
                                                          L.ptr(dYd), None, None])
-                    back = _Call("slora_linear_bwd", base + [L.SLICE_NONE, None, 0, L.ptr(n1),
-                                                             None, L.ptr(XA), L.ptr(dYd), None,
-                                                             L.ptr(dXn), None,
-                                                             L.ptr(G["dA" + nm]),
-                                                             L.ptr(G["dB" + nm])])
+                    back = lin_bwd(base, [L.SLICE_NONE, None, 0], S_, XA, dYd, None, dXn,
+                                   G["dA" + nm], G["dB" + nm])
+                    if turn:
+                        rope, unrope = qk_turn(nm, n // hd, w.get("g" + nm) if qk_norm else None,
+                                               R, dR, X=Y, dX=dYd)
                 proj[nm] = (fwd, rope, unrope, back)
             vbase = [L.BF16, ctypes.byref(tok), d, nkv, L.ptr(w["Wv"]), L.ptr(w["Av"]),
-                     L.ptr(w["Bv"]), r, s, L.SLICE_NONE, None, 0]
-            v_f = _Call("slora_linear_fwd", vbase + [L.ptr(n1), None, L.ptr(S_["V"]), None,
-                                                     L.ptr(S_["XAv"])])
-            v_b = _Call("slora_linear_bwd", vbase + [L.ptr(n1), None, L.ptr(S_["XAv"]),
-                                                     L.ptr(dV), None, L.ptr(dxv), None,
-                                                     L.ptr(G["dAv"]), L.ptr(G["dBv"])])
+                     L.ptr(w["Bv"]), r, s]
+            vside = [L.SLICE_NONE, None, 0]
+            v_f = _Call("slora_linear_fwd", vbase + vside + [L.ptr(n1), None, L.ptr(S_["V"]), None,
+                                                             L.ptr(S_["XAv"])])
+            v_b = lin_bwd(vbase, vside, S_, S_["XAv"], dV, None, dxv, G["dAv"], G["dBv"])
             att_f = _Call("slora_attention_fwd", [L.BF16, ctypes.byref(tok), H, KV, hd,
                                                   L.ptr(S_["Qr"]), L.ptr(S_["Kr"]),
                                                   L.ptr(S_["V"]), L.ptr(S_["O"]),
@@ -510,10 +560,8 @@ class DecoderStack(_Runner):
             calls += [_Par([proj["q"][0], proj["q"][1]], [proj["k"][0], proj["k"][1]], [v_f]),
                       att_f, o_f]
             # -- residual + second normalisation, FFN forward (its own selection)
-            calls.append(_Call("slora_rmsnorm_fwd", [L.BF16, T, d, L.c_f32(eps),
-                                                     L.ptr(self.x[l]), L.ptr(a_out),
-                                                     L.ptr(w["g2"]), L.ptr(S_["h"]),
-                                                     L.ptr(S_["n2"]), L.ptr(S_["r2"])]))
+            calls.append(norm_fwd(self.x[l], a_out, w["g2"], S_["h"], S_["n2"], S_["r2"],
+                                  S_.get("h8"), None))
             sf = float(ffn_sparsity[l])
             fidx = torch.empty(d_ff, dtype=torch.int32, device="cuda")
             force = torch.arange(d_ff, dtype=torch.int32, device="cuda") if sf == 0.0 else None
@@ -551,15 +599,12 @@ class DecoderStack(_Runner):
             fa, fk = L.ffn_args(L.BF16, B["lay"], batch, seq, ctx_len, B["sf"], S_["n2"], dx_cur,
                                 f_out, dn2, B["fgs"], B["fidx"], B["force"])
             calls.append(_Call("slora_ffn_bwd", fa, fk + (B["force"],), own_ws=B["ws"]))
-            calls.append(_Call("slora_rmsnorm_bwd", [L.BF16, T, d, L.ptr(S_["h"]),
-                                                     L.ptr(S_["r2"]), L.ptr(w["g2"]), L.ptr(dn2),
-                                                     None, None, L.ptr(dx_cur), L.ptr(dh)]))
+            calls.append(norm_bwd(S_["h"], S_.get("h8"), S_["r2"], w["g2"], dn2, None, None,
+                                  dx_cur, dh))
             calls += [B["o_b"], B["att_b"],
                       _Par([B["q"][2], B["q"][3]], [B["k"][2], B["k"][3]], [B["v_b"]])]
-            calls.append(_Call("slora_rmsnorm_bwd", [L.BF16, T, d, L.ptr(self.x[l]),
-                                                     L.ptr(S_["r1"]), L.ptr(w["g1"]), L.ptr(dxq),
-                                                     L.ptr(dxk), L.ptr(dxv), L.ptr(dh),
-                                                     L.ptr(dx_next)]))
+            calls.append(norm_bwd(self.x[l], S_.get("x8"), S_["r1"], w["g1"], dxq, dxk, dxv, dh,
+                                  dx_next))
             dx_cur = dx_next
         self.dX = dx_cur
         self.calls = calls

@@ -68,6 +68,83 @@ def qk_backward(x, g, eps, dy, pos, freq, m, dims, layout):
         x) * r ** 3 * np.abs(x * u).mean(-1, keepdims=True)
 
 
+class _Stored(torch.autograd.Function):
+    """A tensor that is kept in bf16, as its gradient is."""
+
+    @staticmethod
+    def forward(ctx, x):
+        return x.bfloat16().double()
+
+    @staticmethod
+    def backward(ctx, g):
+        return g.bfloat16().double()
+
+
+def stack(X, dY, layers, batch, seq, ctx, H, KV, hd, sets, pos, freq, m, dims, layout, eps=1e-5,
+          stored=False):
+    """One step of a decoder stack with head norms (gains gq, gk where a layer has them) and this
+    rotation, by float64 autograd.  sets: per layer the kept (q, k, ffn) channels of the context
+    rows, None for all.  stored: every tensor that the step keeps or hands on, and every operand
+    of the attention's products, is rounded to bf16, and its gradient too; all else stays float64.
+    Returns (y, dX, one dict of LoRA gradients a layer)."""
+    bf = _Stored.apply if stored else lambda a: a
+    t64 = lambda a: torch.as_tensor(np.asarray(a, dtype=np.float64))  # noqa: E731
+    T = batch * seq
+    is_ctx = np.concatenate([np.arange(seq) < c for c in ctx])
+
+    def mask(n, idx):
+        keep = np.ones((T, n))
+        if idx is not None:
+            drop = np.setdiff1d(np.arange(n), idx)
+            keep[np.ix_(is_ctx, drop)] = 0.0
+        return t64(keep)
+
+    def norm(x, g):
+        return x / torch.sqrt((x ** 2).mean(-1, keepdim=True) + eps) * g
+
+    angle = t64(pos)[:, None] * t64(freq)[None]
+    c, s = m * torch.cos(angle)[:, None], m * torch.sin(angle)[:, None]
+    lo, hi = ((slice(0, dims // 2), slice(dims // 2, dims)) if layout == "half"
+              else (slice(0, dims, 2), slice(1, dims, 2)))
+
+    def turn(y, heads, g):
+        y = y.view(T, heads, hd)
+        if g is not None:
+            y = norm(y, g)
+        out = y.clone()
+        out[..., lo] = y[..., lo] * c - y[..., hi] * s
+        out[..., hi] = y[..., lo] * s + y[..., hi] * c
+        return bf(out).view(batch, seq, heads, hd).transpose(1, 2)
+
+    x0 = t64(X).requires_grad_()
+    x, leaves = x0, []
+    causal = torch.ones(seq, seq, dtype=torch.bool).tril()
+    for lay, (iq, ik, iff) in zip(layers, sets):
+        w = {k: t64(v) for k, v in lay.items() if k != "scale"}
+        leaf = {k: w[k].requires_grad_() for k in w if k[0] in "AB"}
+        leaves.append(leaf)
+
+        def lin(a, nm):
+            return bf(a @ w["W" + nm].T + lay["scale"] * (a @ w["A" + nm].T) @ w["B" + nm].T)
+
+        n1 = bf(norm(x, w["g1"]))
+        q = turn(lin(n1, "q") * mask(H * hd, iq), H, w.get("gq"))
+        k = turn(lin(n1, "k") * mask(KV * hd, ik), KV, w.get("gk"))
+        v = lin(n1, "v").view(batch, seq, KV, hd).transpose(1, 2)
+        k, v = (a.repeat_interleave(H // KV, dim=1) for a in (k, v))
+        z = q @ k.transpose(-1, -2) / math.sqrt(hd)
+        if stored:  # the softmax's derivative is handed on in bf16 too, its statistics are not
+            z.register_hook(lambda g: g.bfloat16().double())
+        p = bf(z.masked_fill(~causal, -math.inf).softmax(-1))
+        h = bf(x + lin(bf(p @ v).transpose(1, 2).reshape(T, H * hd), "o"))
+        n2 = bf(norm(h, w["g2"]))
+        z = bf(torch.nn.functional.silu(lin(n2, "g")) * lin(n2, "u"))
+        x = bf(h + lin(z * mask(z.shape[1], iff), "d"))
+    x.backward(t64(dY))
+    return (x.detach().numpy(), x0.grad.numpy(),
+            [{"d" + k: v.grad.numpy() for k, v in leaf.items()} for leaf in leaves])
+
+
 def act8(x):
     """(codes [T x d32], bytes [T x d32/32], values [T x d]) of a checkpoint of x."""
     x = np.asarray(x, dtype=np.float64)
