@@ -1151,13 +1151,11 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
 // launch for dY B (both row kinds), one for dA and dB; the part of a gradient
 // that belongs to the selected channels lands in a buffer of its own and is
 // added onto them.
-slora_status linear_bwd_act8_run(const LinearDesc& L0, const slora_tokens* tok,
+slora_status linear_bwd_act8_run(const LinearDesc& L, const slora_tokens* tok,
                                  const slora_act8& X_ctx, const slora_act8& X_out,
                                  const float* XA, const void* dY_ctx, const void* dY_out,
                                  void* dX_ctx, void* dX_out, float* dA, float* dB, Arena& ar,
                                  bool plan, cudaStream_t st) {
-  LinearDesc L;
-  SLORA_TRY(safe_indices(L0, ar, plan, st, &L));
   const TokenInfo& ti = L.ti;
   const int r = L.r;
   const int64_t k = L.k, n = L.n, ni = L.n_idx, T = ti.T, TC = ti.T_C, TO = ti.T_O;
@@ -1168,11 +1166,10 @@ slora_status linear_bwd_act8_run(const LinearDesc& L0, const slora_tokens* tok,
   auto bf = [&](int64_t rows, int64_t cols) {
     return static_cast<void*>(ar.take<__nv_bfloat16>(size_t(std::max<int64_t>(rows * cols, 1))));
   };
-  int32_t* ctx_rows = ar.take<int32_t>(size_t(std::max<int64_t>(TC, 1)));
-  int32_t* out_rows = ar.take<int32_t>(size_t(std::max<int64_t>(TO, 1)));
-  int4* ctiles = ar.take<int4>(size_t(std::max<int64_t>(nct, 1)));
-  int4* otiles = ar.take<int4>(size_t(std::max<int64_t>(nott, 1)));
-  int4* ptiles = none ? ar.take<int4>(size_t((T + 127) / 128)) : nullptr;
+  int32_t* ctx_rows = none ? nullptr : ar.take<int32_t>(size_t(std::max<int64_t>(TC, 1)));
+  int32_t* out_rows = none ? nullptr : ar.take<int32_t>(size_t(std::max<int64_t>(TO, 1)));
+  int4* ctiles = ar.take<int4>(size_t(std::max<int64_t>(none ? (T + 127) / 128 : nct, 1)));
+  int4* otiles = none ? nullptr : ar.take<int4>(size_t(std::max<int64_t>(nott, 1)));
   // s dY B in bf16, the GEMMs' LoRA operand: full rows, or compact by row kind
   void* dYBb = outr ? nullptr : bf(T, lr);
   void* dYBbC = outr ? bf(TC, lr) : nullptr;
@@ -1225,27 +1222,30 @@ slora_status linear_bwd_act8_run(const LinearDesc& L0, const slora_tokens* tok,
   if (plan) return SLORA_OK;
   SLORA_TRY(arena_fits(ar, "workspace"));
 
-  SLORA_TRY(launch_rowmaps(tok, ti, ctx_rows, out_rows, st, ctiles, otiles, cnt, ncnt));
   if (dYpad) SLORA_TRY(gather_pad(dY_ctx, ni, nullptr, TC, ni, dYpad, ldi, st, TC));
-  {  // B in one bf16 term (exact), XA in three
-    SkPrep jobs[4];
-    int nj = 0;
-    auto prep = [&](const SkR& R, int64_t I, void* rs) {
-      jobs[nj].R = R; jobs[nj].c = r; jobs[nj].I = I; jobs[nj].rs = rs;
-      ++nj;
-    };
-    auto xa = [&](const int32_t* map) {
-      SkR R = rkv(XA, kF32, r, 1, map);
-      R.terms = 0;
-      return R;
-    };
-    prep(rkv(L.B, kBF16, r, 1, outr ? L.idx : nullptr, n), outr ? ni : n, rsB0);
-    prep(xa(outr ? out_rows : nullptr), outr ? TO : T, tX);
+  {
+    LoraSetup u;
+    u.plain = none;
+    u.ctx_rows = ctx_rows; u.out_rows = out_rows; u.ctiles = ctiles; u.otiles = otiles;
+    u.XA = XA; u.terms = outr ? tXc : tX; u.terms_out = outr ? tX : nullptr;
+    u.B[0].src = L.B; u.B[0].idx = outr ? L.idx : nullptr; u.B[0].n = outr ? ni : n;
+    u.B[0].limit = n; u.B[0].dst = rsB0;
     if (outr) {
-      prep(rkv(L.B, kBF16, r, 1), n, rsB1);
-      prep(xa(ctx_rows), TC, tXc);
+      u.B[1].src = L.B; u.B[1].n = u.B[1].limit = n; u.B[1].dst = rsB1;
     }
-    SLORA_TRY(prep_r_batch(jobs, nj, st));
+    if (!none) {
+      u.W.src = L.W; u.W.idx = L.idx; u.W.n = ni; u.W.limit = outr ? n : k; u.W.dst = WS;
+      u.wcols = outr ? k : n;
+    }
+    if (in_cols) {
+      u.A[0].src = u.A[1].src = L.A;
+      u.A[0].idx = L.idx; u.A[0].n = ni; u.A[0].dst = AS;
+      u.A[1].n = k; u.A[1].dst = At;
+      u.A[0].limit = u.A[1].limit = k;
+      u.ldo = lr;
+    }
+    u.zero = cnt; u.nzero = ncnt;
+    SLORA_TRY(lora_setup(u, tok, ti, r, st));
     RankRows rows[2];
     RankRows &rc = rows[0], &ro = rows[1];
     rc.R = rsB0; rc.terms = tP; rc.ldo = lr;
@@ -1266,14 +1266,12 @@ slora_status linear_bwd_act8_run(const LinearDesc& L0, const slora_tokens* tok,
     SLORA_TRY(rank_rows(rows, none ? 1 : 2, r, s, st));
   }
   if (none) {
-    SLORA_TRY(make_plain_tiles(ptiles, T, st));
-    TcBuilder b(ptiles, (T + 127) / 128, 0, 0, T, k, 0, EPI_STORE);
+    TcBuilder b(ctiles, (T + 127) / 128, 0, 0, T, k, 0, EPI_STORE);
     b.seg(mat(dY_ctx, T, n, n), mat(L.W, n, k, k), B_MN, n)
         .seg(mat(dYBb, T, r, lr), mat(L.A, r, k, k), B_MN, r)
         .out(dX_ctx, nullptr, nullptr, k);
     SLORA_TRY(gemm_tc(b.g, st));
   } else if (outr) {
-    SLORA_TRY(gather_rows(L.W, k, L.idx, ni, k, WS, k, st, n));
     TcBuilder bc(ctiles, nct, 1, 0, TC, k, 0, EPI_STORE);
     bc.seg(mat(dYc, TC, ni, lddc), mat(WS, ni, k, k), B_MN, ni)
         .seg(mat(dYBbC, TC, r, lr), mat(L.A, r, k, k), B_MN, r)
@@ -1284,9 +1282,6 @@ slora_status linear_bwd_act8_run(const LinearDesc& L0, const slora_tokens* tok,
         .out(dX_ctx, nullptr, nullptr, k);
     SLORA_TRY(gemm_tc_pair(bc.g, b.g, st));
   } else {
-    SLORA_TRY(gather_rows(L.W, n, L.idx, ni, n, WS, n, st, k));
-    SLORA_TRY(transpose_rows(L.A, r, k, L.idx, ni, lr, AS, st));
-    SLORA_TRY(transpose_rows(L.A, r, k, nullptr, k, lr, At, st));
     TcBuilder bc(ctiles, nct, 0, 1, TC, ni, 0, EPI_STORE);
     bc.seg(mat(dY_ctx, T, n, n), mat(WS, ni, n, n), B_K, n)
         .seg(mat(dYBb, T, r, lr), mat(AS, ni, r, lr), B_K, r)

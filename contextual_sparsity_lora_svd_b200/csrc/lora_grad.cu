@@ -1,8 +1,14 @@
 // The rank-r contractions of a LoRA linear's backward (y = x W0^T + s (x A^T) B^T):
+//   lora_setup  the operands' layouts, the row maps and the tile lists
 //   rank_rows   p = dY B, row by row               (reads dY)
 //   rank_sums   dA = s p^T X, dB = s dY^T (X A^T)  (sums over tokens; read X and dY)
 // Each streams a large activation past a matrix with r columns, so both are
 // bound by that stream; X may be an 8-bit checkpoint (1.03 bytes a value).
+//
+// lora_setup: what six launches did (indices checked, row maps, terms, rows of W, two
+// transposes of A) in one whose blocks each take a piece of one of them: none waits for
+// another, so the small ones run beside the copy of W's rows, and every block works out
+// the compact place of a row from the sequences' offsets instead of reading a map.
 //
 // rank_rows: mma.sync m16n8k16 with fragments loaded straight from global
 // memory.  The channel order inside a reduction is free, so lane t of a quad
@@ -40,6 +46,7 @@
 namespace slora {
 
 __device__ int g_rank_error = 0;
+__device__ int g_rank_bad_index = 0;
 
 namespace {
 
@@ -53,6 +60,134 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// ------------------------------------------------------------------ setup
+constexpr int kSetupThreads = 256;
+constexpr int kSetupRows = 64;  // rows of XA or B of a block
+constexpr int kSmallBatch = 64;  // sequences in the small parameter block
+
+template <int CAP>
+struct SetupParams {
+  LoraSetup d;
+  int seq, batch, cols, cp;
+  long long ldt, ldto;  // columns of the terms' rows
+  long long T;
+  // first block of: the rows of W, the tokens, B's copies, A's transposes
+  int w0, t0, b0, b1, a0, a1;
+  int off[CAP + 1];  // context rows before each sequence
+};
+
+__device__ __forceinline__ long long setup_index(const LoraCopy& c, long long i) {
+  const long long v = c.idx ? (long long)c.idx[i] : i;
+  if (v >= 0 && v < c.limit) return v;
+  atomicExch(&g_rank_bad_index, 1);
+  return -1;
+}
+__device__ __forceinline__ void put_terms(__nv_bfloat16* o, long long plane, float v) {
+#pragma unroll
+  for (int k = 0; k < kTerms; ++k) {
+    const __nv_bfloat16 h = __float2bfloat16_rn(v);
+    v -= __bfloat162float(h);
+    o[k * plane] = h;
+  }
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kSetupThreads)
+    lora_setup_kernel(const __grid_constant__ SetupParams<CAP> P) {
+  const LoraSetup& d = P.d;
+  const int tid = threadIdx.x, blk = blockIdx.x, seq = P.seq;
+  if (blk < P.w0) {  // tile lists and counters
+    for (int64_t i = tid; i < d.nzero; i += kSetupThreads) d.zero[i] = 0u;
+    if (d.plain) {
+      for (long long r = 128ll * tid; r < P.T; r += 128ll * kSetupThreads)
+        d.ctiles[r / 128] = make_int4(int(r), int(r), int(min(128ll, P.T - r)), 0);
+      return;
+    }
+    __shared__ int ct[CAP], ot[CAP];
+    if (tid == 0) {
+      int c = 0, o = 0;
+      for (int b = 0; b < P.batch; ++b) {
+        const int len = P.off[b + 1] - P.off[b];
+        ct[b] = c;
+        ot[b] = o;
+        c += (len + 127) / 128;
+        o += (seq - len + 127) / 128;
+      }
+    }
+    __syncthreads();
+    for (int b = tid; b < P.batch; b += kSetupThreads) {
+      const int c0 = P.off[b], len = P.off[b + 1] - c0, row = b * seq;
+      for (int j = 0; j * 128 < len; ++j)
+        d.ctiles[ct[b] + j] = make_int4(row + 128 * j, c0 + 128 * j, min(128, len - 128 * j), 0);
+      for (int j = 0; j * 128 < seq - len; ++j)
+        d.otiles[ot[b] + j] = make_int4(row + len + 128 * j, row - c0 + 128 * j,
+                                        min(128, seq - len - 128 * j), 0);
+    }
+  } else if (blk < P.t0) {  // a warp a row of W, eight 16-byte loads a lane in flight
+    const long long j = (long long)(blk - P.w0) * (kSetupThreads / 32) + (tid >> 5);
+    if (j >= d.W.n) return;
+    const long long src = setup_index(d.W, j);
+    const int lane = tid & 31, n16 = int(d.wcols / 8);
+    const uint4* in = static_cast<const uint4*>(d.W.src) + max(src, 0ll) * n16;
+    uint4* out = static_cast<uint4*>(d.W.dst) + j * n16;
+    for (int c0 = lane; c0 < n16; c0 += 32 * 8) {
+      uint4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        v[u] = src >= 0 && c0 + 32 * u < n16 ? __ldg(in + c0 + 32 * u) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (c0 + 32 * u < n16) out[c0 + 32 * u] = v[u];
+    }
+  } else if (blk < P.b0) {  // tokens: maps and XA's terms; the row runs fastest in what is written
+    const long long t = (long long)(blk - P.t0) * kSetupRows + tid % kSetupRows;
+    if (t >= P.T) return;
+    long long at = t;
+    __nv_bfloat16* terms = static_cast<__nv_bfloat16*>(d.terms);
+    long long ldt = P.ldt;
+    if (!d.plain) {
+      const int b = int(t / seq), i = int(t % seq), c0 = P.off[b], len = P.off[b + 1] - c0;
+      const bool ctx = i < len;
+      const int place = ctx ? c0 + i : b * seq - c0 + (i - len);
+      if (tid < kSetupRows) (ctx ? d.ctx_rows : d.out_rows)[place] = int(t);
+      if (d.terms_out) {
+        at = place;
+        if (!ctx) {
+          terms = static_cast<__nv_bfloat16*>(d.terms_out);
+          ldt = P.ldto;
+        }
+      }
+    }
+    for (int q = tid / kSetupRows; q < P.cols; q += kSetupThreads / kSetupRows)
+      put_terms(terms + q * ldt + at, P.cp * ldt, __ldg(d.XA + t * P.cols + q));
+  } else if (blk < P.a0) {  // rows of B, transposed; zeros to whole rows of 64
+    const bool second = blk >= P.b1;
+    const LoraCopy& c = d.B[second ? 1 : 0];
+    const long long i = (long long)(blk - (second ? P.b1 : P.b0)) * kSetupRows + tid % kSetupRows;
+    const long long ld = (max((long long)c.n, 1ll) + kSetupRows - 1) / kSetupRows * kSetupRows;
+    const long long src = i < c.n ? setup_index(c, i) : -1;
+    const __nv_bfloat16* in = static_cast<const __nv_bfloat16*>(c.src) + max(src, 0ll) * P.cols;
+    for (int q = tid / kSetupRows; q < P.cp; q += kSetupThreads / kSetupRows)
+      static_cast<__nv_bfloat16*>(c.dst)[q * ld + i] =
+          src >= 0 && q < P.cols ? in[q] : __float2bfloat16_rn(0.0f);
+  } else {  // A's transposes: a thread eight columns of a row
+    const bool second = blk >= P.a1;
+    const LoraCopy& c = d.A[second ? 1 : 0];
+    const long long e = (long long)(blk - (second ? P.a1 : P.a0)) * kSetupThreads + tid;
+    const long long i = e % c.n, q0 = e / c.n * 8;  // rows run fastest: A is read along its rows
+    if (q0 >= d.ldo) return;
+    const long long src = setup_index(c, i);
+    alignas(16) __nv_bfloat16 v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      v[q] = src >= 0 && q0 + q < P.cols
+                 ? static_cast<const __nv_bfloat16*>(c.src)[(q0 + q) * c.limit + src]
+                 : __float2bfloat16_rn(0.0f);
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.dst) + i * d.ldo + q0) =
+        *reinterpret_cast<const uint4*>(v);
+  }
 }
 
 // ------------------------------------------------------------------- rows
@@ -129,13 +264,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 2)
 #pragma unroll
   for (int w = 0; w < kRowWarps; ++w) v += red[w][mr][q];
   j.out[row(m, true, j.map_out) * j.ldo + q0 + q] = __float2bfloat16_rn(P.s * v);
-  __nv_bfloat16* o = j.terms + (q0 + q) * j.ldt + row(m, true, j.map_terms);
-#pragma unroll
-  for (int k = 0; k < kTerms; ++k) {
-    const __nv_bfloat16 h = __float2bfloat16_rn(v);
-    v -= __bfloat162float(h);
-    o[(long long)k * P.cp * j.ldt] = h;
-  }
+  put_terms(j.terms + (q0 + q) * j.ldt + row(m, true, j.map_terms), P.cp * j.ldt, v);
 }
 
 // ------------------------------------------------------------------- sums
@@ -577,6 +706,45 @@ int64_t rank_terms_elems(int64_t M, int cols) {
   return kTerms * padded_cols(cols) * rank_terms_ld(M);
 }
 
+namespace {
+template <int CAP>
+slora_status setup(const LoraSetup& d, const slora_tokens* tok, const TokenInfo& ti, int cols,
+                   cudaStream_t st) {
+  SetupParams<CAP> p{};
+  p.d = d;
+  p.seq = ti.seq; p.batch = ti.batch; p.cols = cols;
+  p.cp = int(padded_cols(cols));
+  p.T = ti.T;
+  p.ldt = rank_terms_ld(d.terms_out ? ti.T_C : ti.T);
+  p.ldto = rank_terms_ld(ti.T_O);
+  for (int b = 0; b < ti.batch; ++b) p.off[b + 1] = p.off[b] + tok->ctx_len[b];
+  int64_t at = 1;
+  auto add = [&](int64_t items, int64_t each) {
+    const int64_t first = at;
+    at += (items + each - 1) / each;
+    return int(first);
+  };
+  p.w0 = add(d.W.n, kSetupThreads / 32);
+  p.t0 = add(ti.T, kSetupRows);
+  p.b0 = add(d.B[0].dst ? std::max<int64_t>(d.B[0].n, 1) : 0, kSetupRows);
+  p.b1 = add(d.B[1].dst ? std::max<int64_t>(d.B[1].n, 1) : 0, kSetupRows);
+  p.a0 = add(d.A[0].n * (d.ldo / 8), kSetupThreads);
+  p.a1 = add(d.A[1].n * (d.ldo / 8), kSetupThreads);
+  double bytes = double(ti.T) * cols * (4 + 2 * kTerms) + 4.0 * double(d.W.n) * d.wcols;
+  for (int i = 0; i < 2; ++i) bytes += 4.0 * double(d.B[i].n + d.A[i].n) * cols;
+  LaunchScope ls(kAux, bytes, st);
+  lora_setup_kernel<CAP><<<unsigned(at), kSetupThreads, 0, st>>>(p);
+  SLORA_CHECK_LAUNCH();
+  return SLORA_OK;
+}
+}  // namespace
+
+slora_status lora_setup(const LoraSetup& d, const slora_tokens* tok, const TokenInfo& ti, int cols,
+                        cudaStream_t st) {
+  return ti.batch <= kSmallBatch ? setup<kSmallBatch>(d, tok, ti, cols, st)
+                                 : setup<kMaxBatch>(d, tok, ti, cols, st);
+}
+
 slora_status rank_rows(const RankRows* jobs, int n, int cols, float s, cudaStream_t st) {
   if (n < 1 || n > 2) SLORA_FAIL(SLORA_ERR_SHAPE, "rank_rows: %d jobs", n);
   RowsParams p{};
@@ -678,12 +846,16 @@ slora_status rank_sums(const RankSum* jobs, int n, int cols, float scale, float*
 }
 
 slora_status rank_check_error(bool clear) {
-  int v = 0;
+  int v = 0, bad = 0;
   SLORA_CUDA(cudaMemcpyFromSymbol(&v, g_rank_error, sizeof(int)));
-  if (clear && v) {
+  SLORA_CUDA(cudaMemcpyFromSymbol(&bad, g_rank_bad_index, sizeof(int)));
+  if (clear && (v || bad)) {
     const int z = 0;
     SLORA_CUDA(cudaMemcpyToSymbol(g_rank_error, &z, sizeof(int)));
+    SLORA_CUDA(cudaMemcpyToSymbol(g_rank_bad_index, &z, sizeof(int)));
   }
+  if (bad)
+    SLORA_FAIL(SLORA_ERR_INVALID_ARG, "a channel index lies outside its weight (read as zeros)");
   if (v) SLORA_FAIL(SLORA_ERR_TIMEOUT, "a rank contraction's bounded wait expired");
   return SLORA_OK;
 }

@@ -8,14 +8,41 @@
 namespace slora {
 
 // An fp32 rank operand P [M x cols] as rank_sums reads it: three bf16 terms,
-// transposed, [3][cols rounded up to 16][rank_terms_ld(M)] (what prep_r_batch
-// makes of an fp32 operand; columns past M and rows past cols are not read).
+// transposed, [3][cols rounded up to 16][rank_terms_ld(M)]; columns past M are not read,
+// rows past cols reach no output.
 int64_t rank_terms_ld(int64_t M);
 int64_t rank_terms_elems(int64_t M, int cols);
 
+// What the contractions and products of one backward read, laid out in one launch:
+// the rows of each kind and their M tiles (SLORA_SLICE_NONE: plain tiles over all
+// rows, no maps), XA [T x cols] as terms (by full row, or by row kind in compact order),
+// up to two copies of rows of B [. x cols], transposed to [cols rounded up to 16][rows
+// rounded up to 64] (rank_rows' R), the kept rows of W, up to two transposes of A
+// [cols x .] to rows of ldo, and the zeroed counters.  idx null: every row or column;
+// an index outside `limit` stands for zeros and raises the flag of rank_check_error.
+struct LoraCopy {
+  const void* src = nullptr;
+  const int32_t* idx = nullptr;
+  int64_t n = 0, limit = 0;
+  void* dst = nullptr;
+};
+struct LoraSetup {
+  bool plain = false;
+  int32_t *ctx_rows = nullptr, *out_rows = nullptr;
+  int4 *ctiles = nullptr, *otiles = nullptr;  // plain: ctiles alone
+  const float* XA = nullptr;
+  void *terms = nullptr, *terms_out = nullptr;  // terms_out: by row kind, `terms` the context's
+  LoraCopy B[2], W, A[2];
+  int64_t wcols = 0, ldo = 0;  // columns of a row of W (a multiple of 8, 16-byte aligned rows)
+  unsigned* zero = nullptr;
+  int64_t nzero = 0;
+};
+slora_status lora_setup(const LoraSetup& d, const slora_tokens* tok, const TokenInfo& ti, int cols,
+                        cudaStream_t st);
+
 // Rows of a rank projection: p[m, q] = sum over c < K of Y(m, c) R(c, q), q <
 // cols, for m < M.  Y bf16 with 16-byte aligned rows whose columns past K, up
-// to a multiple of 8, are zero; R split by prep_r_batch into one bf16 term.
+// to a multiple of 8, are zero; R as lora_setup copies it.
 // Written as terms (column m) and, scaled by s and in bf16, to out (row m).
 // With map_*, map[m] stands for m: in the row of Y, the terms' column, out's row.
 struct RankRows {
@@ -52,7 +79,7 @@ int64_t rank_sums_counters(const RankSum* jobs, int n, int cols);
 slora_status rank_sums(const RankSum* jobs, int n, int cols, float scale, float* part,
                        unsigned* counters, cudaStream_t st);
 
-// Raised when a rank_sums wait ran out of its budget.
+// Raised when a rank_sums wait ran out of its budget, or by an index outside its weight.
 slora_status rank_check_error(bool clear);
 
 }  // namespace slora
