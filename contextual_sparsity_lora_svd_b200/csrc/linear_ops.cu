@@ -1265,6 +1265,14 @@ slora_status linear_bwd_act8_run(const LinearDesc& L, const slora_tokens* tok,
     }
     SLORA_TRY(rank_rows(rows, none ? 1 : 2, r, s, st));
   }
+  // before the product: dY is still in L2, and nothing of this needs dX
+  SLORA_TRY(rank_sums(sums, nsums, r, s, part, cnt, st));
+  if (sliced) {
+    ScatterAddJob sj;
+    sj.dst = outr ? dB : dA; sj.ld_dst = outr ? r : k;
+    sj.src = SG; sj.ld_src = outr ? r : ni; sj.trans = outr ? 0 : 1;
+    SLORA_TRY(scatter_add_cols(&sj, 1, L.idx, ni, r, outr ? n : k, st));
+  }
   if (none) {
     TcBuilder b(ctiles, (T + 127) / 128, 0, 0, T, k, 0, EPI_STORE);
     b.seg(mat(dY_ctx, T, n, n), mat(L.W, n, k, k), B_MN, n)
@@ -1292,12 +1300,7 @@ slora_status linear_bwd_act8_run(const LinearDesc& L, const slora_tokens* tok,
         .out(dX_out, nullptr, nullptr, k);
     SLORA_TRY(gemm_tc_pair(bc.g, b.g, st));
   }
-  SLORA_TRY(rank_sums(sums, nsums, r, s, part, cnt, st));
-  if (!sliced) return SLORA_OK;
-  ScatterAddJob sj;
-  sj.dst = outr ? dB : dA; sj.ld_dst = outr ? r : k;
-  sj.src = SG; sj.ld_src = outr ? r : ni; sj.trans = outr ? 0 : 1;
-  return scatter_add_cols(&sj, 1, L.idx, ni, r, outr ? n : k, st);
+  return SLORA_OK;
 }
 
 }  // namespace slora

@@ -446,15 +446,32 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
   const long long m0 = (long long)split * j.stages * kTok;
   const int stages = int(max(0ll, min((long long)j.stages, (j.M - m0 + kTok - 1) / kTok)));
   const bool codes = j.scales != nullptr;
-  if (tid == 0) {
+  const uint32_t sB = su32(smem), sX = sB + kRing * kBBytes;  // sX: operands, or codes
+  const uint32_t sA = sX + kRing * kXBytes;                   // codes' operand slots
+  auto copy = [&](int st) {
+    const int place = st % kRing, m = int(m0) + st * kTok;
+    mbar_expect(&copied[place], kBBytes + (codes ? kXBytes : kABytes));
+#pragma unroll
+    for (int s = 0; s < kTerms; ++s)
+      tma_load(sB + place * kBBytes + s * kCols * 128, &j.pmap, &copied[place], m,
+               s * P.cp + q0);
+    if (codes) {
+      tma_load(sX + place * kXBytes, &j.xmap, &copied[place], int(ch0), m);
+    } else {
+      tma_load(sX + place * kABytes, &j.xmap, &copied[place], int(ch0), m);
+      tma_load(sX + place * kABytes + kTok * 128, &j.xmap, &copied[place], int(ch0) + 64, m);
+    }
+  };
+  if (tid == kSumThreads - 32) {  // the copies' thread fills the ring while memory is allocated
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&copied[i], 1);
-      mbar_init(&ready[i], kXWarps);
+      mbar_init(&ready[i], kXWarps / kSlots8);
       mbar_init(&empty[i], 1);
     }
     mbar_init(&done, 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int st = 0; st < min(stages, kRing); ++st) copy(st);
   }
   if (warp == kXWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -468,8 +485,6 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tbase = s_tmem;
   volatile int* abort = &s_abort;
-  const uint32_t sB = su32(smem), sX = sB + kRing * kBBytes;  // sX: operands, or codes
-  const uint32_t sA = sX + kRing * kXBytes;                   // codes' operand slots
   // the products of stage st (which used its ring place and operand slot) are done
   auto products_done = [&](int st) {
     return st < 0 || mbar_wait(&empty[st % kRing], uint32_t(st / kRing) & 1u, abort);
@@ -478,23 +493,8 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
   if (warp == kXWarps + 1) {
     // ------------------------------------------------------------ copies
     if (lane == 0) {
-      int issued = 0;
-      for (int st = 0; st < stages; ++st, ++issued) {
-        const int place = st % kRing;
-        if (!products_done(st - kRing)) break;
-        const int m = int(m0) + st * kTok;
-        mbar_expect(&copied[place], kBBytes + (codes ? kXBytes : kABytes));
-#pragma unroll
-        for (int s = 0; s < kTerms; ++s)
-          tma_load(sB + place * kBBytes + s * kCols * 128, &j.pmap, &copied[place], m,
-                   s * P.cp + q0);
-        if (codes) {
-          tma_load(sX + place * kXBytes, &j.xmap, &copied[place], int(ch0), m);
-        } else {
-          tma_load(sX + place * kABytes, &j.xmap, &copied[place], int(ch0), m);
-          tma_load(sX + place * kABytes + kTok * 128, &j.xmap, &copied[place], int(ch0) + 64, m);
-        }
-      }
+      int issued = min(stages, kRing);
+      for (; issued < stages && products_done(issued - kRing); ++issued) copy(issued);
       // the copies land before the block may leave (normally long since read)
       for (int st = max(0, issued - kRing); st < issued; ++st) {
         const long long t0 = clock64();
@@ -532,31 +532,39 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
     }
   } else if (codes) {
     // --------------------------------------------------------- expansion
-    // this thread: 16 channels (unit tid % 8) of tokens tid / 8 and tid / 8 + 32
-    const int xt = tid >> 3, xu = tid & 7;
+    // The stages take turns on groups of four warps, a slot each: a group's barriers
+    // and its proxy fence come once in two stages.  This thread: 16 channels (unit
+    // tid % 8) of every sixteenth token.
+    const int group = warp / (kXWarps / kSlots8), gt = tid % (kXWarps / kSlots8 * 32);
+    const int xt = gt >> 3, xu = gt & 7;
     const long long ch = ch0 + 16 * xu;
     const bool inside = ch < j.ld8 * kActBlock;  // rows are whole blocks
     const uint8_t* sc = j.scales + (inside ? (m0 + xt) * j.ld8 + (ch >> 5) : 0);
     const int rows = int(min((long long)stages * kTok, j.M - m0));
-    auto byte_of = [&](int at) -> uint32_t {  // of the split's token xt + at
-      return inside && at + xt < rows ? sc[at * j.ld8] : 7u;
+    constexpr int kEach = kTok / 16;
+    uint32_t b[kEach], next[kEach];
+    auto bytes_of = [&](int st, uint32_t (&v)[kEach]) {  // of the split's tokens xt + ...
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int at = st * kTok + 16 * i;
+        v[i] = inside && at + xt < rows ? sc[at * j.ld8] : 7u;
+      }
     };
-    const uint32_t d0 = x_at(xt, 2 * xu), d1 = x_at(xt + 32, 2 * xu);
-    uint32_t b0[2] = {byte_of(0), byte_of(kTok)}, b1[2] = {byte_of(32), byte_of(kTok + 32)};
-    for (int st = 0; st < stages; ++st) {
+    const uint32_t dst = sA + group * kABytes + x_at(xt, 2 * xu);  // 16 tokens on: 2 KB on
+    bytes_of(group, b);
+    for (int st = group; st < stages; st += kSlots8) {
       const int place = st % kRing;
-      const uint32_t n0 = byte_of((st + 2) * kTok), n1 = byte_of((st + 2) * kTok + 32);
+      bytes_of(st + kSlots8, next);
       if (!mbar_wait(&copied[place], uint32_t(st / kRing) & 1u, abort)) break;
-      const uint4 w0 = lds128(sX + place * kXBytes + tid * 16);
-      const uint4 w1 = lds128(sX + place * kXBytes + tid * 16 + 4096);
+      uint4 w[kEach];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) w[i] = lds128(sX + place * kXBytes + gt * 16 + i * 2048);
       if (!products_done(st - kSlots8)) break;
-      const uint32_t dst = sA + (st % kSlots8) * kABytes;
-      expand16(dst + d0, w0, b0[0]);
-      expand16(dst + d1, w1, b1[0]);
-      b0[0] = b0[1];
-      b1[0] = b1[1];
-      b0[1] = n0;
-      b1[1] = n1;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        expand16(dst + i * 2048, w[i], b[i]);
+        b[i] = next[i];
+      }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(&ready[place]);
@@ -569,12 +577,13 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
   const long long ch = ch0 + 32 * warp + lane;  // TMEM lane = channel (warps 0 .. 3)
   float4* mine = reinterpret_cast<float4*>(
       P.part + ((long long)blockIdx.y * gridDim.x + blockIdx.x) * kTile) + 32 * (warp & 3) + lane;
-  auto emit = [&](const float (&v)[16]) {
-    if (ch >= j.K) return;
+  auto emit = [&](const auto& v, long long c, int first) {
+    if (c >= j.K) return;
 #pragma unroll
-    for (int q = 0; q < kCols; ++q)
-      if (q0 + q < P.cols)
-        j.out[j.trans ? (q0 + q) * j.ldo + ch : ch * j.ldo + q0 + q] = v[q] * P.scale;
+    for (int i = 0; i < int(sizeof(v) / sizeof(float)); ++i) {
+      const int q = q0 + first + i;
+      if (q < P.cols) j.out[j.trans ? q * j.ldo + c : c * j.ldo + q] = v[i] * P.scale;
+    }
   };
   if (warp < 4) {
     float v[16];
@@ -589,7 +598,7 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
         for (int q = 0; q < 16; ++q) v[q] += t[q];
       }
     if (j.nsplit == 1) {
-      emit(v);
+      emit(v, ch, 0);
     } else {  // [4 columns of 4][128 channels] of float4
 #pragma unroll
       for (int q = 0; q < 4; ++q)
@@ -612,26 +621,34 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
     if (s_last) P.counters[tile] = 0u;
   }
   __syncthreads();
-  if (!s_last || warp >= 4) return;
+  if (!s_last || warp >= kXWarps) return;
   __threadfence();
   // split s of this channel block ran as block (blockIdx.x - blk) + s * nch + cb
+  // (eight warps: a thread half the columns of a channel, eight splits' loads at once)
+  const int c = tid % kCh, half = tid / kCh * 2;
   const float4* src = reinterpret_cast<const float4*>(
-      P.part + ((long long)blockIdx.y * gridDim.x + blockIdx.x - blk + cb) * kTile) + 32 * warp + lane;
-  float v[16];
+      P.part + ((long long)blockIdx.y * gridDim.x + blockIdx.x - blk + cb) * kTile) + half * kCh + c;
+  const long long step = (long long)nch * kTile / 4;
+  float v[8] = {};
+  for (int s0 = 0; s0 < j.nsplit; s0 += 8) {
+    float4 f[8][2];
 #pragma unroll
-  for (int q = 0; q < 16; ++q) v[q] = 0.0f;
-#pragma unroll 2
-  for (int s = 0; s < j.nsplit; ++s) {
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float4 f = __ldcg(src + ((long long)s * nch * kTile) / 4 + q * kCh);
-      v[4 * q] += f.x;
-      v[4 * q + 1] += f.y;
-      v[4 * q + 2] += f.z;
-      v[4 * q + 3] += f.w;
-    }
+      for (int q = 0; q < 2; ++q)
+        f[i][q] = s0 + i < j.nsplit ? __ldcg(src + (s0 + i) * step + q * kCh)
+                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        v[4 * q] += f[i][q].x;
+        v[4 * q + 1] += f[i][q].y;
+        v[4 * q + 2] += f[i][q].z;
+        v[4 * q + 3] += f[i][q].w;
+      }
   }
-  emit(v);
+  emit(v, ch0 + c, 4 * half);
 }
 
 int slices(int cols) { return (cols + kCols - 1) / kCols; }
