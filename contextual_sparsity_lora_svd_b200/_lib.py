@@ -463,7 +463,9 @@ def qk_rows(heads, X=None, g=None, Y=None, dY=None, dX=None, dg=None, idx=None, 
     r = QkRows(heads)
     first = X if X is not None else Y if Y is not None else dX
     if first is None:
-        first = next(t for t in (X_ctx, X_out, dX_ctx, dX_out, dY) if t is not None)
+        first = next((t for t in (X_ctx, X_out, dX_ctx, dX_out, dY) if t is not None), None)
+        if first is None:
+            raise ValueError("rows without a tensor")
     dt = first.dtype
     r.dt = _DTYPES.get(dt)
     if r.dt is None:
@@ -471,8 +473,11 @@ def qk_rows(heads, X=None, g=None, Y=None, dY=None, dX=None, dg=None, idx=None, 
     if X is not None:
         r.X, r.ldx = _rows(X, "X")
     if Y is not None:
-        r.Y, r.ldy = _rows(Y, "Y")
-        _same(Y, "Y", dt)
+        if Y is X:
+            r.Y, r.ldy = r.X, r.ldx
+        else:
+            r.Y, r.ldy = _rows(Y, "Y")
+            _same(Y, "Y", dt)
     if dX is not None:
         r.dX, r.lddx = _rows(dX, "dX")
         _same(dX, "dX", dt)
@@ -527,14 +532,16 @@ def _qk(fn, head, batch, seq, head_dim, q, k, rotary_, pos, eps, ctx_len, ws, st
     if q.scratch or (k is not None and k.scratch):
         _run(fn, args, ws, stream)
     else:
-        _run_plain(fn, args, q, stream)
+        _run_plain(fn, args, stream)
     del keep
 
 
-def _run_plain(fn_name, args, anything, stream):
+_NO_BYTES = ctypes.byref(c_sz(0))  # written by workspace queries alone
+
+
+def _run_plain(fn_name, args, stream):
     """A call that needs no scratch: any non-null workspace address runs it."""
-    st = getattr(_lib, fn_name)(*args, ctypes.addressof(anything) & ~15, ctypes.byref(c_sz(0)),
-                                _stream(stream))
+    st = getattr(_lib, fn_name)(*args, 16, _NO_BYTES, _stream(stream))
     if st:
         _check(fn_name, st)
 
@@ -583,14 +590,14 @@ def slora_act8_pack(X, codes, scales, stream=None):
     T, d = X.shape
     px, ldx = _rows(X, "X")
     c = act8(codes, scales, T, d)
-    _run_plain("slora_act8_pack", [dtype_code(X), T, d, px, ldx, ctypes.byref(c)], c, stream)
+    _run_plain("slora_act8_pack", [dtype_code(X), T, d, px, ldx, ctypes.byref(c)], stream)
 
 
 def slora_act8_unpack(codes, scales, X, stream=None):
     T, d = X.shape
     px, ldx = _rows(X, "X")
     c = act8(codes, scales, T, d)
-    _run_plain("slora_act8_unpack", [dtype_code(X), T, d, ctypes.byref(c), px, ldx], c, stream)
+    _run_plain("slora_act8_unpack", [dtype_code(X), T, d, ctypes.byref(c), px, ldx], stream)
 
 
 def slora_rmsnorm_fwd_act8(X, g, N, rstd=None, A=None, H=None, H8=None, N8=None, eps=RMS_EPS,
@@ -601,7 +608,7 @@ def slora_rmsnorm_fwd_act8(X, g, N, rstd=None, A=None, H=None, H8=None, N8=None,
     n8 = None if N8 is None else act8(*N8, T, d)
     _run_plain("slora_rmsnorm_fwd_act8",
                [BF16, T, d, eps, ptr(X), ptr(A), ptr(g), ptr(H), ptr(N), ptr(rstd), _ref(h8),
-                _ref(n8)], n8 or h8 or Act8(), stream)
+                _ref(n8)], stream)
 
 
 def slora_rmsnorm_bwd_act8(H8, rstd, g, dN0, dX, dN1=None, dN2=None, dRes=None, stream=None):
@@ -609,7 +616,7 @@ def slora_rmsnorm_bwd_act8(H8, rstd, g, dN0, dX, dN1=None, dN2=None, dRes=None, 
     h8 = act8(*H8, T, d)
     _run_plain("slora_rmsnorm_bwd_act8",
                [BF16, T, d, ctypes.byref(h8), ptr(rstd), ptr(g), ptr(dN0), ptr(dN1), ptr(dN2),
-                ptr(dRes), ptr(dX)], h8, stream)
+                ptr(dRes), ptr(dX)], stream)
 
 
 def slora_linear_bwd_act8(side, batch, seq, ctx_len, k, n, W, A, B, lora_scale, idx, X8_ctx,
