@@ -48,12 +48,13 @@ __device__ int g_qk_bad_index = 0;
 namespace {
 
 constexpr int kWarps = 8;  // of a block, fewer where sliced rows need the shared memory
+constexpr int kSmallBatch = 64;  // sequences whose offsets travel in the parameters
 
 struct QkPart {
   const void* X;
   long long ldx;
   const void *Xc, *Xo;
-  const int32_t* inv;
+  const int32_t* idx;
   int n_idx;
   const void* g;
   void* out;  // Y, or dX
@@ -69,7 +70,9 @@ struct QkParams {
   QkPart part[2];
   unsigned long long turns[kMaxHeadDim / 2];
   const int32_t* pos;
-  const int32_t* ctx_off;  // sliced: context rows before sequence b, [batch + 1]
+  // sliced: context rows before sequence b, [batch + 1]; up to kSmallBatch in `off`
+  const int32_t* ctx_off;
+  int off[kSmallBatch + 1];
   int T, seq, hd, dims, units, tl;
   int TC, batch, batch_pow;  // sliced: context rows, sequences, a power of two not above them
   int stage;  // sliced: elements of a warp's stage, a multiple of 8; the last 8 stay zero
@@ -390,16 +393,35 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
   // of a warp's item: x, then dy
   constexpr int kXBytes = 32 * item_bytes<T, V>(), kYBytes = kBwd ? 32 * item_bytes<G, V>() : 0;
   constexpr int kYAt = kRingX ? kXBytes : 0, kItemBytes = kYAt + kYBytes;
+  __shared__ int s_off[kSliced ? kSmallBatch + 1 : 1];
+  const int32_t* ctx_off = kSliced && P.batch <= kSmallBatch ? s_off : P.ctx_off;
   uint16_t* s_inv = nullptr;
   T* stage = nullptr;
   const unsigned skipped = P.stage - 8;
   if constexpr (kSliced) {
     s_inv = reinterpret_cast<uint16_t*>(rings + nwarps * ring_bytes<T, G, V, kBwd, kSliced>());
     stage = reinterpret_cast<T*>(s_inv + (n + 7) / 8 * 8) + warp * P.stage;
-    for (int i = tid; i < n; i += blockDim.x) {
-      const int at = q.inv[i];
-      s_inv[i] = uint16_t(at < 0 ? skipped : unsigned(at));
+    // every block inverts the list for itself (8 KB of indices from L2): a launch
+    // that did it once before cost 4 to 5 us
+    for (int i = tid; i < n; i += blockDim.x) s_inv[i] = uint16_t(skipped);
+    if (P.batch <= kSmallBatch)
+      for (int i = tid; i <= P.batch; i += blockDim.x) s_off[i] = P.off[i];
+    __syncthreads();
+    auto listed = [&](int i) {  // entry i's channel, or -1
+      const int c = q.idx[i];
+      return c >= 0 && c < n ? c : -1;
+    };
+#pragma unroll 4
+    for (int i = tid; i < q.n_idx; i += blockDim.x) {
+      const int c = listed(i);
+      if (c >= 0) s_inv[c] = uint16_t(i);
     }
+    __syncthreads();
+    if (blk == 0)  // outside its channels, or a later or earlier entry took the place
+      for (int i = tid; i < q.n_idx; i += blockDim.x) {
+        const int c = listed(i);
+        if (c < 0 || s_inv[c] != i) atomicExch(&g_qk_bad_index, 1);
+      }
     if (lane < 8) stage[skipped + lane] = from_f<T>(0.0f);
   }
   for (int p = tid; p < dims / 2; p += blockDim.x) s_turns[p] = P.turns[p];
@@ -723,10 +745,10 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
       int b = 0;
       for (int s = P.batch_pow; s; s >>= 1)
         if (b + s < P.batch) {
-          const int before = P.ctx_off[b + s];
+          const int before = ctx_off[b + s];
           if ((ctx ? before : (b + s) * P.seq - before) <= at) b += s;
         }
-      const int o0 = P.ctx_off[b], o1 = P.ctx_off[b + 1];
+      const int o0 = ctx_off[b], o1 = ctx_off[b + 1];
       w.kind = ctx ? at : -1 - at;
       w.t = ctx ? b * P.seq + (at - o0) : at + o1;
       const long long full = w.kind < 0 ? (long long)(-1 - w.kind) * n : 0;
@@ -909,31 +931,13 @@ __global__ void __launch_bounds__(1024) qk_dg_kernel(const __grid_constant__ DgP
   }
 }
 
-// Sliced rows: block 0 and 1 invert the channel lists (inv[channel] = column,
-// or -1), block 2 writes the context rows before every sequence.
-template <int CAP>
-struct SliceParams {
-  const int32_t* idx[2];
-  int32_t* inv[2];
-  int n_idx[2], n[2];
+// The context rows before every sequence of a large batch.
+struct OffsetParams {
   int32_t* ctx_off;
   int batch;
-  int ctx_len[CAP];
+  int ctx_len[kMaxBatch];
 };
-template <int CAP>
-__global__ void __launch_bounds__(1024) qk_slice_kernel(const __grid_constant__ SliceParams<CAP> p) {
-  if (blockIdx.x < 2) {
-    const int w = blockIdx.x;
-    if (!p.inv[w]) return;
-    for (int i = threadIdx.x; i < p.n[w]; i += blockDim.x) p.inv[w][i] = -1;
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.n_idx[w]; i += blockDim.x) {
-      const int c = p.idx[w][i];
-      if (c < 0 || c >= p.n[w] || atomicCAS(&p.inv[w][c], -1, i) != -1)
-        atomicExch(&g_qk_bad_index, 1);
-    }
-    return;
-  }
+__global__ void __launch_bounds__(1024) qk_offsets_kernel(const __grid_constant__ OffsetParams p) {
   // exclusive scan of ctx_len, 1024 sequences at a time (batch is at most kMaxBatch)
   __shared__ int part[1024];
   int carry = 0;
@@ -953,23 +957,6 @@ __global__ void __launch_bounds__(1024) qk_slice_kernel(const __grid_constant__ 
     carry += part[1023];
     __syncthreads();
   }
-}
-
-template <int CAP>
-void launch_slices(const QkDesc& D, const slora_tokens* tok, int32_t* const* inv, int32_t* ctx_off,
-                   cudaStream_t st) {
-  SliceParams<CAP> p{};
-  for (int i = 0; i < D.nparts; ++i) {
-    if (!D.part[i].idx) continue;
-    p.idx[i] = D.part[i].idx;
-    p.inv[i] = inv[i];
-    p.n_idx[i] = D.part[i].n_idx;
-    p.n[i] = D.part[i].heads * D.head_dim;
-  }
-  p.ctx_off = ctx_off;
-  p.batch = D.ti.batch;
-  for (int b = 0; b < D.ti.batch; ++b) p.ctx_len[b] = tok->ctx_len[b];
-  qk_slice_kernel<CAP><<<3, 1024, 0, st>>>(p);
 }
 
 struct Geometry {
@@ -1150,27 +1137,26 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
   const int V = vector_width(D, backward);
   const Shape shape = block_shape(D, backward, sliced, V);
   const int max_blocks = num_sms() * std::max(shape.per_sm, 1);
-  int32_t* inv[2] = {nullptr, nullptr};
   int32_t* ctx_off = nullptr;
   float* dgp = nullptr;
-  if (sliced) {
-    ctx_off = ar.take<int32_t>(size_t(D.ti.batch) + 1);
-    for (int i = 0; i < D.nparts; ++i)
-      if (D.part[i].idx) inv[i] = ar.take<int32_t>(size_t(D.part[i].heads) * hd);
-  }
+  if (sliced) ctx_off = ar.take<int32_t>(size_t(D.ti.batch) + 1);
   // one partial of each block; the parts' blocks together are at most max_blocks + 1
   if (any_dg) dgp = ar.take<float>(size_t(max_blocks + 1) * hd);
   if (plan) return SLORA_OK;
   SLORA_TRY(arena_fits(ar, "qk_rotary"));
 
-  if (sliced) {
+  QkParams P{};
+  if (sliced && D.ti.batch <= kSmallBatch) {
+    for (int b = 0; b < D.ti.batch; ++b) P.off[b + 1] = P.off[b] + tok->ctx_len[b];
+  } else if (sliced) {
+    OffsetParams o{};
+    o.ctx_off = ctx_off;
+    o.batch = D.ti.batch;
+    std::copy(tok->ctx_len, tok->ctx_len + D.ti.batch, o.ctx_len);
     LaunchScope ls(kAux, double(D.ti.batch) * 4, st);
-    if (D.ti.batch <= 64) launch_slices<64>(D, tok, inv, ctx_off, st);
-    else launch_slices<kMaxBatch>(D, tok, inv, ctx_off, st);
+    qk_offsets_kernel<<<1, 1024, 0, st>>>(o);
     SLORA_CHECK_LAUNCH();
   }
-
-  QkParams P{};
   P.pos = D.pos;
   P.ctx_off = ctx_off;
   P.T = int(D.ti.T);
@@ -1213,7 +1199,7 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
     const slora_qk_rows& s = D.part[i];
     QkPart& q = P.part[i];
     q.X = s.X; q.ldx = s.ldx; q.Xc = s.X_ctx; q.Xo = s.X_out;
-    q.inv = inv[i]; q.n_idx = s.n_idx; q.g = s.g; q.heads = s.heads;
+    q.idx = s.idx; q.n_idx = s.n_idx; q.g = s.g; q.heads = s.heads;
     if (backward) {
       q.out = s.dX; q.ldo = s.lddx; q.outc = s.dX_ctx; q.outo = s.dX_out;
       q.dY = s.dY; q.ldy = s.lddy;
