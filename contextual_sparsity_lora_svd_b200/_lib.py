@@ -454,6 +454,17 @@ def _same(t, what, dt):
         raise TypeError(f"{what} is {t.dtype}, the rows are {dt}")
 
 
+def _fit(t, what, n, dt):
+    """Address of a contiguous tensor of n elements (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not dt:
+        raise TypeError(f"{what} is {t.dtype}, not {dt}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous tensor of {n} elements is needed")
+    return t.data_ptr() or None
+
+
 def qk_rows(heads, X=None, g=None, Y=None, dY=None, dX=None, dg=None, idx=None, X_ctx=None,
             X_out=None, dX_ctx=None, dX_out=None) -> QkRows:
     """The rows of q or k for slora_qk_rotary_fwd / _bwd: dense (X, Y, dX may
@@ -516,6 +527,26 @@ def _whole_sequences(batch, seq):
     return make_tokens(batch, seq, [seq] * batch)
 
 
+def _sizes(r, T, head_dim, ctx_len):
+    """Refuses tensors of a qk_rows that do not hold T rows of its heads."""
+    n = r.heads * head_dim
+    X, g, Y, dY, dX, dg, idx, X_ctx, X_out, dX_ctx, dX_out = r.tensors
+    shape = (T, n)
+    for t in (X, None if Y is X else Y, dY, None if dX is dY else dX):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"rows of {T} x {n} are needed, not {tuple(t.shape)}")
+    if g is not None or dg is not None:
+        for t in (g, dg):
+            if t is not None and t.numel() != head_dim:
+                raise ValueError(f"g and dg have one value a channel of a head, {head_dim}")
+    if idx is not None:
+        TC = T if ctx_len is None else sum(ctx_len)
+        for t, want in ((X_ctx, TC * r.n_idx), (dX_ctx, TC * r.n_idx), (X_out, (T - TC) * n),
+                        (dX_out, (T - TC) * n)):
+            if t is not None and t.numel() != want:
+                raise ValueError(f"sliced rows: {want} elements are needed, not {t.numel()}")
+
+
 def _qk(fn, head, batch, seq, head_dim, q, k, rotary_, pos, eps, ctx_len, ws, stream):
     tok, keep = (_whole_sequences(batch, seq) if ctx_len is None
                  else make_tokens(batch, seq, ctx_len))
@@ -527,6 +558,9 @@ def _qk(fn, head, batch, seq, head_dim, q, k, rotary_, pos, eps, ctx_len, ws, st
         if k.dt != q.dt or k.gdt != q.gdt:
             raise TypeError("q and k have the same dtypes")
         kr = ctypes.byref(k)
+    _sizes(q, batch * seq, head_dim, ctx_len)
+    if k is not None:
+        _sizes(k, batch * seq, head_dim, ctx_len)
     args = head + [ctypes.byref(tok), head_dim, eps, ctypes.byref(rotary_ or rotary()), ptr(pos),
                    ctypes.byref(q), kr]
     if q.scratch or (k is not None and k.scratch):
@@ -562,6 +596,7 @@ def slora_qk_rotary_bwd(batch, seq, head_dim, q, k=None, rotary=None, pos=None, 
 
 # ------------------------------------------- 8-bit activation checkpoints
 ACT8_BLOCK = 32
+BF = torch.bfloat16
 
 
 def act8_empty(T, d, device="cuda"):
@@ -607,16 +642,19 @@ def slora_rmsnorm_fwd_act8(X, g, N, rstd=None, A=None, H=None, H8=None, N8=None,
     h8 = None if H8 is None else act8(*H8, T, d)
     n8 = None if N8 is None else act8(*N8, T, d)
     _run_plain("slora_rmsnorm_fwd_act8",
-               [BF16, T, d, eps, ptr(X), ptr(A), ptr(g), ptr(H), ptr(N), ptr(rstd), _ref(h8),
-                _ref(n8)], stream)
+               [BF16, T, d, eps, _fit(X, "X", T * d, BF), _fit(A, "A", T * d, BF),
+                _fit(g, "g", d, BF), _fit(H, "H", T * d, BF), _fit(N, "N", T * d, BF),
+                _fit(rstd, "rstd", T, torch.float32), _ref(h8), _ref(n8)], stream)
 
 
 def slora_rmsnorm_bwd_act8(H8, rstd, g, dN0, dX, dN1=None, dN2=None, dRes=None, stream=None):
     T, d = dN0.shape
     h8 = act8(*H8, T, d)
     _run_plain("slora_rmsnorm_bwd_act8",
-               [BF16, T, d, ctypes.byref(h8), ptr(rstd), ptr(g), ptr(dN0), ptr(dN1), ptr(dN2),
-                ptr(dRes), ptr(dX)], stream)
+               [BF16, T, d, ctypes.byref(h8), _fit(rstd, "rstd", T, torch.float32),
+                _fit(g, "g", d, BF), _fit(dN0, "dN0", T * d, BF), _fit(dN1, "dN1", T * d, BF),
+                _fit(dN2, "dN2", T * d, BF), _fit(dRes, "dRes", T * d, BF),
+                _fit(dX, "dX", T * d, BF)], stream)
 
 
 def slora_linear_bwd_act8(side, batch, seq, ctx_len, k, n, W, A, B, lora_scale, idx, X8_ctx,
@@ -626,14 +664,20 @@ def slora_linear_bwd_act8(side, batch, seq, ctx_len, k, n, W, A, B, lora_scale, 
     for SLICE_IN_COLS, X8_out are (codes, scales)."""
     tok, keep = make_tokens(batch, seq, ctx_len)
     n_idx = 0 if idx is None else idx.numel()
-    T, TC = batch * seq, sum(int(c) for c in ctx_len)
-    cols = side == SLICE_IN_COLS
+    T, TC, r = batch * seq, sum(int(c) for c in ctx_len), A.shape[0]
+    cols, rows = side == SLICE_IN_COLS, side == SLICE_OUT_ROWS
     xc = None if X8_ctx is None else act8(*X8_ctx, TC if cols else T, n_idx if cols else k)
     xo = None if X8_out is None else act8(*X8_out, T - TC, k)
     # an empty channel list is still a list: its address, never read, may be null
-    pidx = ptr(idx) or (None if idx is None else ptr(XA_save))
+    pidx = _fit(idx, "idx", n_idx, torch.int32) or (None if idx is None else ptr(XA_save))
+    f32 = torch.float32
     _run("slora_linear_bwd_act8",
-         [dtype_code(W), ctypes.byref(tok), k, n, ptr(W), ptr(A), ptr(B), A.shape[0],
-          float(lora_scale), side, pidx, n_idx, _ref(xc), _ref(xo), ptr(XA_save),
-          ptr(dY_ctx), ptr(dY_out), ptr(dX_ctx), ptr(dX_out), ptr(dA), ptr(dB)], ws, stream)
+         [dtype_code(W), ctypes.byref(tok), k, n, _fit(W, "W", n * k, BF), _fit(A, "A", r * k, BF),
+          _fit(B, "B", n * r, BF), r, float(lora_scale), side, pidx, n_idx, _ref(xc), _ref(xo),
+          _fit(XA_save, "XA_save", T * r, f32),
+          _fit(dY_ctx, "dY_ctx", TC * n_idx if rows else T * n, BF),
+          _fit(dY_out, "dY_out", (T - TC) * n, BF),
+          _fit(dX_ctx, "dX_ctx", TC * n_idx if cols else T * k, BF),
+          _fit(dX_out, "dX_out", (T - TC) * k, BF), _fit(dA, "dA", r * k, f32),
+          _fit(dB, "dB", n * r, f32)], ws, stream)
     del keep

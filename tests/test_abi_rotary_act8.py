@@ -58,10 +58,10 @@ def test_dense_calls_need_no_workspace(L):
     assert st == OK and need >= 64 * 4
 
 
-def test_sliced_calls_need_the_channel_maps(L):
+def test_sliced_calls_need_a_workspace(L):
     s = dict(idx=FAKE, n_idx=100, X=None, X_ctx=FAKE, X_out=FAKE, dX_ctx=FAKE, dX_out=FAKE)
     st, need = fwd(L, dense(L, **s))
-    assert st == OK and need >= 4 * 64 * 4 + 3 * 4
+    assert st == OK and need >= 3 * 4                                  # the sequences' offsets
     assert bwd(L, dense(L, **s))[0] == OK
     assert fwd(L, dense(L, **s), dense(L, 2))[0] == SHAPE              # one sliced, one dense
     assert fwd(L, dense(L, **s), dt=L.F32)[0] == UNSUPPORTED
@@ -129,6 +129,36 @@ def test_binding_refuses_wrong_tensors(L):
         L.slora_qk_rotary_fwd(2, 2, 64, L.qk_rows(2, X=X, Y=X), pos=torch.zeros(4), stream=0)
     with pytest.raises(KeyError):
         L.rotary(scaling="other")
+
+
+def test_binding_refuses_sizes_that_do_not_fit(L):
+    """A tensor too small for the call is refused before any address leaves the binding."""
+    bf, f32 = torch.bfloat16, torch.float32
+    z = lambda *s, dt=bf: torch.zeros(*s, dtype=dt)  # noqa: E731
+    for rows in (L.qk_rows(2, X=z(3, 128), Y=z(4, 128)), L.qk_rows(2, X=z(4, 64), Y=z(4, 64)),
+                 L.qk_rows(2, X=z(4, 128), Y=z(4, 128), g=z(63)),
+                 L.qk_rows(2, idx=z(5, dt=torch.int32), X_ctx=z(2, 5), X_out=z(1, 128), Y=z(4, 128)),
+                 L.qk_rows(2, idx=z(5, dt=torch.int32), X_ctx=z(2, 4), X_out=z(2, 128), Y=z(4, 128))):
+        with pytest.raises(ValueError):
+            L.slora_qk_rotary_fwd(2, 2, 64, rows, ctx_len=[1, 1], stream=0)
+    with pytest.raises(ValueError):
+        L.qk_rows(2)
+    H8 = (z(4, 64, dt=torch.int8), z(4, 2, dt=torch.uint8))
+    good = dict(X=z(4, 64), g=z(64), N=z(4, 64), rstd=z(4, dt=f32), H8=H8)
+    for name, t, err in (("g", z(32), ValueError), ("N", z(3, 64), ValueError), ("N", z(4, 64, dt=f32), TypeError),
+                         ("X", z(64, 4).t(), ValueError), ("rstd", z(4), TypeError),
+                         ("H8", (H8[0][:3], H8[1]), ValueError)):
+        with pytest.raises(err):
+            L.slora_rmsnorm_fwd_act8(**dict(good, **{name: t}), stream=0)
+    with pytest.raises(ValueError):
+        L.slora_rmsnorm_bwd_act8(H8, z(4, dt=f32), z(64), z(4, 64), z(5, 64), stream=0)
+    lin = dict(side=L.SLICE_OUT_ROWS, batch=2, seq=2, ctx_len=[1, 1], k=64, n=64, W=z(64, 64), A=z(8, 64),
+               B=z(64, 8), lora_scale=1.0, idx=z(16, dt=torch.int32), X8_ctx=H8, XA_save=z(4, 8, dt=f32),
+               dY_ctx=z(2, 16), dY_out=z(2, 64), dX_ctx=z(4, 64), dA=z(8, 64, dt=f32), dB=z(64, 8, dt=f32))
+    for name, t in (("W", z(64, 32)), ("B", z(8, 8)), ("XA_save", z(2, 8, dt=f32)), ("dY_ctx", z(2, 15)),
+                    ("dY_out", z(1, 64)), ("dX_ctx", z(2, 64)), ("dA", z(8, 32, dt=f32))):
+        with pytest.raises(ValueError):
+            L.slora_linear_bwd_act8(**dict(lin, **{name: t}), stream=0)
 
 
 def test_act8_refusals(L):
