@@ -104,7 +104,9 @@ int slora_version(void);
  *                          outside its weight: the library replaced it by
  *                          channel 0 before any kernel read through it, so
  *                          that call's results are wrong but no memory
- *                          outside the caller's buffers was touched;
+ *                          outside the caller's buffers was touched
+ *                          (slora_linear_bwd_act8 and slora_qk_rotary_* leave
+ *                          the entry out instead, see there);
  *   SLORA_ERR_TIMEOUT      a pipeline wait inside a kernel gave up (its
  *                          call's outputs are undefined);
  *   SLORA_OK               neither happened since the last clear.
@@ -571,8 +573,10 @@ typedef struct {
  *             overlap.
  * Angles are exact to about 1e-7 at every position: the turns are counted in
  * 64-bit fixed point.  Sliced tensors need a workspace; dense ones none.
- * A sliced tensor's entry outside its channels, or twice in idx, is left out
- * and reported by slora_device_error (SLORA_ERR_INVALID_ARG).
+ * A sliced tensor has at most 32768 channels (heads * head_dim).  An entry of
+ * idx outside them, or one that stands there twice, is left out (of two, either)
+ * and reported by slora_device_error (SLORA_ERR_INVALID_ARG); the backward
+ * leaves its column of dX_ctx as it was or undefined.
  */
 slora_status slora_qk_rotary_fwd(slora_dtype dt, const slora_tokens* tok, int head_dim, float eps,
                                  const slora_rotary* rot, const int32_t* pos,
@@ -646,7 +650,9 @@ slora_status slora_rmsnorm_bwd_act8(slora_dtype dt, int64_t T, int64_t d, const 
  * X_ctx (and X_out, for SLORA_SLICE_IN_COLS) of the same shapes, read as codes
  * by the dA contraction itself.  SLORA_BF16 only.  The rank-r operands dY B and
  * XA_save enter the sums in fp32, so dA and dB are exact to fp32 rounding for
- * the values that the checkpoint holds.
+ * the values that the checkpoint holds.  The same call gives the same bits.  An
+ * entry of idx outside the weight counts as a channel of zeros and is reported
+ * by slora_device_error (SLORA_ERR_INVALID_ARG).
  */
 slora_status slora_linear_bwd_act8(slora_dtype dt, const slora_tokens* tok, int64_t k, int64_t n,
                                    const void* W, const void* A, const void* B, int r_lora,
