@@ -17,11 +17,18 @@
 // sixteen warps take every sixteenth 32-channel group and are summed in order
 // in shared memory: no partial sums leave the block.  p is written as the
 // GEMM's LoRA operand (bf16) and as the three bf16 terms that rank_sums reads.
+// 12.7 us for 4096 x 4096 (5 for the 34 MB of dY from memory): every block reads
+// all of B's copy from L2, as much as its rows of dY.  Clusters of four blocks
+// that split the channels of 64 rows read a quarter of that, and took 20 us.
+//
+// lora_setup takes 8 us for the q projection of 4096 rows at half its channels
+// (27 us in six launches before), 14 us for a down projection of 11008 (53 us).
 //
 // rank_sums: tcgen05.mma with 128 channels as M, the tokens as the reduction and
 // N = 48: 16 rank columns in three bf16 terms (an fp32 operand to 2^-24), so the
-// sums are those of fp32 operands.  For 4096 x 4096 codes at r = 16, legacy
-// mma.sync took 21 us and packed fp32 FMAs 30 us.  X lies in shared memory as
+// sums are those of fp32 operands.  For 4096 x 4096 codes at r = 16 they take
+// 15 us (legacy mma.sync 21, packed fp32 FMAs 30): 2 until the first stage is in,
+// 6 for the stages, 1.5 to hand the partial sums over, 2 to join them.  X lies in shared memory as
 // it does in global memory, a token's 128 channels in a row (an M-major operand,
 // 128-byte swizzle): bf16 rows and the rank operand's terms come by TMA; codes
 // come by TMA into a ring and eight warps expand them into the operand (a byte

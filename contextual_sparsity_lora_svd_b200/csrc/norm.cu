@@ -10,7 +10,9 @@
 // The variants with 8-bit checkpoints (act8.cuh) write the codes of H and N in
 // the same pass (a 32-channel block is four neighbouring lanes' chunks, its
 // maximum two shuffles), and read H as codes in the backward: 1.03 bytes a
-// value in place of 2, and no separate pass over H and N to pack them.
+// value in place of 2, and no separate pass over H and N to pack them.  At
+// 4096 x 4096: forward 26 us (169 MB), backward 25 us (118 MB; every value of a
+// row is on its way before the first use, 24 warps an SM).
 #include "act8.cuh"
 #include "act8_dev.cuh"
 #include "attention.cuh"
