@@ -90,6 +90,8 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) act8_pack_kernel(
     const T* __restrict__ X, int64_t ldx, int64_t d, uint32_t total, const FastDiv per_row,
     bool vec, uint2* __restrict__ codes, uint8_t* __restrict__ scales) {
+  grid_wait();
+  grid_ahead();
   constexpr bool kF = std::is_same<T, float>::value;
   const uint32_t base = blockIdx.x * uint32_t(kThreads * kChunks) + threadIdx.x;
   float f[kF ? kChunks : 1][8];
@@ -126,6 +128,8 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) act8_unpack_kernel(
     const uint2* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t ldx, int64_t d,
     uint32_t total, const FastDiv per_row, bool vec, T* __restrict__ X) {
+  grid_wait();
+  grid_ahead();
   const uint32_t base = blockIdx.x * uint32_t(kThreads * kChunks) + threadIdx.x;
   uint2 c[kChunks];
   uint32_t b[kChunks];
@@ -171,12 +175,13 @@ slora_status act8_pack_run(int dt, int64_t T, int64_t d, const void* X, int64_t 
     uint8_t* scales = out.scales + t0 * (d32 / kActBlock);
     LaunchScope ls(kElementwise, double(rows) * d * (dt_size(dt) + 1.03125), st);
     if (dt == kF32)
-      act8_pack_kernel<float><<<grid, kThreads, 0, st>>>(static_cast<const float*>(X) + t0 * ldx,
-                                                         ldx, d, total, fd, vec, codes, scales);
+      SLORA_CUDA(launch_early(act8_pack_kernel<float>, dim3(grid), kThreads, 0, st,
+                              static_cast<const float*>(X) + t0 * ldx, ldx, d, total, fd, vec,
+                              codes, scales));
     else
-      act8_pack_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(
-          static_cast<const __nv_bfloat16*>(X) + t0 * ldx, ldx, d, total, fd, vec, codes, scales);
-    SLORA_CHECK_LAUNCH();
+      SLORA_CUDA(launch_early(act8_pack_kernel<__nv_bfloat16>, dim3(grid), kThreads, 0, st,
+                              static_cast<const __nv_bfloat16*>(X) + t0 * ldx, ldx, d, total, fd,
+                              vec, codes, scales));
   }
   return SLORA_OK;
 }
@@ -195,12 +200,12 @@ slora_status act8_unpack_run(int dt, int64_t T, int64_t d, const slora_act8& in,
     const uint8_t* scales = in.scales + t0 * (d32 / kActBlock);
     LaunchScope ls(kElementwise, double(rows) * d * (dt_size(dt) + 1.03125), st);
     if (dt == kF32)
-      act8_unpack_kernel<float><<<grid, kThreads, 0, st>>>(
-          codes, scales, ldx, d, total, fd, vec, static_cast<float*>(X) + t0 * ldx);
+      SLORA_CUDA(launch_early(act8_unpack_kernel<float>, dim3(grid), kThreads, 0, st, codes, scales,
+                              ldx, d, total, fd, vec, static_cast<float*>(X) + t0 * ldx));
     else
-      act8_unpack_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(
-          codes, scales, ldx, d, total, fd, vec, static_cast<__nv_bfloat16*>(X) + t0 * ldx);
-    SLORA_CHECK_LAUNCH();
+      SLORA_CUDA(launch_early(act8_unpack_kernel<__nv_bfloat16>, dim3(grid), kThreads, 0, st, codes,
+                              scales, ldx, d, total, fd, vec,
+                              static_cast<__nv_bfloat16*>(X) + t0 * ldx));
   }
   return SLORA_OK;
 }

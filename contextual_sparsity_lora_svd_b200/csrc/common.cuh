@@ -128,6 +128,34 @@ struct LaunchScope {
   int slot_;
 };
 
+// A kernel that starts while the one before it on the stream ends: its blocks are
+// placed as soon as every block of that one has called grid_ahead() (or ended) and
+// an SM has room, and wait in grid_wait() until that grid has ended and its writes
+// are visible.  Every thread calls grid_wait() before it touches memory that
+// another kernel may write or read; a grid that waits there has also waited for
+// all before it.  After a kernel that never calls grid_ahead() it starts at its end.
+__device__ __forceinline__ void grid_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void grid_ahead() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                         cudaStream_t st, const A&... args) {
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // ------------------------------------------------------------- elements
 __device__ __forceinline__ float ld_elem(const void* p, int64_t i, int dt) {
   if (dt == kF32) return static_cast<const float*>(p)[i];

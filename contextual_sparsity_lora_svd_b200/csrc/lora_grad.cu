@@ -103,6 +103,8 @@ __device__ __forceinline__ void put_terms(__nv_bfloat16* o, long long plane, flo
 template <int CAP>
 __global__ void __launch_bounds__(kSetupThreads)
     lora_setup_kernel(const __grid_constant__ SetupParams<CAP> P) {
+  grid_wait();
+  grid_ahead();
   const LoraSetup& d = P.d;
   const int tid = threadIdx.x, blk = blockIdx.x, seq = P.seq;
   if (blk < P.w0) {  // tile lists and counters
@@ -221,6 +223,8 @@ struct RowsParams {
 __global__ void __launch_bounds__(kRowWarps * 32, 2)
     rank_rows_kernel(const __grid_constant__ RowsParams P) {
   __shared__ float red[kRowWarps][16][kCols + 1];
+  grid_wait();
+  grid_ahead();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const bool second = int(blockIdx.x) >= P.blocks0;
   const RowsJob& j = P.job[second ? 1 : 0];
@@ -478,6 +482,7 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
     mbar_init(&done, 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    grid_wait();
     for (int st = 0; st < min(stages, kRing); ++st) copy(st);
   }
   if (warp == kXWarps) {
@@ -487,6 +492,8 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  grid_wait();
+  grid_ahead();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -757,8 +764,7 @@ slora_status setup(const LoraSetup& d, const slora_tokens* tok, const TokenInfo&
   double bytes = double(ti.T) * cols * (4 + 2 * kTerms) + 4.0 * double(d.W.n) * d.wcols;
   for (int i = 0; i < 2; ++i) bytes += 4.0 * double(d.B[i].n + d.A[i].n) * cols;
   LaunchScope ls(kAux, bytes, st);
-  lora_setup_kernel<CAP><<<unsigned(at), kSetupThreads, 0, st>>>(p);
-  SLORA_CHECK_LAUNCH();
+  SLORA_CUDA(launch_early(lora_setup_kernel<CAP>, dim3(unsigned(at)), kSetupThreads, 0, st, p));
   return SLORA_OK;
 }
 }  // namespace
@@ -795,9 +801,9 @@ slora_status rank_rows(const RankRows* jobs, int n, int cols, float s, cudaStrea
   p.cp = int(padded_cols(cols));
   p.s = s;
   LaunchScope ls(kSkinny, bytes, st);
-  rank_rows_kernel<<<dim3(unsigned(blocks[0] + blocks[1]), unsigned(slices(cols))),
-                     kRowWarps * 32, 0, st>>>(p);
-  SLORA_CHECK_LAUNCH();
+  SLORA_CUDA(launch_early(rank_rows_kernel,
+                          dim3(unsigned(blocks[0] + blocks[1]), unsigned(slices(cols))),
+                          kRowWarps * 32, 0, st, p));
   return SLORA_OK;
 }
 
@@ -864,8 +870,8 @@ slora_status rank_sums(const RankSum* jobs, int n, int cols, float scale, float*
   SLORA_CUDA(cudaFuncSetAttribute(rank_sums_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   kSumSmem));
   LaunchScope ls(kSkinny, bytes * slices(cols), st);
-  rank_sums_kernel<<<dim3(unsigned(blocks), unsigned(slices(cols))), kSumThreads, kSumSmem, st>>>(p);
-  SLORA_CHECK_LAUNCH();
+  SLORA_CUDA(launch_early(rank_sums_kernel, dim3(unsigned(blocks), unsigned(slices(cols))),
+                          kSumThreads, kSumSmem, st, p));
   return SLORA_OK;
 }
 

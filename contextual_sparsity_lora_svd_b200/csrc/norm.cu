@@ -248,6 +248,8 @@ __global__ void __launch_bounds__(kRowThreads)
                             uint8_t* __restrict__ h8s, uint2* __restrict__ n8,
                             uint8_t* __restrict__ n8s) {
   __shared__ float red[4];
+  grid_wait();
+  grid_ahead();
   const int64_t o = int64_t(blockIdx.x) * nch;
   const int nchp = (nch + 3) & ~3;  // chunks of a checkpoint's row
   const int64_t o8 = int64_t(blockIdx.x) * nchp;
@@ -317,6 +319,8 @@ __global__ void __launch_bounds__(kRowThreads)
                             const uint4* __restrict__ dN2, const uint4* __restrict__ dRes,
                             int nch, uint4* __restrict__ dX) {
   __shared__ float red[4];
+  grid_wait();
+  grid_ahead();
   const int64_t o = int64_t(blockIdx.x) * nch, o8 = int64_t(blockIdx.x) * ((nch + 3) & ~3);
   // every input of the row is on its way before the first use
   uint2 hc[CPT];
@@ -445,17 +449,19 @@ slora_status rmsnorm_bwd_run(const void* Hin, const float* rstd, const void* g, 
   return SLORA_OK;
 }
 
+#define SLORA_ROW(KERNEL, ...) \
+  SLORA_CUDA(launch_early(KERNEL, dim3(rows), kRowThreads, 0, st, __VA_ARGS__))
 #define SLORA_ROW_SWITCH(KERNEL, ...)                                             \
   if (nch <= kRowThreads) {                                                       \
-    KERNEL<1><<<rows, kRowThreads, 0, st>>>(__VA_ARGS__);                         \
+    SLORA_ROW(KERNEL<1>, __VA_ARGS__);                                            \
   } else if (nch <= 2 * kRowThreads) {                                            \
-    KERNEL<2><<<rows, kRowThreads, 0, st>>>(__VA_ARGS__);                         \
+    SLORA_ROW(KERNEL<2>, __VA_ARGS__);                                            \
   } else if (nch <= 4 * kRowThreads) {                                            \
-    KERNEL<4><<<rows, kRowThreads, 0, st>>>(__VA_ARGS__);                         \
+    SLORA_ROW(KERNEL<4>, __VA_ARGS__);                                            \
   } else if (nch <= 8 * kRowThreads) {                                            \
-    KERNEL<8><<<rows, kRowThreads, 0, st>>>(__VA_ARGS__);                         \
+    SLORA_ROW(KERNEL<8>, __VA_ARGS__);                                            \
   } else {                                                                        \
-    KERNEL<16><<<rows, kRowThreads, 0, st>>>(__VA_ARGS__);                        \
+    SLORA_ROW(KERNEL<16>, __VA_ARGS__);                                           \
   }
 
 slora_status rmsnorm_fwd_act8_run(const void* X, const void* A, const void* g, int64_t T,
@@ -476,7 +482,6 @@ slora_status rmsnorm_fwd_act8_run(const void* X, const void* A, const void* g, i
   uint8_t* n8s = N8 ? N8->scales : nullptr;
   const unsigned rows = unsigned(T);
   SLORA_ROW_SWITCH(rmsnorm_fwd_act8_kernel, x, a, gg, nch, eps, h, n, rstd, h8, h8s, n8, n8s)
-  SLORA_CHECK_LAUNCH();
   return SLORA_OK;
 }
 
@@ -497,7 +502,6 @@ slora_status rmsnorm_bwd_act8_run(const slora_act8& H8, const float* rstd, const
   auto* dx = static_cast<uint4*>(dX);
   const unsigned rows = unsigned(T);
   SLORA_ROW_SWITCH(rmsnorm_bwd_act8_kernel, h8, H8.scales, rstd, gg, n0, n1, n2, res, nch, dx)
-  SLORA_CHECK_LAUNCH();
   return SLORA_OK;
 }
 

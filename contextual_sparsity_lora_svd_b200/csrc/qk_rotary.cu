@@ -384,6 +384,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
   // is not computed: the stage's zero) and a stage a warp
   extern __shared__ __align__(16) float smem[];
   __shared__ unsigned long long s_turns[kMaxHeadDim / 2];
+  grid_wait();
+  grid_ahead();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nwarps = blockDim.x >> 5;
   const bool second = int(blockIdx.x) >= P.part[0].blocks;
   const QkPart q = second ? P.part[1] : P.part[0];  // (in registers: read in every round)
@@ -920,6 +922,8 @@ __global__ void __launch_bounds__(1024) qk_dg_kernel(const __grid_constant__ DgP
   __shared__ float red[32][33];
   const int which = blockIdx.y, cl = threadIdx.x & 31, gr = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + cl;
+  grid_wait();
+  grid_ahead();
   if (!p.dg[which]) return;
   float v = 0.0f;
   if (c < p.hd)
@@ -944,6 +948,8 @@ struct OffsetParams {
 __global__ void __launch_bounds__(1024) qk_offsets_kernel(const __grid_constant__ OffsetParams p) {
   // exclusive scan of ctx_len, 1024 sequences at a time (batch is at most kMaxBatch)
   __shared__ int part[1024];
+  grid_wait();
+  grid_ahead();
   int carry = 0;
   for (int b0 = 0; b0 < p.batch; b0 += 1024) {
     const int b = b0 + threadIdx.x;
@@ -972,8 +978,7 @@ slora_status launch(const QkParams& P, const Geometry& g, cudaStream_t st) {
   auto kernel = qk_rotary_kernel<T, G, V, kInter, kBwd, kSliced>;
   if (g.smem > 48 * 1024)
     SLORA_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, g.smem));
-  kernel<<<g.grid, g.warps * 32, g.smem, st>>>(P);
-  SLORA_CHECK_LAUNCH();
+  SLORA_CUDA(launch_early(kernel, dim3(unsigned(g.grid)), g.warps * 32, size_t(g.smem), st, P));
   return SLORA_OK;
 }
 template <typename T, typename G, int V, bool kInter, bool kBwd>
@@ -1158,8 +1163,7 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
     o.batch = D.ti.batch;
     std::copy(tok->ctx_len, tok->ctx_len + D.ti.batch, o.ctx_len);
     LaunchScope ls(kAux, double(D.ti.batch) * 4, st);
-    qk_offsets_kernel<<<1, 1024, 0, st>>>(o);
-    SLORA_CHECK_LAUNCH();
+    SLORA_CUDA(launch_early(qk_offsets_kernel, dim3(1), 1024, 0, st, o));
   }
   P.pos = D.pos;
   P.ctx_off = ctx_off;
@@ -1256,8 +1260,8 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
       d.blocks[i] = P.part[i].blocks;
     }
     LaunchScope ls(kAux, double(g.grid) * hd * 4, st);
-    qk_dg_kernel<<<dim3(unsigned((hd + 31) / 32), unsigned(D.nparts)), 1024, 0, st>>>(d);
-    SLORA_CHECK_LAUNCH();
+    SLORA_CUDA(launch_early(qk_dg_kernel, dim3(unsigned((hd + 31) / 32), unsigned(D.nparts)), 1024,
+                            0, st, d));
   }
   return SLORA_OK;
 }
