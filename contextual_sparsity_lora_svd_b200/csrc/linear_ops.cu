@@ -1148,9 +1148,8 @@ slora_status linear_bwd_tc(const LinearDesc& L, const slora_tokens* tok, const v
 // The backward from 8-bit checkpoints: dX as above, on the same GEMMs; the
 // rank-r contractions on the kernels of lora_grad.cu, which read the
 // checkpoint's codes and take dY B and X A^T to fp32 precision.  Per call: one
-// launch for dY B (both row kinds), one for dA and dB; the part of a gradient
-// that belongs to the selected channels lands in a buffer of its own and is
-// added onto them.
+// launch lays the operands out, one makes dY B (both row kinds), one dA and dB,
+// one dX.
 slora_status linear_bwd_act8_run(const LinearDesc& L, const slora_tokens* tok,
                                  const slora_act8& X_ctx, const slora_act8& X_out,
                                  const float* XA, const void* dY_ctx, const void* dY_out,
@@ -1178,7 +1177,6 @@ slora_status linear_bwd_act8_run(const LinearDesc& L, const slora_tokens* tok,
   void* AS = none || outr ? nullptr : bf(ni, lr);    // A[:, idx]^T and A^T, padded
   void* At = none || outr ? nullptr : bf(k, lr);
   void* dYpad = outr && ni % 8 ? bf(TC, ldi) : nullptr;
-  float* SG = none ? nullptr : ar.take<float>(size_t(std::max<int64_t>(ni, 1)) * r);
   void* rsB0 = ar.take<__nv_bfloat16>(size_t(skinny_rsplit_elems(outr ? ni : n)));
   void* rsB1 = outr ? ar.take<__nv_bfloat16>(size_t(skinny_rsplit_elems(n))) : nullptr;
   const void* dYc = dYpad ? dYpad : dY_ctx;
@@ -1201,20 +1199,31 @@ slora_status linear_bwd_act8_run(const LinearDesc& L, const slora_tokens* tok,
     j.M = M; j.K = K; j.terms = t; j.out = out; j.ldo = ldo; j.trans = trans;
     return j;
   };
-  if (in_cols) add_sum(TO, k, tPo, dA, k, 1).X8 = X_out;
-  else add_sum(T, k, tP, dA, k, 1).X8 = X_ctx;
+  // the part of a gradient that belongs to the selected channels' context rows
+  // is added to the part of all channels
+  const bool sliced = !none && TC > 0 && ni > 0;
+  {
+    RankSum& j = in_cols ? add_sum(TO, k, tPo, dA, k, 1) : add_sum(T, k, tP, dA, k, 1);
+    j.X8 = in_cols ? X_out : X_ctx;
+    j.add = sliced && in_cols;
+  }
   {
     RankSum& j = add_sum(outr ? TO : T, n, tX, dB, r, 0);
     j.X = outr ? dY_out : dY_ctx;
     j.ld = n;
+    j.add = sliced && outr;
   }
-  const bool sliced = !none && TC > 0 && ni > 0;
-  if (sliced && outr) {
-    RankSum& j = add_sum(TC, ni, tXc, SG, r, 0);
-    j.X = dYc;
-    j.ld = lddc;
-  } else if (sliced) {
-    add_sum(TC, ni, tP, SG, ni, 1).X8 = X_ctx;
+  if (sliced) {
+    RankSum& j = outr ? add_sum(TC, ni, tXc, dB, r, 0) : add_sum(TC, ni, tP, dA, k, 1);
+    if (outr) {
+      j.X = dYc;
+      j.ld = lddc;
+    } else {
+      j.X8 = X_ctx;
+    }
+    j.add = true;
+    j.idx = L.idx;
+    j.limit = outr ? n : k;
   }
   float* part = ar.take<float>(size_t(rank_sums_part(sums, nsums, r)));
   const int64_t ncnt = rank_sums_counters(sums, nsums, r);
@@ -1245,6 +1254,9 @@ slora_status linear_bwd_act8_run(const LinearDesc& L, const slora_tokens* tok,
       u.ldo = lr;
     }
     u.zero = cnt; u.nzero = ncnt;
+    if (sliced) {
+      u.sums = outr ? dB : dA; u.nsums = int64_t(r) * (outr ? n : k);
+    }
     SLORA_TRY(lora_setup(u, tok, ti, r, st));
     RankRows rows[2];
     RankRows &rc = rows[0], &ro = rows[1];
@@ -1267,12 +1279,6 @@ slora_status linear_bwd_act8_run(const LinearDesc& L, const slora_tokens* tok,
   }
   // before the product: dY is still in L2, and nothing of this needs dX
   SLORA_TRY(rank_sums(sums, nsums, r, s, part, cnt, st));
-  if (sliced) {
-    ScatterAddJob sj;
-    sj.dst = outr ? dB : dA; sj.ld_dst = outr ? r : k;
-    sj.src = SG; sj.ld_src = outr ? r : ni; sj.trans = outr ? 0 : 1;
-    SLORA_TRY(scatter_add_cols(&sj, 1, L.idx, ni, r, outr ? n : k, st));
-  }
   if (none) {
     TcBuilder b(ctiles, (T + 127) / 128, 0, 0, T, k, 0, EPI_STORE);
     b.seg(mat(dY_ctx, T, n, n), mat(L.W, n, k, k), B_MN, n)

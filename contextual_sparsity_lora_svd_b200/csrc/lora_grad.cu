@@ -80,8 +80,8 @@ struct SetupParams {
   int seq, batch, cols, cp;
   long long ldt, ldto;  // columns of the terms' rows
   long long T;
-  // first block of: the rows of W, the tokens, B's copies, A's transposes
-  int w0, t0, b0, b1, a0, a1;
+  // first block of: the rows of W, the tokens, B's copies, A's transposes, the zeros
+  int w0, t0, b0, b1, a0, a1, z0;
   int off[CAP + 1];  // context rows before each sequence
 };
 
@@ -181,6 +181,11 @@ __global__ void __launch_bounds__(kSetupThreads)
     for (int q = tid / kSetupRows; q < P.cp; q += kSetupThreads / kSetupRows)
       static_cast<__nv_bfloat16*>(c.dst)[q * ld + i] =
           src >= 0 && q < P.cols ? in[q] : __float2bfloat16_rn(0.0f);
+  } else if (blk >= P.z0) {  // four values a thread
+    const int64_t i = ((int64_t)(blk - P.z0) * kSetupThreads + tid) * 4;
+    if (i + 3 < d.nsums) *reinterpret_cast<float4*>(d.sums + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    else
+      for (int64_t e = i; e < d.nsums; ++e) d.sums[e] = 0.0f;
   } else {  // A's transposes: a thread eight columns of a row
     const bool second = blk >= P.a1;
     const LoraCopy& c = d.A[second ? 1 : 0];
@@ -305,6 +310,9 @@ struct alignas(64) SumJob {
   long long M, K;
   float* out;
   long long ldo;
+  const int32_t* idx;
+  long long limit;
+  int add;
   int trans, nsplit, blocks;  // blocks: channel blocks * splits
   int stages;                 // of one split
   int tile0;                  // first output tile (partials and counters)
@@ -593,10 +601,16 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
       P.part + ((long long)blockIdx.y * gridDim.x + blockIdx.x) * kTile) + 32 * (warp & 3) + lane;
   auto emit = [&](const auto& v, long long c, int first) {
     if (c >= j.K) return;
+    if (j.idx) c = j.idx[c];
+    if (j.idx && (c < 0 || c >= j.limit)) return;
+    float* out = j.out + (j.trans ? c : c * j.ldo);
+    const long long step = j.trans ? j.ldo : 1;
 #pragma unroll
     for (int i = 0; i < int(sizeof(v) / sizeof(float)); ++i) {
       const int q = q0 + first + i;
-      if (q < P.cols) j.out[j.trans ? q * j.ldo + c : c * j.ldo + q] = v[i] * P.scale;
+      if (q >= P.cols) continue;
+      if (j.add) atomicAdd(out + q * step, v[i] * P.scale);
+      else out[q * step] = v[i] * P.scale;
     }
   };
   if (warp < 4) {
@@ -761,6 +775,7 @@ slora_status setup(const LoraSetup& d, const slora_tokens* tok, const TokenInfo&
   p.b1 = add(d.B[1].dst ? std::max<int64_t>(d.B[1].n, 1) : 0, kSetupRows);
   p.a0 = add(d.A[0].n * (d.ldo / 8), kSetupThreads);
   p.a1 = add(d.A[1].n * (d.ldo / 8), kSetupThreads);
+  p.z0 = add(d.nsums, kSetupThreads * 4);
   double bytes = double(ti.T) * cols * (4 + 2 * kTerms) + 4.0 * double(d.W.n) * d.wcols;
   for (int i = 0; i < 2; ++i) bytes += 4.0 * double(d.B[i].n + d.A[i].n) * cols;
   LaunchScope ls(kAux, bytes, st);
@@ -836,6 +851,7 @@ slora_status rank_sums(const RankSum* jobs, int n, int cols, float scale, float*
     const bool codes = s.X8.codes != nullptr;
     j.M = s.M; j.K = s.K;
     j.out = s.out; j.ldo = s.ldo; j.trans = s.trans;
+    j.add = s.add; j.idx = s.idx; j.limit = s.limit;
     j.nsplit = nsplit[i];
     j.stages = per[i];
     j.blocks = int(channel_blocks(s)) * nsplit[i];

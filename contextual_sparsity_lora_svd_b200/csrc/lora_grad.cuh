@@ -36,6 +36,8 @@ struct LoraSetup {
   int64_t wcols = 0, ldo = 0;  // columns of a row of W (a multiple of 8, 16-byte aligned rows)
   unsigned* zero = nullptr;
   int64_t nzero = 0;
+  float* sums = nullptr;  // zeroed: what two jobs of rank_sums add to (16-byte aligned)
+  int64_t nsums = 0;
 };
 slora_status lora_setup(const LoraSetup& d, const slora_tokens* tok, const TokenInfo& ti, int cols,
                         cudaStream_t st);
@@ -61,7 +63,10 @@ slora_status rank_rows(const RankRows* jobs, int n, int cols, float s, cudaStrea
 
 // Sum over tokens: v[c, q] = scale * sum over m < M of X(m, c) P(m, q) for c < K,
 // q < cols, P given as its terms, X bf16 (16-byte aligned rows of ld, a multiple
-// of 8) or a checkpoint.  Written to out[q * ldo + c] (trans) or out[c * ldo + q].
+// of 8) or a checkpoint.  Written to out[q * ldo + c] (trans) or out[c * ldo + q];
+// with `add`, added there, at channel idx[c] where idx is given (outside `limit`:
+// left out).  Of distinct channels at most two jobs add to a zero, so their order
+// does not show.
 struct RankSum {
   const void* X = nullptr;
   slora_act8 X8 = {nullptr, nullptr};  // codes: the checkpoint, else X
@@ -70,6 +75,9 @@ struct RankSum {
   float* out = nullptr;
   int64_t ldo = 0;
   int trans = 0;
+  bool add = false;
+  const int32_t* idx = nullptr;
+  int64_t limit = 0;
 };
 constexpr int kRankSums = 3;  // of one launch
 // Workspace of a launch: partial sums (floats) and arrival counters (unsigned,

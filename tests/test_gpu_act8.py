@@ -329,3 +329,47 @@ def test_linear_backward_captured(L):
         torch.cuda.synchronize()
         assert all(torch.equal(a, c) for a, c in zip(out, want))
     assert L.lib().slora_device_error(1) == 0
+
+
+def test_calls_follow_one_another_without_waiting(L):
+    """A kernel may be placed while the one before it ends: chains on one stream, in which every
+    call reads what the last one wrote and overwrites what it read, and the same chains on four
+    streams at once, give the serial bits."""
+    def chain(seed, T, k, n, r=16):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        bf = lambda *s: torch.randn(*s, device="cuda", generator=gen).bfloat16()  # noqa: E731
+        W, A, B, X = bf(n, k), bf(r, k), bf(n, r), bf(T, k)
+        XA = torch.randn(T, r, device="cuda", generator=gen)
+        c, Y, dX = L.act8_empty(T, k), bf(T, k), bf(T, k)
+        dA, dB = torch.empty(r, k, device="cuda"), torch.empty(n, r, device="cuda")
+        dY = bf(T, n)
+        need = 1 << 25
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+        def run(stream):
+            Y.copy_(X)
+            for _ in range(3):
+                L.slora_act8_pack(Y, *c, stream=stream)
+                L.slora_linear_bwd_act8(L.SLICE_NONE, 1, T, [T], k, n, W, A, B, 0.5, None, c, XA, dY, dX,
+                                        dA, dB, ws=ws, stream=stream)
+                L.slora_act8_pack(dX, *c, stream=stream)
+                L.slora_act8_unpack(*c, Y, stream=stream)
+            return Y, dX, dA, dB
+        return run
+
+    chains = [chain(1, 512, 1024, 768), chain(2, 77, 688, 256), chain(3, 300, 256, 688), chain(4, 512, 512, 512)]
+    want = []
+    for f in chains:
+        outs = f(torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in outs])
+    streams = [torch.cuda.Stream() for _ in chains]
+    for _ in range(20):
+        got = []
+        for f, st in zip(chains, streams):
+            with torch.cuda.stream(st):
+                got.append(f(st))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
+    assert L.lib().slora_device_error(1) == 0
