@@ -72,6 +72,7 @@ struct alignas(64) TcParams {
 struct alignas(64) TcGroup {
   TcParams p[2];
   int ng;
+  int ahead;  // a kernel launched early may run beside the last tiles
   int tot0, tot1;
   int mpairs[2];
 };
@@ -654,6 +655,7 @@ __device__ __forceinline__ void tc2_bwd_epilogue(const TcGroup& G, uint8_t* wbuf
 template <int kStages, bool kBwdTma>
 __global__ void __launch_bounds__(256, 1) tc_gemm2_kernel(const __grid_constant__ TcGroup G) {
   extern __shared__ uint8_t smem_raw2[];
+  if (G.ahead) grid_ahead();
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw2) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * STAGE2_BYTES);
@@ -1110,6 +1112,7 @@ slora_status launch_group(const TcGemm* const* gs, int n, cudaStream_t st) {
     double f = 0.0;
     SLORA_TRY(build_params(*gs[i], &G.p[ng], &run, &tma[ng], &f));
     if (!run) continue;
+    G.ahead |= gs[i]->ahead ? 1 : 0;
     flops += f;
     ++ng;
   }

@@ -68,6 +68,9 @@ struct TcGemm {
   int proj_r = 0;
   float* proj_part = nullptr;
   int64_t proj_rows = 0;
+  // The next kernel on the stream, if launched early (launch_early), may run on the
+  // SMs that have no tile left.
+  bool ahead = false;
   // SWIGLU_BWD: rows of in0, in1, out0 and out1 (all [io_rows x N], leading
   // dimensions ldi / ldo).  When set (16-byte aligned pointers) g and u are
   // loaded and dG and dU stored by TMA through shared

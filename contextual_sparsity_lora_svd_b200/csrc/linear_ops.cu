@@ -1277,13 +1277,12 @@ slora_status linear_bwd_act8_run(const LinearDesc& L, const slora_tokens* tok,
     }
     SLORA_TRY(rank_rows(rows, none ? 1 : 2, r, s, st));
   }
-  // before the product: dY is still in L2, and nothing of this needs dX
-  SLORA_TRY(rank_sums(sums, nsums, r, s, part, cnt, st));
   if (none) {
     TcBuilder b(ctiles, (T + 127) / 128, 0, 0, T, k, 0, EPI_STORE);
     b.seg(mat(dY_ctx, T, n, n), mat(L.W, n, k, k), B_MN, n)
         .seg(mat(dYBb, T, r, lr), mat(L.A, r, k, k), B_MN, r)
         .out(dX_ctx, nullptr, nullptr, k);
+    b.g.ahead = true;
     SLORA_TRY(gemm_tc(b.g, st));
   } else if (outr) {
     TcBuilder bc(ctiles, nct, 1, 0, TC, k, 0, EPI_STORE);
@@ -1294,6 +1293,7 @@ slora_status linear_bwd_act8_run(const LinearDesc& L, const slora_tokens* tok,
     b.seg(mat(dY_out, TO, n, n), mat(L.W, n, k, k), B_MN, n)
         .seg(mat(dYBbO, TO, r, lr), mat(L.A, r, k, k), B_MN, r)
         .out(dX_ctx, nullptr, nullptr, k);
+    bc.g.ahead = b.g.ahead = true;
     SLORA_TRY(gemm_tc_pair(bc.g, b.g, st));
   } else {
     TcBuilder bc(ctiles, nct, 0, 1, TC, ni, 0, EPI_STORE);
@@ -1304,9 +1304,13 @@ slora_status linear_bwd_act8_run(const LinearDesc& L, const slora_tokens* tok,
     b.seg(mat(dY_ctx, T, n, n), mat(L.W, k, n, n), B_K, n)
         .seg(mat(dYBb, T, r, lr), mat(At, k, r, lr), B_K, r)
         .out(dX_out, nullptr, nullptr, k);
+    bc.g.ahead = b.g.ahead = true;
     SLORA_TRY(gemm_tc_pair(bc.g, b.g, st));
   }
-  return SLORA_OK;
+  // beside the product's last tiles, on the SMs that have none left: it reads
+  // nothing that the product writes
+  const bool product = !in_cols || sliced || TO > 0;
+  return rank_sums(sums, nsums, r, s, part, cnt, product, st);
 }
 
 }  // namespace slora

@@ -17,9 +17,9 @@
 // sixteen warps take every sixteenth 32-channel group and are summed in order
 // in shared memory: no partial sums leave the block.  p is written as the
 // GEMM's LoRA operand (bf16) and as the three bf16 terms that rank_sums reads.
-// 12.7 us for 4096 x 4096 (5 for the 34 MB of dY from memory): every block reads
-// all of B's copy from L2, as much as its rows of dY.  Clusters of four blocks
-// that split the channels of 64 rows read a quarter of that, and took 20 us.
+// 12.7 us for 4096 x 4096 (5 for the 34 MB of dY from memory), bound by the latency
+// of three rounds of loads a warp: blocks of 32 rows, which read B's copy half as
+// often, take as long, clusters of four that split the channels of 64 rows 20 us.
 //
 // lora_setup takes 8 us for the q projection of 4096 rows at half its channels
 // (27 us in six launches before), 14 us for a down projection of 11008 (53 us).
@@ -37,7 +37,11 @@
 // flight.  The stages take turns on four accumulators: the tensor core truncates
 // each addition, and four short chains added in fp32 are off by a quarter of one
 // long one.  Blocks that share channels leave partial sums that the last to
-// arrive adds in order: the result does not depend on timing.  Every wait is
+// arrive adds in order: the result does not depend on timing.  The launch runs
+// beside the last tiles of the product before it (its blocks fit on SMs that have
+// none left) and its blocks leave after that: 116 -> 114 us for the q projection's
+// backward of 4096 rows, 20 -> 16 for 256 rows of 256 -> 688.  It lets nothing start
+// early itself: blocks of a small grid would crowd on the SMs that end first.  Every wait is
 // bounded; on expiry the block raises a device flag (slora_device_error:
 // SLORA_ERR_TIMEOUT) and leaves after its own copies and products ended.
 #include <cuda.h>
@@ -320,6 +324,7 @@ struct alignas(64) SumJob {
 struct SumParams {
   SumJob job[kRankSums];
   int n, cols, cp, tiles;  // tiles: output tiles of one column slice
+  int beside;
   float scale;
   float* part;
   unsigned* counters;
@@ -490,7 +495,7 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
     mbar_init(&done, 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    grid_wait();
+    if (!P.beside) grid_wait();
     for (int st = 0; st < min(stages, kRing); ++st) copy(st);
   }
   if (warp == kXWarps) {
@@ -500,8 +505,7 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  grid_wait();
-  grid_ahead();
+  if (!P.beside) grid_wait();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -641,7 +645,10 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
                  "n"(kTmemCols)
                  : "memory");
   }
-  if (j.nsplit == 1) return;
+  if (j.nsplit == 1) {
+    grid_wait();
+    return;
+  }
   if (tid == 0) {
     __threadfence();
     const unsigned prev = atomicAdd(&P.counters[tile], 1u);
@@ -649,7 +656,10 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
     if (s_last) P.counters[tile] = 0u;
   }
   __syncthreads();
-  if (!s_last || warp >= kXWarps) return;
+  if (!s_last || warp >= kXWarps) {
+    grid_wait();
+    return;
+  }
   __threadfence();
   // split s of this channel block ran as block (blockIdx.x - blk) + s * nch + cb
   // (eight warps: a thread half the columns of a channel, eight splits' loads at once)
@@ -677,6 +687,7 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
       }
   }
   emit(v, ch0 + c, 4 * half);
+  grid_wait();
 }
 
 int slices(int cols) { return (cols + kCols - 1) / kCols; }
@@ -837,7 +848,7 @@ int64_t rank_sums_counters(const RankSum* jobs, int n, int cols) {
 }
 
 slora_status rank_sums(const RankSum* jobs, int n, int cols, float scale, float* part,
-                       unsigned* counters, cudaStream_t st) {
+                       unsigned* counters, bool beside, cudaStream_t st) {
   if (n < 1 || n > kRankSums) SLORA_FAIL(SLORA_ERR_SHAPE, "rank_sums: %d jobs", n);
   int nsplit[kRankSums];
   int per[kRankSums];
@@ -883,6 +894,7 @@ slora_status rank_sums(const RankSum* jobs, int n, int cols, float scale, float*
   p.scale = scale;
   p.part = part;
   p.counters = counters;
+  p.beside = beside;
   SLORA_CUDA(cudaFuncSetAttribute(rank_sums_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   kSumSmem));
   LaunchScope ls(kSkinny, bytes * slices(cols), st);

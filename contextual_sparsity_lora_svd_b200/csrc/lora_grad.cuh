@@ -84,8 +84,11 @@ constexpr int kRankSums = 3;  // of one launch
 // zero on entry, left zero).  M and K of the jobs alone decide.
 int64_t rank_sums_part(const RankSum* jobs, int n, int cols);
 int64_t rank_sums_counters(const RankSum* jobs, int n, int cols);
+// beside: the launch may run beside the kernel before it on the stream and ends after
+// it.  That kernel may not write what is read here, nor touch what is written, and what
+// is read here was complete before that kernel called grid_ahead().
 slora_status rank_sums(const RankSum* jobs, int n, int cols, float scale, float* part,
-                       unsigned* counters, cudaStream_t st);
+                       unsigned* counters, bool beside, cudaStream_t st);
 
 // Raised when a rank_sums wait ran out of its budget, or by an index outside its weight.
 slora_status rank_check_error(bool clear);
