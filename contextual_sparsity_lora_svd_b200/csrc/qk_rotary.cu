@@ -26,8 +26,8 @@
 // rows are few: it computes the row's hd / 2 sines and cosines once, spread
 // over its lanes, keeps each lane's in registers and walks the heads, the next
 // ones on their way to shared memory.  Nothing in the loop waits for another
-// warp.  32 + 8 heads of 128 channels, 8192 rows: 34 us, as long as a plain copy
-// of the same 168 MB takes (33 us); with norms, fp32 dy and dg backward 64 us for
+// warp.  32 + 8 heads of 128 channels, 8192 rows: 31 us, as long as a plain copy
+// of the same 168 MB takes (33 us); with norms, fp32 dy and dg backward 61 us for
 // 336 MB.
 //
 // Sliced rows: the inverse channel list lies in shared memory; a context row's
@@ -36,9 +36,10 @@
 // heads pass through the same stage, two ahead.  The next row is asked into L2
 // meanwhile: a second stage a warp would cost more resident warps than it
 // hides.  A forward and backward of 64 heads x 4096 rows at half the channels
-// take 116 us, bound by issue and latency at 16 (backward) and 24 warps an SM;
-// with two stages 131 us, with a full-width row a warp 147 us, with the staged
-// row swizzled against bank conflicts (a quarter fewer) 120 us.
+// take 113 us, bound by issue and latency at 16 (backward) and 24 warps an SM.
+// Other ways, at an earlier state of the rest: two stages a warp 131 us against
+// 129, a full-width row a warp 147; the staged row swizzled against bank conflicts
+// (a quarter fewer) 120 against 116.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
