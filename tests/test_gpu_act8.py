@@ -269,6 +269,58 @@ def test_linear_backward_empty_parts(L, side, ctx, ni):
     linear_case(L, side, 2, 40, ctx, 72, 72, 8, ni)
 
 
+@pytest.mark.parametrize("side", ["none", "out_rows", "in_cols"])
+@pytest.mark.parametrize("b,s", [(64, 5), (65, 5), (1500, 3)])
+def test_linear_backward_many_sequences(L, side, b, s):
+    """Around the number of sequences that the small launch parameters hold, uneven contexts."""
+    linear_case(L, side, b, s, [(7 * i) % (s + 1) for i in range(b)], 72, 136, 8, 40)
+
+
+@pytest.mark.parametrize("side", ["out_rows", "in_cols"])
+@pytest.mark.parametrize("last", [104, 2 ** 31 - 1])
+def test_linear_backward_leaves_channels_outside_out(L, side, last):
+    """An entry outside the weight counts as a channel of zeros and raises the error flag."""
+    b, s, ctx, k, n, r = 2, 20, [15, 9], 104, 104, 8
+    gen = gen_of(4)
+    T, TC = b * s, sum(ctx)
+    W, A, B = rand(gen, (104, 104)), rand(gen, (r, k)), rand(gen, (n, r))
+    XA = rand(gen, (T, r), torch.float32)
+    code = L.SLICE_OUT_ROWS if side == "out_rows" else L.SLICE_IN_COLS
+    xs = rand(gen, (T, k)), rand(gen, (TC, 4)), rand(gen, (T - TC, k))
+    dys = rand(gen, (TC, 4)), rand(gen, (T - TC, n)), rand(gen, (T, n))
+    outs = []
+    for keep in (4, 3):
+        idx = torch.tensor([2, 5, 60, last][:keep], dtype=torch.int32, device="cuda")
+        dA, dB = torch.full((r, k), 7.0, device="cuda"), torch.full((n, r), 7.0, device="cuda")
+        ck = []
+        for x in (xs[0], xs[1], xs[2]):
+            ck.append(L.act8_empty(*x.shape))
+            L.slora_act8_pack(x, *ck[-1])
+        if keep == 3:  # the values that the four channels' checkpoint holds, of three of them
+            v = torch.empty_like(xs[1])
+            L.slora_act8_unpack(*ck[1], v)
+            ck[1] = L.act8_empty(TC, 3)
+            L.slora_act8_pack(v[:, :3].contiguous(), *ck[1])
+        if side == "out_rows":
+            dX = torch.empty_like(xs[0])
+            L.slora_linear_bwd_act8(code, b, s, ctx, k, n, W, A, B, 0.5, idx, ck[0], XA,
+                                    dys[0][:, :keep].contiguous(), dX, dA, dB, dY_out=dys[1])
+            outs.append((dX, dA, dB))
+        else:
+            dXc, dXo = torch.full((TC, keep), 7.0, device="cuda").bfloat16(), torch.empty_like(xs[2])
+            L.slora_linear_bwd_act8(code, b, s, ctx, k, n, W, A, B, 0.5, idx, ck[1], XA, dys[2], dXc, dA,
+                                    dB, X8_out=ck[2], dX_out=dXo)
+            if keep == 4:
+                assert (dXc[:, 3] == 0).all()
+            outs.append((dXc[:, :3], dXo, dA, dB))
+        assert L.lib().slora_device_error(1) == (1 if keep == 4 else 0)
+        assert L.lib().slora_device_error(1) == 0
+    for got, want in zip(*outs):  # the same terms and zeros, in fp32 sums of fewer than 128 terms
+        tol = 2.0 ** -8 if got.dtype == torch.bfloat16 else 128 * 2.0 ** -24
+        err = rel_frob(R.f64(got), R.f64(want))
+        assert err <= tol
+
+
 def test_linear_backward_is_the_bf16_call_on_the_values(L):
     """dX has the bits of slora_linear_bwd (which does not read the activation
     for it); the gradients agree to that call's bf16 operands."""

@@ -300,6 +300,38 @@ def test_sliced_rows_equal_dense_rows_with_zeros(L, ctx, layout, hd, norm):
     assert L.lib().slora_device_error(1) == 0
 
 
+@pytest.mark.parametrize("b,s,ctx,parts,hd", [
+    (1, 5, [3], [(128, 32768), (128, 20001)], 256),  # the most channels, every one of them kept
+    (2, 350, [350, 200], [(8, 500), (2, 250)], 128), (3, 90, [90, 0, 33], [(32, 2048), (8, 512)], 128),
+    (65, 11, None, [(4, 100), (1, 31)], 64), (1, 1, [1], [(32, 1), (8, 1024)], 128)])
+def test_sliced_rows_of_many_channels(L, b, s, ctx, parts, hd):
+    """Whole blocks of rows, lists of two lengths: the dense bits, forward and backward."""
+    ctx = ctx or [(5 * i) % (s + 1) for i in range(b)]
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(b + s)
+    calls, outs = [[], [], [], []], []
+    for h, ni in parts:
+        n = h * hd
+        idx = torch.randperm(n, generator=gen, device="cuda")[:ni].int()
+        Xc, Xo, full, is_ctx = sliced(gen, b, s, ctx, h, hd, idx)
+        g, dY = rand(gen, (hd,), torch.bfloat16), rand(gen, (b * s, n), torch.float32)
+        Y, Y2, dX = (torch.empty_like(full) for _ in range(3))
+        dXc, dXo = torch.full_like(Xc, 5), torch.full_like(Xo, 5)
+        for c, rows in zip(calls, (
+                dict(X=full, Y=Y), dict(X=full, dY=dY, dX=dX), dict(Y=Y2, idx=idx, X_ctx=Xc, X_out=Xo),
+                dict(dY=dY, idx=idx, X_ctx=Xc, X_out=Xo, dX_ctx=dXc, dX_out=dXo))):
+            c.append(L.qk_rows(h, g=g, **rows))
+        outs.append((Y, Y2, dX, dXc, dXo, idx, is_ctx))
+    L.slora_qk_rotary_fwd(b, s, hd, *calls[0])
+    L.slora_qk_rotary_bwd(b, s, hd, *calls[1])
+    L.slora_qk_rotary_fwd(b, s, hd, *calls[2], ctx_len=ctx)
+    L.slora_qk_rotary_bwd(b, s, hd, *calls[3], ctx_len=ctx)
+    for Y, Y2, dX, dXc, dXo, idx, is_ctx in outs:
+        assert torch.equal(Y, Y2)
+        assert torch.equal(dX[is_ctx][:, idx.long()], dXc) and torch.equal(dX[~is_ctx], dXo)
+    assert L.lib().slora_device_error(1) == 0
+
+
 def test_sliced_rows_with_no_channels(L):
     """A context row whose head keeps nothing: zero rows, no gradient to write."""
     b, s, h, hd = 1, 6, 2, 64
