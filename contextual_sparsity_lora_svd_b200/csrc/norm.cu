@@ -238,16 +238,46 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 // A row's chunks stay packed between the two passes over them (4 registers a
-// chunk); the arithmetic and its order are those of the kernels above.
-template <int CPT>
-__global__ void __launch_bounds__(kRowThreads)
+// chunk); the arithmetic and its order are those of the kernels above.  Rows above
+// 4096 channels lie in up to four parts of 128 threads, four chunks a thread:
+// thread t of part p holds chunks t + 128 (p CPT + k), and its sum goes on where
+// thread t of part p - 1 left it, so the bits are those of one part with all the
+// chunks.  That part's registers leave 8 to 12 warps an SM; with residual,
+// 2048 x 11008: forward 60 -> 40 us, backward 59 -> 39; 4096 x 8192: 57 -> 55 and
+// 55 -> 49.  (Parts of two chunks a thread: backward 52 both.)
+template <int PARTS, typename F>
+__device__ __forceinline__ float row_sum(float* chain, float* red, F add) {
+  const int part = threadIdx.x / kRowThreads, t = threadIdx.x % kRowThreads;
+  float v = 0.0f;
+  if constexpr (PARTS == 1) {
+    return block_sum128(add(v), red);
+  } else {
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+      if (part == p) {
+        v = add(p ? chain[t] : 0.0f);
+        chain[t] = v;
+      }
+      if (p + 1 < PARTS) __syncthreads();
+    }
+    if (part == PARTS - 1) {
+      v = warp_sum(v);
+      if ((t & 31) == 0) red[t >> 5] = v;
+    }
+    __syncthreads();
+    return red[0] + red[1] + red[2] + red[3];  // (block_sum128's order)
+  }
+}
+template <int CPT, int PARTS>
+__global__ void __launch_bounds__(kRowThreads * PARTS)
     rmsnorm_fwd_act8_kernel(const uint4* __restrict__ X, const uint4* __restrict__ A,
                             const uint4* __restrict__ g, int nch, float eps,
                             uint4* __restrict__ Hout, uint4* __restrict__ N,
                             float* __restrict__ rstd, uint2* __restrict__ h8,
                             uint8_t* __restrict__ h8s, uint2* __restrict__ n8,
                             uint8_t* __restrict__ n8s) {
-  __shared__ float red[4];
+  __shared__ float red[4], chain[PARTS > 1 ? kRowThreads : 1];
+  const int first = threadIdx.x % kRowThreads + threadIdx.x / kRowThreads * (CPT * kRowThreads);
   grid_wait();
   grid_ahead();
   const int64_t o = int64_t(blockIdx.x) * nch;
@@ -256,28 +286,21 @@ __global__ void __launch_bounds__(kRowThreads)
   uint4 u[CPT], a[CPT];
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
-    const int c = threadIdx.x + k * kRowThreads;
+    const int c = first + k * kRowThreads;
     u[k] = c < nch ? X[o + c] : make_uint4(0, 0, 0, 0);
     if (A && c < nch) a[k] = A[o + c];
   }
-  float ss = 0.f;
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
-    const int c = threadIdx.x + k * kRowThreads;
-    if (c < nch) {
-      float h[8];
+    const int c = first + k * kRowThreads;
+    if (c < nch && A) {
+      float h[8], b[8];
       unpack8(u[k], h);
-      if (A) {
-        float b[8];
-        unpack8(a[k], b);
+      unpack8(a[k], b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] += b[i];
-        u[k] = pack8(h);
-        unpack8(u[k], h);
-        if (Hout) Hout[o + c] = u[k];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss += h[i] * h[i];
+      for (int i = 0; i < 8; ++i) h[i] += b[i];
+      u[k] = pack8(h);
+      if (Hout) Hout[o + c] = u[k];
     }
     if (h8) {
       const uint32_t byte = act8_byte_bf16(u[k]);
@@ -287,11 +310,22 @@ __global__ void __launch_bounds__(kRowThreads)
       }
     }
   }
-  const float r = rsqrtf(block_sum128(ss, red) / float(nch * 8) + eps);
+  const float ss = row_sum<PARTS>(chain, red, [&](float v) {
+#pragma unroll
+    for (int k = 0; k < CPT; ++k)
+      if (first + k * kRowThreads < nch) {
+        float h[8];
+        unpack8(u[k], h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v += h[i] * h[i];
+      }
+    return v;
+  });
+  const float r = rsqrtf(ss / float(nch * 8) + eps);
   if (threadIdx.x == 0 && rstd) rstd[blockIdx.x] = r;
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
-    const int c = threadIdx.x + k * kRowThreads;
+    const int c = first + k * kRowThreads;
     if (c < nch) {
       float h[8], gg[8];
       unpack8(u[k], h);
@@ -311,14 +345,19 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-template <int CPT>
-__global__ void __launch_bounds__(kRowThreads)
+// Blocks an SM: 80 registers a thread at four chunks, 64 at three.
+constexpr int row_blocks(int cpt, int parts) {
+  return cpt == 4 ? 6 / parts : cpt == 3 ? 8 / parts : 1;
+}
+template <int CPT, int PARTS>
+__global__ void __launch_bounds__(kRowThreads * PARTS, row_blocks(CPT, PARTS))
     rmsnorm_bwd_act8_kernel(const uint2* __restrict__ h8, const uint8_t* __restrict__ h8s,
                             const float* __restrict__ rstd, const uint4* __restrict__ g,
                             const uint4* __restrict__ dN0, const uint4* __restrict__ dN1,
                             const uint4* __restrict__ dN2, const uint4* __restrict__ dRes,
                             int nch, uint4* __restrict__ dX) {
-  __shared__ float red[4];
+  __shared__ float red[4], chain[PARTS > 1 ? kRowThreads : 1];
+  const int first = threadIdx.x % kRowThreads + threadIdx.x / kRowThreads * (CPT * kRowThreads);
   grid_wait();
   grid_ahead();
   const int64_t o = int64_t(blockIdx.x) * nch, o8 = int64_t(blockIdx.x) * ((nch + 3) & ~3);
@@ -329,7 +368,7 @@ __global__ void __launch_bounds__(kRowThreads)
   const float r = rstd[blockIdx.x];
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
-    const int c = threadIdx.x + k * kRowThreads;
+    const int c = first + k * kRowThreads;
     hc[k] = make_uint2(0, 0);
     hb[k] = 7u;
     d0[k] = res[k] = make_uint4(0, 0, 0, 0);
@@ -341,13 +380,11 @@ __global__ void __launch_bounds__(kRowThreads)
     }
   }
   float gd[CPT][8];
-  float dot = 0.f;
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
-    const int c = threadIdx.x + k * kRowThreads;
+    const int c = first + k * kRowThreads;
     if (c < nch) {
-      float t[8], h[8];
-      act8_values8(hc[k], hb[k], h);
+      float t[8];
       unpack8(d0[k], gd[k]);
       if (dN1) {
         unpack8(dN1[o + c], t);
@@ -361,16 +398,24 @@ __global__ void __launch_bounds__(kRowThreads)
       }
       unpack8(g[c], t);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        gd[k][i] *= t[i];  // g dN
-        dot += h[i] * gd[k][i];
-      }
+      for (int i = 0; i < 8; ++i) gd[k][i] *= t[i];  // g dN
     }
   }
-  const float coef = r * r * r * block_sum128(dot, red) / float(nch * 8);
+  const float dot = row_sum<PARTS>(chain, red, [&](float v) {
+#pragma unroll
+    for (int k = 0; k < CPT; ++k)
+      if (first + k * kRowThreads < nch) {
+        float h[8];
+        act8_values8(hc[k], hb[k], h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v += h[i] * gd[k][i];
+      }
+    return v;
+  });
+  const float coef = r * r * r * dot / float(nch * 8);
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
-    const int c = threadIdx.x + k * kRowThreads;
+    const int c = first + k * kRowThreads;
     if (c < nch) {
       float h[8], b[8];
       act8_values8(hc[k], hb[k], h);
@@ -449,19 +494,22 @@ slora_status rmsnorm_bwd_run(const void* Hin, const float* rstd, const void* g, 
   return SLORA_OK;
 }
 
-#define SLORA_ROW(KERNEL, ...) \
-  SLORA_CUDA(launch_early(KERNEL, dim3(rows), kRowThreads, 0, st, __VA_ARGS__))
-#define SLORA_ROW_SWITCH(KERNEL, ...)                                             \
-  if (nch <= kRowThreads) {                                                       \
-    SLORA_ROW(KERNEL<1>, __VA_ARGS__);                                            \
-  } else if (nch <= 2 * kRowThreads) {                                            \
-    SLORA_ROW(KERNEL<2>, __VA_ARGS__);                                            \
-  } else if (nch <= 4 * kRowThreads) {                                            \
-    SLORA_ROW(KERNEL<4>, __VA_ARGS__);                                            \
-  } else if (nch <= 8 * kRowThreads) {                                            \
-    SLORA_ROW(KERNEL<8>, __VA_ARGS__);                                            \
-  } else {                                                                        \
-    SLORA_ROW(KERNEL<16>, __VA_ARGS__);                                           \
+// Levels of 128 chunks in as few parts of at most four as hold them, evenly.
+#define SLORA_ROW(KERNEL, CPT, PARTS, ...)                                                    \
+  SLORA_CUDA(launch_early(KERNEL<CPT, PARTS>, dim3(rows), kRowThreads * PARTS, 0, st, __VA_ARGS__))
+#define SLORA_ROW_SWITCH(KERNEL, ...)                                \
+  switch ((nch + kRowThreads - 1) / kRowThreads) {                   \
+    case 1: SLORA_ROW(KERNEL, 1, 1, __VA_ARGS__); break;             \
+    case 2: SLORA_ROW(KERNEL, 2, 1, __VA_ARGS__); break;             \
+    case 3: SLORA_ROW(KERNEL, 3, 1, __VA_ARGS__); break;             \
+    case 4: SLORA_ROW(KERNEL, 4, 1, __VA_ARGS__); break;             \
+    case 5: case 6: SLORA_ROW(KERNEL, 3, 2, __VA_ARGS__); break;     \
+    case 7: case 8: SLORA_ROW(KERNEL, 4, 2, __VA_ARGS__); break;     \
+    case 9: SLORA_ROW(KERNEL, 3, 3, __VA_ARGS__); break;             \
+    case 10: case 11: case 12:                                       \
+      SLORA_ROW(KERNEL, 4, 3, __VA_ARGS__);                          \
+      break;                                                         \
+    default: SLORA_ROW(KERNEL, 4, 4, __VA_ARGS__);                   \
   }
 
 slora_status rmsnorm_fwd_act8_run(const void* X, const void* A, const void* g, int64_t T,

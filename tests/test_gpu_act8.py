@@ -144,6 +144,28 @@ def test_norm_writes_its_checkpoints(L, T, d, res):
     assert torch.equal(H8[0], H9[0]) and torch.equal(N8[0], N9[0])
 
 
+@pytest.mark.parametrize("T,d", [(3, 2600), (700, 5120), (2, 6144), (400, 8192), (3, 9216), (300, 11008),
+                                 (2, 12296), (300, 14336)])
+def test_rows_of_several_parts_have_the_plain_bits(L, T, d):
+    gen = gen_of(d)
+    X, A, g = rand(gen, (T, d)), rand(gen, (T, d)), rand(gen, (d,))
+    dN, dRes = [rand(gen, (T, d)) for _ in range(3)], rand(gen, (T, d))
+    H, N, H2, N2, dX, dX2 = (torch.empty_like(X) for _ in range(6))
+    r, r2 = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    H8, N8, want = L.act8_empty(T, d), L.act8_empty(T, d), L.act8_empty(T, d)
+    L.slora_rmsnorm_fwd(X, g, N=N, A=A, H=H, rstd=r)
+    L.slora_rmsnorm_fwd_act8(X, g, N2, r2, A=A, H=H2, H8=H8, N8=N8)
+    assert torch.equal(H, H2) and torch.equal(N, N2) and torch.equal(r, r2)
+    for got, src in ((H8, H), (N8, N)):
+        L.slora_act8_pack(src, *want)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    V = torch.empty_like(X)
+    L.slora_act8_unpack(*H8, V)
+    L.slora_rmsnorm_bwd(V, r, g, dN[0], dX, dN1=dN[1], dN2=dN[2], dRes=dRes)
+    L.slora_rmsnorm_bwd_act8(H8, r, g, dN[0], dX2, dN1=dN[1], dN2=dN[2], dRes=dRes)
+    assert torch.equal(dX, dX2)
+
+
 @pytest.mark.parametrize("T,d", [(1, 8), (5, 688), (3, 1032), (9, 4096), (2, 8200), (2, 16384)])
 @pytest.mark.parametrize("extra", [0, 1, 2])
 def test_norm_backward_reads_its_checkpoint(L, T, d, extra):
