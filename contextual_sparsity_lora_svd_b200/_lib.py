@@ -443,7 +443,9 @@ def _rows(t, what):
     return t.data_ptr(), st[0] if n[0] > 1 else max(st[0], n[1])
 
 
-def _whole(t, what):
+def _whole(t, what, dt):
+    if t.dtype is not dt:
+        raise TypeError(f"{what} is {t.dtype}, not {dt}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous tensor is needed")
     return t.data_ptr()
@@ -493,27 +495,25 @@ def qk_rows(heads, X=None, g=None, Y=None, dY=None, dX=None, dg=None, idx=None, 
         r.dX, r.lddx = _rows(dX, "dX")
         _same(dX, "dX", dt)
     if g is not None:
-        r.g = _whole(g, "g")
-        _same(g, "g", dt)
+        r.g = _whole(g, "g", dt)
     r.gdt = F32
     if dY is not None:
         r.dY, r.lddy = _rows(dY, "dY")
         r.gdt = dtype_code(dY)
-    r.scratch = dg is not None or idx is not None
     if dg is not None:
-        r.dg = _whole(dg, "dg")
-        if dg.dtype != torch.float32:
-            raise TypeError("dg is an fp32 tensor")
+        r.dg = _whole(dg, "dg", torch.float32)
     if idx is not None:
-        if idx.dtype != torch.int32:
-            raise TypeError("idx is an int32 tensor")
         r.n_idx = idx.numel()
-        for name, t in (("X_ctx", X_ctx), ("X_out", X_out), ("dX_ctx", dX_ctx), ("dX_out", dX_out)):
-            if t is not None:
-                setattr(r, name, _whole(t, name))
-                _same(t, name, dt)
+        if X_ctx is not None:
+            r.X_ctx = _whole(X_ctx, "X_ctx", dt)
+        if X_out is not None:
+            r.X_out = _whole(X_out, "X_out", dt)
+        if dX_ctx is not None:
+            r.dX_ctx = _whole(dX_ctx, "dX_ctx", dt)
+        if dX_out is not None:
+            r.dX_out = _whole(dX_out, "dX_out", dt)
         # an empty list is still a list: its address, never read, may be null
-        r.idx = _whole(idx, "idx") or r.X_out or r.dX_out or r.Y or r.dY
+        r.idx = _whole(idx, "idx", torch.int32) or r.X_out or r.dX_out or r.Y or r.dY
     r.tensors = (X, g, Y, dY, dX, dg, idx, X_ctx, X_out, dX_ctx, dX_out)
     return r
 
@@ -522,12 +522,14 @@ _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 @functools.lru_cache(maxsize=64)
-def _whole_sequences(batch, seq):
-    """Tokens of `batch` sequences for calls that do not split them."""
-    return make_tokens(batch, seq, [seq] * batch)
+def _tokens(batch, seq, ctx_len):
+    """(struct, its host array, context rows); ctx_len a tuple, or None: undivided."""
+    if ctx_len is None:
+        ctx_len = (seq,) * batch
+    return *make_tokens(batch, seq, ctx_len), sum(ctx_len)
 
 
-def _sizes(r, T, head_dim, ctx_len):
+def _sizes(r, T, TC, head_dim):
     """Refuses tensors of a qk_rows that do not hold T rows of its heads."""
     n = r.heads * head_dim
     X, g, Y, dY, dX, dg, idx, X_ctx, X_out, dX_ctx, dX_out = r.tensors
@@ -540,7 +542,6 @@ def _sizes(r, T, head_dim, ctx_len):
             if t is not None and t.numel() != head_dim:
                 raise ValueError(f"g and dg have one value a channel of a head, {head_dim}")
     if idx is not None:
-        TC = T if ctx_len is None else sum(ctx_len)
         for t, want in ((X_ctx, TC * r.n_idx), (dX_ctx, TC * r.n_idx), (X_out, (T - TC) * n),
                         (dX_out, (T - TC) * n)):
             if t is not None and t.numel() != want:
@@ -548,8 +549,7 @@ def _sizes(r, T, head_dim, ctx_len):
 
 
 def _qk(fn, head, batch, seq, head_dim, q, k, rotary_, pos, eps, ctx_len, ws, stream):
-    tok, keep = (_whole_sequences(batch, seq) if ctx_len is None
-                 else make_tokens(batch, seq, ctx_len))
+    tok, keep, TC = _tokens(batch, seq, None if ctx_len is None else tuple(map(int, ctx_len)))
     if pos is not None and (pos.dtype != torch.int32 or pos.numel() != batch * seq
                             or not pos.is_contiguous()):
         raise TypeError("pos is a contiguous int32 tensor with one position a row")
@@ -558,19 +558,18 @@ def _qk(fn, head, batch, seq, head_dim, q, k, rotary_, pos, eps, ctx_len, ws, st
         if k.dt != q.dt or k.gdt != q.gdt:
             raise TypeError("q and k have the same dtypes")
         kr = ctypes.byref(k)
-    _sizes(q, batch * seq, head_dim, ctx_len)
+    _sizes(q, batch * seq, TC, head_dim)
     if k is not None:
-        _sizes(k, batch * seq, head_dim, ctx_len)
+        _sizes(k, batch * seq, TC, head_dim)
     args = head + [ctypes.byref(tok), head_dim, eps, ctypes.byref(rotary_ or rotary()), ptr(pos),
                    ctypes.byref(q), kr]
-    if q.scratch or (k is not None and k.scratch):
-        _run(fn, args, ws, stream)
-    else:
-        _run_plain(fn, args, stream)
+    _run_scratch(fn, args, ws, stream)
     del keep
 
 
 _NO_BYTES = ctypes.byref(c_sz(0))  # written by workspace queries alone
+_last_need = {}  # bytes that a function's last call took
+_SMALL = 1 << 20
 
 
 def _run_plain(fn_name, args, stream):
@@ -578,6 +577,29 @@ def _run_plain(fn_name, args, stream):
     st = getattr(_lib, fn_name)(*args, 16, _NO_BYTES, _stream(stream))
     if st:
         _check(fn_name, st)
+
+
+def _run_scratch(fn_name, args, ws, stream):
+    """_run without its query where the scratch of the last such call does (a call
+    with too little starts nothing); large scratch is asked for each time."""
+    if ws is not None:
+        size = ws.numel() * ws.element_size()
+        _check(fn_name, getattr(_lib, fn_name)(*args, ptr(ws), ctypes.byref(c_sz(size)),
+                                               _stream(stream)))
+        return
+    size = _last_need.get(fn_name, 0)
+    if size <= _SMALL:
+        if size:
+            ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+            st = getattr(_lib, fn_name)(*args, ws.data_ptr(), ctypes.byref(c_sz(size)),
+                                        _stream(stream))
+        else:
+            st = getattr(_lib, fn_name)(*args, 16, _NO_BYTES, _stream(stream))
+        if st != 4:  # SLORA_ERR_WORKSPACE
+            _check(fn_name, st)
+            return
+    owned = _run(fn_name, args, None, stream)
+    _last_need[fn_name] = owned.numel()
 
 
 def slora_qk_rotary_fwd(batch, seq, head_dim, q, k=None, rotary=None, pos=None, eps=RMS_EPS,
@@ -662,22 +684,23 @@ def slora_linear_bwd_act8(side, batch, seq, ctx_len, k, n, W, A, B, lora_scale, 
                           ws=None, stream=None):
     """slora_linear_bwd with the layer input given as checkpoints: X8_ctx and,
     for SLICE_IN_COLS, X8_out are (codes, scales)."""
-    tok, keep = make_tokens(batch, seq, ctx_len)
+    tok, keep, TC = _tokens(batch, seq, tuple(map(int, ctx_len)))
     n_idx = 0 if idx is None else idx.numel()
-    T, TC, r = batch * seq, sum(int(c) for c in ctx_len), A.shape[0]
+    T, r = batch * seq, A.shape[0]
     cols, rows = side == SLICE_IN_COLS, side == SLICE_OUT_ROWS
     xc = None if X8_ctx is None else act8(*X8_ctx, TC if cols else T, n_idx if cols else k)
     xo = None if X8_out is None else act8(*X8_out, T - TC, k)
     # an empty channel list is still a list: its address, never read, may be null
     pidx = _fit(idx, "idx", n_idx, torch.int32) or (None if idx is None else ptr(XA_save))
     f32 = torch.float32
-    _run("slora_linear_bwd_act8",
-         [dtype_code(W), ctypes.byref(tok), k, n, _fit(W, "W", n * k, BF), _fit(A, "A", r * k, BF),
-          _fit(B, "B", n * r, BF), r, float(lora_scale), side, pidx, n_idx, _ref(xc), _ref(xo),
-          _fit(XA_save, "XA_save", T * r, f32),
-          _fit(dY_ctx, "dY_ctx", TC * n_idx if rows else T * n, BF),
-          _fit(dY_out, "dY_out", (T - TC) * n, BF),
-          _fit(dX_ctx, "dX_ctx", TC * n_idx if cols else T * k, BF),
-          _fit(dX_out, "dX_out", (T - TC) * k, BF), _fit(dA, "dA", r * k, f32),
-          _fit(dB, "dB", n * r, f32)], ws, stream)
+    _run_scratch(
+        "slora_linear_bwd_act8",
+        [dtype_code(W), ctypes.byref(tok), k, n, _fit(W, "W", n * k, BF), _fit(A, "A", r * k, BF),
+         _fit(B, "B", n * r, BF), r, float(lora_scale), side, pidx, n_idx, _ref(xc), _ref(xo),
+         _fit(XA_save, "XA_save", T * r, f32),
+         _fit(dY_ctx, "dY_ctx", TC * n_idx if rows else T * n, BF),
+         _fit(dY_out, "dY_out", (T - TC) * n, BF),
+         _fit(dX_ctx, "dX_ctx", TC * n_idx if cols else T * k, BF),
+         _fit(dX_out, "dX_out", (T - TC) * k, BF), _fit(dA, "dA", r * k, f32),
+         _fit(dB, "dB", n * r, f32)], ws, stream)
     del keep

@@ -1149,7 +1149,7 @@ slora_status qk_rotary_run(const QkDesc& D, bool backward, const slora_tokens* t
   const int max_blocks = num_sms() * std::max(shape.per_sm, 1);
   int32_t* ctx_off = nullptr;
   float* dgp = nullptr;
-  if (sliced) ctx_off = ar.take<int32_t>(size_t(D.ti.batch) + 1);
+  if (sliced && D.ti.batch > kSmallBatch) ctx_off = ar.take<int32_t>(size_t(D.ti.batch) + 1);
   // one partial of each block; the parts' blocks together are at most max_blocks + 1
   if (any_dg) dgp = ar.take<float>(size_t(max_blocks + 1) * hd);
   if (plan) return SLORA_OK;

@@ -572,7 +572,9 @@ typedef struct {
  *             tensor).  Y may be X itself (same stride) on dense rows; no other
  *             overlap.
  * Angles are exact to about 1e-7 at every position: the turns are counted in
- * 64-bit fixed point.  Sliced tensors need a workspace; dense ones none.
+ * 64-bit fixed point.  Of the forward, sliced tensors of more than 64 sequences
+ * need a workspace, nothing else; a query gives 0 where none is needed, and any
+ * aligned address but NULL runs the call then.
  * A sliced tensor has at most 32768 channels (heads * head_dim).  An entry of
  * idx outside them, or one that stands there twice, is left out (of two, either)
  * and reported by slora_device_error (SLORA_ERR_INVALID_ARG); the backward

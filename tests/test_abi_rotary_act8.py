@@ -58,10 +58,14 @@ def test_dense_calls_need_no_workspace(L):
     assert st == OK and need >= 64 * 4
 
 
-def test_sliced_calls_need_a_workspace(L):
+def test_sliced_calls(L):
     s = dict(idx=FAKE, n_idx=100, X=None, X_ctx=FAKE, X_out=FAKE, dX_ctx=FAKE, dX_out=FAKE)
-    st, need = fwd(L, dense(L, **s))
-    assert st == OK and need >= 3 * 4                                  # the sequences' offsets
+    for batch, bytes_ in ((2, 0), (64, 0), (65, 4 * 66)):              # many sequences' offsets
+        tok, keep = L.make_tokens(batch, 5, [3] * batch)
+        rows, rot = dense(L, **s), L.rotary()
+        st, need = status(L, "slora_qk_rotary_fwd", [L.BF16, ctypes.byref(tok), 64, 1e-5, ctypes.byref(rot),
+                                                     None, ctypes.byref(rows), None])
+        assert st == OK and need >= bytes_ and (need > 0) == (bytes_ > 0)
     assert bwd(L, dense(L, **s))[0] == OK
     assert fwd(L, dense(L, **s), dense(L, 2))[0] == SHAPE              # one sliced, one dense
     assert fwd(L, dense(L, **s), dt=L.F32)[0] == UNSUPPORTED
