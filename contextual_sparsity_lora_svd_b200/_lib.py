@@ -591,6 +591,8 @@ def _run_scratch(fn_name, args, ws, stream):
     if size <= _SMALL:
         if size:
             ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+            if stream is not None:  # not the allocation's own: kept until its work is done
+                ws.record_stream(stream)
             st = getattr(_lib, fn_name)(*args, ws.data_ptr(), ctypes.byref(c_sz(size)),
                                         _stream(stream))
         else:
@@ -599,6 +601,8 @@ def _run_scratch(fn_name, args, ws, stream):
             _check(fn_name, st)
             return
     owned = _run(fn_name, args, None, stream)
+    if stream is not None:
+        owned.record_stream(stream)
     _last_need[fn_name] = owned.numel()
 
 

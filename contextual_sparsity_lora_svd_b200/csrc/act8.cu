@@ -8,7 +8,7 @@
 // bf16.  A thread holds 8 channels (a 16-byte load, an 8-byte store), four
 // neighbouring lanes share a block and its maximum (two shuffles), and each
 // thread has four chunks in flight.  Packing and unpacking 8192 x 14336 bf16
-// values, 710 MB in all, take 117 us, 6.1 TB/s, the rate of a plain copy of 590 MB.
+// values, 710 MB in all, take 114 us, 6.2 TB/s, the rate of a plain copy of 590 MB.
 #include <algorithm>
 #include <type_traits>
 

@@ -26,8 +26,8 @@
 // rows are few: it computes the row's hd / 2 sines and cosines once, spread
 // over its lanes, keeps each lane's in registers and walks the heads, the next
 // ones on their way to shared memory.  Nothing in the loop waits for another
-// warp.  32 + 8 heads of 128 channels, 8192 rows: 31 us, as long as a plain copy
-// of the same 168 MB takes (33 us); with norms, fp32 dy and dg backward 61 us for
+// warp.  32 + 8 heads of 128 channels, 8192 rows: 32 us, as long as a plain copy
+// of the same 168 MB takes (33 us); with norms, fp32 dy and dg backward 60 us for
 // 336 MB.
 //
 // Sliced rows: the inverse channel list lies in shared memory; a context row's

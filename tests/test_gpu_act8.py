@@ -447,3 +447,33 @@ def test_calls_follow_one_another_without_waiting(L):
         for g, w in zip(got, want):
             assert all(torch.equal(a, b) for a, b in zip(g, w))
     assert L.lib().slora_device_error(1) == 0
+
+
+def test_scratch_of_a_call_on_another_stream_is_kept(L):
+    """Workspace that the binding takes for a call on a side stream is not handed out again before
+    that call has run: the current stream allocates and overwrites as much meanwhile."""
+    T, k, n, r = 256, 512, 384, 16
+    gen = gen_of(12)
+    W, A, B = rand(gen, (n, k)), rand(gen, (r, k)), rand(gen, (n, r))
+    X, dY, XA = rand(gen, (T, k)), rand(gen, (T, n)), rand(gen, (T, r), torch.float32)
+    X8 = L.act8_empty(T, k)
+    L.slora_act8_pack(X, *X8)
+    outs = []
+    for _ in range(6):
+        outs.append((torch.empty_like(X), torch.empty(r, k, device="cuda"), torch.empty(n, r, device="cuda")))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        stream = None
+        if i:
+            stream = side
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(2_000_000)  # about a millisecond in which the call has not begun
+        L.slora_linear_bwd_act8(L.SLICE_NONE, 1, T, [T], k, n, W, A, B, 0.5, None, X8, XA, dY, *o, stream=stream)
+        junk = [torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+                for size in (1 << 14, 1 << 16, 1 << 18, 1 << 20, 1 << 21) for _ in range(4)]
+        del junk
+    torch.cuda.synchronize()
+    for o in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(o, outs[0]))
+    assert L.lib().slora_device_error(1) == 0
