@@ -477,3 +477,111 @@ def test_scratch_of_a_call_on_another_stream_is_kept(L):
     for o in outs[1:]:
         assert all(torch.equal(a, b) for a, b in zip(o, outs[0]))
     assert L.lib().slora_device_error(1) == 0
+
+
+@pytest.mark.parametrize("side", ["none", "out_rows", "in_cols"])
+def test_linear_gradients_against_differences(L, side):
+    """dX, dA and dB of sum(Y dY), Y the sliced forward in float64 on the checkpoint's values: Y is
+    linear in each of them, so a central difference is exact; the tolerances are linear_case's."""
+    b, s, ctx, k, n, r, scale = 2, 6, [4, 3], 64, 72, 8, 0.75
+    gen = gen_of(21)
+    T, TC = b * s, sum(ctx)
+    is_ctx = np.concatenate([np.arange(s) < c for c in ctx])
+    cols = k if side == "in_cols" else n
+    idx = torch.sort(torch.randperm(cols, generator=gen, device="cuda")[:24]).values.int()
+    sel = R.f64(idx).astype(int)
+    W, A, B = rand(gen, (n, k), scale=0.125), rand(gen, (r, k), scale=0.125), rand(gen, (n, r), scale=0.1)
+    X, dY = rand(gen, (T, k)), rand(gen, (T, n))
+    keep = torch.from_numpy(is_ctx).cuda()
+    if side == "in_cols":
+        parts = [X[keep][:, idx.long()].contiguous(), X[~keep].contiguous()]
+    else:
+        parts = [X]
+    cks = []
+    x = np.zeros((T, k))
+    for t in parts:
+        cks.append(L.act8_empty(*t.shape))
+        L.slora_act8_pack(t, *cks[-1])
+    if side == "in_cols":
+        rows = np.zeros((TC, k))
+        rows[:, sel] = R.act8(R.f64(parts[0]))[2]
+        x[is_ctx], x[~is_ctx] = rows, R.act8(R.f64(parts[1]))[2]
+    else:
+        x = R.act8(R.f64(X))[2]
+    w, dy = R.f64(W), R.f64(dY)
+    drop = np.setdiff1d(np.arange(cols), sel)
+
+    def value(x, a, bb):
+        x = x.copy()
+        if side == "in_cols":
+            x[np.ix_(is_ctx, drop)] = 0
+        y = x @ w.T + scale * (x @ a.T) @ bb.T
+        if side == "out_rows":
+            y[np.ix_(is_ctx, drop)] = 0
+        return (y * dy).sum()
+
+    a64, b64 = R.f64(A), R.f64(B)
+    XA = torch.from_numpy(x @ a64.T).float().cuda()
+    dA, dB = torch.empty(r, k, device="cuda"), torch.empty(n, r, device="cuda")
+    code = {"none": L.SLICE_NONE, "out_rows": L.SLICE_OUT_ROWS, "in_cols": L.SLICE_IN_COLS}[side]
+    dXs = [torch.empty_like(t) for t in parts]
+    kw, dYc, Wd = {}, dY, W
+    if side == "out_rows":
+        dYc = dY[keep][:, idx.long()].contiguous()
+        kw = dict(dY_out=dY[~keep].contiguous())
+    elif side == "in_cols":
+        Wd = W.t().contiguous()
+        kw = dict(X8_out=cks[1], dX_out=dXs[1])
+    L.slora_linear_bwd_act8(code, b, s, ctx, k, n, Wd, A, B, scale, None if side == "none" else idx, cks[0], XA,
+                            dYc, dXs[0], dA, dB, **kw)
+    got = np.zeros((T, k))
+    if side == "in_cols":
+        block = np.zeros((TC, k))
+        block[:, sel] = R.f64(dXs[0])
+        got[is_ctx], got[~is_ctx] = block, R.f64(dXs[1])
+    else:
+        got = R.f64(dXs[0])
+
+    def differences(which, m):
+        out = np.zeros(m.shape)
+        for i in np.ndindex(m.shape):
+            args = [x, a64, b64]
+            args[which] = m.copy()
+            args[which][i] += 1.0
+            up = value(*args)
+            args[which][i] -= 2.0
+            out[i] = (up - value(*args)) / 2
+        return out
+
+    assert rel_frob(got, differences(0, x)) <= 2.0 ** -7
+    assert rel_frob(R.f64(dA), differences(1, a64)) <= 1e-5
+    assert rel_frob(R.f64(dB), differences(2, b64)) <= 1e-5
+
+
+def test_norm_gradient_against_differences(L):
+    """dX of sum(N dN) at the checkpoint's values, against central differences of the float64 norm:
+    truncation 1e-8, half a bf16 step of the result and the fp32 sum of d terms."""
+    T, d = 3, 72
+    gen = gen_of(31)
+    X, g, dN = rand(gen, (T, d)), rand(gen, (d,)), rand(gen, (T, d))
+    H8, N, N8 = L.act8_empty(T, d), torch.empty_like(X), L.act8_empty(T, d)
+    rstd, dX = torch.empty(T, device="cuda"), torch.empty_like(X)
+    L.slora_act8_pack(X, *H8)
+    V = torch.empty_like(X)
+    L.slora_act8_unpack(*H8, V)  # the forward on the values that the backward will see
+    L.slora_rmsnorm_fwd_act8(V, g, N, rstd, H8=H8, N8=N8)
+    L.slora_rmsnorm_bwd_act8(H8, rstd, g, dN, dX)
+    v, gg, dn = R.f64(V), R.f64(g), R.f64(dN)
+
+    def value(h):
+        return (h / np.sqrt((h ** 2).mean(1, keepdims=True) + 1e-5) * gg * dn).sum()
+
+    want = np.zeros((T, d))
+    for i in np.ndindex(T, d):
+        up, dn_ = v.copy(), v.copy()
+        up[i] += 1e-4
+        dn_[i] -= 1e-4
+        want[i] = (value(up) - value(dn_)) / 2e-4
+    r = R.f64(rstd)[:, None]
+    size = r * np.abs(gg * dn) + np.abs(v) * r ** 3 * np.abs(gg * dn * v).mean(1, keepdims=True)
+    assert (np.abs(R.f64(dX) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -16 * size + 1e-6).all()
