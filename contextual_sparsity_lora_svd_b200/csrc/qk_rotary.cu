@@ -373,8 +373,16 @@ struct Place {
   T* o;
 };
 
+// Blocks of kWarps warps an SM by registers: 80 a thread, 128 for the backward with
+// eight pairs a lane (80 would spill: sliced 57 -> 79 us) or one (likewise).  16 + 4
+// heads of 80 channels, 20 of them rotated, 8192 rows, sliced: backward 69 us at
+// two blocks, 59 at three; forward with eight pairs 32 at three, 35 at two or four.
+constexpr int blocks_of(bool backward, int V) {
+  return backward && (V == 8 || V == 1) ? 2 : 3;
+}
+
 template <typename T, typename G, int V, bool kInter, bool kBwd, bool kSliced>
-__global__ void __launch_bounds__(kWarps * 32, kBwd ? 2 : 3)
+__global__ void __launch_bounds__(kWarps * 32, blocks_of(kBwd, V))
     qk_rotary_kernel(const __grid_constant__ QkParams P) {
   constexpr int NU = units_per_lane<V>(), NP = packs<V>();
   constexpr int kAhead = ahead<kBwd, kSliced>();
@@ -1028,9 +1036,8 @@ constexpr double kAngles = 0.6;  // a unit's angles, in rounds (about 150 of 245
 
 // Warps of a block, its shared memory (tables and rings, and for sliced rows the
 // inverse channel list and a stage a warp) and the blocks that an SM
-// holds of them: registers allow 16 warps backward and 24 forward (the kernel's
-// launch bounds), shared memory 226 KB with 2 KB of a block's own.  Eight warps, or the smaller block that
-// keeps more warps resident.
+// holds of them: by registers (blocks_of), and by shared memory, 226 KB with 2 KB
+// of a block's own.  Eight warps, or the smaller block that keeps more warps resident.
 struct Shape {
   int warps = 1, smem = 0, per_sm = 1, stage = 0;
 };
@@ -1053,7 +1060,7 @@ Shape block_shape(const QkDesc& D, bool backward, bool sliced, int V) {
     s.stage = stage;
     s.smem = (w * D.head_dim * 4 + 15) / 16 * 16 + w * ring;
     if (sliced) s.smem += (n + 7) / 8 * 16 + w * stage * 2;
-    s.per_sm = std::min((backward ? 16 : 24) / w, 226 * 1024 / (s.smem + 2048));
+    s.per_sm = std::min(kWarps * blocks_of(backward, V) / w, 226 * 1024 / (s.smem + 2048));
     if (w == kWarps || s.warps * s.per_sm > best.warps * best.per_sm) best = s;
   }
   return best;
