@@ -227,6 +227,16 @@ def make_tokens(batch: int, seq: int, ctx_len) -> tuple[Tokens, object]:
     return Tokens(batch, seq, ctypes.cast(arr, P_I32)), arr
 
 
+def _scratch(size, stream):
+    """Device bytes for a call on `stream` (None: the current one), from that stream's own pool.
+    A block of another stream's pool may still be in use there; and this one, dropped with the
+    call pending, goes to later work of the same stream alone."""
+    if stream is None:
+        return torch.empty(size, dtype=torch.uint8, device="cuda")
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=torch.uint8, device="cuda")
+
+
 def _run(fn_name, args_before_ws, ws, stream):
     """Query the workspace size, take/allocate it, run the call."""
     f = getattr(_lib, fn_name)
@@ -234,7 +244,7 @@ def _run(fn_name, args_before_ws, ws, stream):
     _check(fn_name, f(*args_before_ws, None, ctypes.byref(need), st))
     owned = None
     if ws is None:
-        owned = torch.empty(max(int(need.value), 16), dtype=torch.uint8, device="cuda")
+        owned = _scratch(max(int(need.value), 16), stream)
         ws = owned
     have = c_sz(ws.numel() * ws.element_size())
     _check(fn_name, f(*args_before_ws, ptr(ws), ctypes.byref(have), st))
@@ -590,9 +600,7 @@ def _run_scratch(fn_name, args, ws, stream):
     size = _last_need.get(fn_name, 0)
     if size <= _SMALL:
         if size:
-            ws = torch.empty(size, dtype=torch.uint8, device="cuda")
-            if stream is not None:  # not the allocation's own: kept until its work is done
-                ws.record_stream(stream)
+            ws = _scratch(size, stream)
             st = getattr(_lib, fn_name)(*args, ws.data_ptr(), ctypes.byref(c_sz(size)),
                                         _stream(stream))
         else:
@@ -600,10 +608,7 @@ def _run_scratch(fn_name, args, ws, stream):
         if st != 4:  # SLORA_ERR_WORKSPACE
             _check(fn_name, st)
             return
-    owned = _run(fn_name, args, None, stream)
-    if stream is not None:
-        owned.record_stream(stream)
-    _last_need[fn_name] = owned.numel()
+    _last_need[fn_name] = _run(fn_name, args, None, stream).numel()
 
 
 def slora_qk_rotary_fwd(batch, seq, head_dim, q, k=None, rotary=None, pos=None, eps=RMS_EPS,

@@ -263,3 +263,45 @@ def test_reference_frequencies_by_hand():
     assert np.allclose(f, [1.0, 0.1 / 8], rtol=1e-15)
     _, m = R.frequencies(8, scaling="yarn", factor=4.0, orig_len=4096)
     assert m == pytest.approx(0.1 * np.log(4.0) + 1.0)
+
+
+def test_scratch_comes_from_the_pool_of_the_call_s_stream(L, monkeypatch):
+    """Scratch that the binding takes for a call on a given stream is allocated with that stream
+    current: from another stream's pool it could be a block whose last user still runs."""
+    class Stream:
+        cuda_stream = 0x40
+    current, seen = [None], []
+
+    class Within:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *error):
+            current.pop()
+
+    def empty(size, **kw):
+        seen.append((size, current[-1]))
+        return torch.zeros(size, dtype=torch.uint8)
+
+    class Calls:
+        @staticmethod
+        def call(*args):  # needs 96 bytes
+            ws, size = args[-3], args[-2]._obj
+            if ws is None:
+                size.value = 96
+                return OK
+            return OK if size.value >= 96 else WORKSPACE
+
+    monkeypatch.setattr(torch.cuda, "stream", Within)
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(L, "_lib", Calls)
+    monkeypatch.setattr(L, "_last_need", {})
+    st = Stream()
+    L._run("call", [], None, st)
+    L._run_scratch("call", [], None, st)  # by its query
+    L._run_scratch("call", [], None, st)  # by the last call's need
+    assert seen == [(96, st)] * 3
+    assert L._last_need == {"call": 96} and current == [None]

@@ -585,3 +585,38 @@ def test_norm_gradient_against_differences(L):
     r = R.f64(rstd)[:, None]
     size = r * np.abs(gg * dn) + np.abs(v) * r ** 3 * np.abs(gg * dn * v).mean(1, keepdims=True)
     assert (np.abs(R.f64(dX) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -16 * size + 1e-6).all()
+
+
+def test_scratch_of_a_pending_call_is_not_given_to_another_stream(L):
+    """A call on the current stream drops its scratch with its kernels pending; calls on a side
+    stream at once, without a workspace of their own, must not get that block."""
+    T, k, n, r = 256, 512, 384, 16
+    gen = gen_of(13)
+    W, A, B = rand(gen, (n, k)), rand(gen, (r, k)), rand(gen, (n, r))
+    X, XA = rand(gen, (T, k)), rand(gen, (T, r), torch.float32)
+    dYs = [rand(gen, (T, n)) for _ in range(2)]
+    X8 = L.act8_empty(T, k)
+    L.slora_act8_pack(X, *X8)
+
+    def outputs():
+        return torch.empty_like(X), torch.empty(r, k, device="cuda"), torch.empty(n, r, device="cuda")
+
+    def call(dY, o, stream=None):
+        L.slora_linear_bwd_act8(L.SLICE_NONE, 1, T, [T], k, n, W, A, B, 0.5, None, X8, XA, dY, *o, stream=stream)
+
+    want = [outputs() for _ in dYs]
+    for dY, o in zip(dYs, want):
+        call(dY, o)
+        torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        got = [outputs() for _ in dYs]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(2_000_000)  # about a millisecond in which the first call has not begun
+        call(dYs[0], got[0])
+        for _ in range(20):           # beside it, from before its start to after its end
+            call(dYs[1], got[1], stream=side)
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
+    assert L.lib().slora_device_error(1) == 0
