@@ -466,6 +466,15 @@ def _same(t, what, dt):
         raise TypeError(f"{what} is {t.dtype}, the rows are {dt}")
 
 
+def _here(*tensors):
+    """Refuses tensors (None stays None) that are not on the current CUDA device."""
+    for t in tensors:
+        if t is not None:
+            at = t.get_device()  # -1: on the CPU
+            if at < 0 or at != torch._C._cuda_getDevice():
+                raise ValueError(f"a tensor on {t.device} is no operand of a call on the current CUDA device")
+
+
 def _fit(t, what, n, dt):
     """Address of a contiguous tensor of n elements (None stays None)."""
     if t is None:
@@ -525,6 +534,10 @@ def qk_rows(heads, X=None, g=None, Y=None, dY=None, dX=None, dg=None, idx=None, 
         # an empty list is still a list: its address, never read, may be null
         r.idx = _whole(idx, "idx", torch.int32) or r.X_out or r.dX_out or r.Y or r.dY
     r.tensors = (X, g, Y, dY, dX, dg, idx, X_ctx, X_out, dX_ctx, dX_out)
+    r.at = first.get_device()
+    for t in r.tensors:
+        if t is not None and t.get_device() != r.at:
+            raise ValueError(f"rows on {first.device} and on {t.device}")
     return r
 
 
@@ -571,6 +584,10 @@ def _qk(fn, head, batch, seq, head_dim, q, k, rotary_, pos, eps, ctx_len, ws, st
     _sizes(q, batch * seq, TC, head_dim)
     if k is not None:
         _sizes(k, batch * seq, TC, head_dim)
+    for rows in (q, k):  # (a qk_rows' tensors are all where its first one is)
+        if rows is not None and (rows.at < 0 or rows.at != torch._C._cuda_getDevice()):
+            _here(*rows.tensors)
+    _here(pos, ws)
     args = head + [ctypes.byref(tok), head_dim, eps, ctypes.byref(rotary_ or rotary()), ptr(pos),
                    ctypes.byref(q), kr]
     _run_scratch(fn, args, ws, stream)
@@ -656,6 +673,7 @@ def slora_act8_pack(X, codes, scales, stream=None):
     T, d = X.shape
     px, ldx = _rows(X, "X")
     c = act8(codes, scales, T, d)
+    _here(X, codes, scales)
     _run_plain("slora_act8_pack", [dtype_code(X), T, d, px, ldx, ctypes.byref(c)], stream)
 
 
@@ -663,6 +681,7 @@ def slora_act8_unpack(codes, scales, X, stream=None):
     T, d = X.shape
     px, ldx = _rows(X, "X")
     c = act8(codes, scales, T, d)
+    _here(X, codes, scales)
     _run_plain("slora_act8_unpack", [dtype_code(X), T, d, ctypes.byref(c), px, ldx], stream)
 
 
@@ -672,20 +691,21 @@ def slora_rmsnorm_fwd_act8(X, g, N, rstd=None, A=None, H=None, H8=None, N8=None,
     T, d = X.shape
     h8 = None if H8 is None else act8(*H8, T, d)
     n8 = None if N8 is None else act8(*N8, T, d)
-    _run_plain("slora_rmsnorm_fwd_act8",
-               [BF16, T, d, eps, _fit(X, "X", T * d, BF), _fit(A, "A", T * d, BF),
-                _fit(g, "g", d, BF), _fit(H, "H", T * d, BF), _fit(N, "N", T * d, BF),
-                _fit(rstd, "rstd", T, torch.float32), _ref(h8), _ref(n8)], stream)
+    args = [BF16, T, d, eps, _fit(X, "X", T * d, BF), _fit(A, "A", T * d, BF), _fit(g, "g", d, BF),
+            _fit(H, "H", T * d, BF), _fit(N, "N", T * d, BF),
+            _fit(rstd, "rstd", T, torch.float32), _ref(h8), _ref(n8)]
+    _here(X, g, N, rstd, A, H, *(H8 or ()), *(N8 or ()))
+    _run_plain("slora_rmsnorm_fwd_act8", args, stream)
 
 
 def slora_rmsnorm_bwd_act8(H8, rstd, g, dN0, dX, dN1=None, dN2=None, dRes=None, stream=None):
     T, d = dN0.shape
     h8 = act8(*H8, T, d)
-    _run_plain("slora_rmsnorm_bwd_act8",
-               [BF16, T, d, ctypes.byref(h8), _fit(rstd, "rstd", T, torch.float32),
-                _fit(g, "g", d, BF), _fit(dN0, "dN0", T * d, BF), _fit(dN1, "dN1", T * d, BF),
-                _fit(dN2, "dN2", T * d, BF), _fit(dRes, "dRes", T * d, BF),
-                _fit(dX, "dX", T * d, BF)], stream)
+    args = [BF16, T, d, ctypes.byref(h8), _fit(rstd, "rstd", T, torch.float32), _fit(g, "g", d, BF),
+            _fit(dN0, "dN0", T * d, BF), _fit(dN1, "dN1", T * d, BF), _fit(dN2, "dN2", T * d, BF),
+            _fit(dRes, "dRes", T * d, BF), _fit(dX, "dX", T * d, BF)]
+    _here(*H8, rstd, g, dN0, dN1, dN2, dRes, dX)
+    _run_plain("slora_rmsnorm_bwd_act8", args, stream)
 
 
 def slora_linear_bwd_act8(side, batch, seq, ctx_len, k, n, W, A, B, lora_scale, idx, X8_ctx,
@@ -702,14 +722,14 @@ def slora_linear_bwd_act8(side, batch, seq, ctx_len, k, n, W, A, B, lora_scale, 
     # an empty channel list is still a list: its address, never read, may be null
     pidx = _fit(idx, "idx", n_idx, torch.int32) or (None if idx is None else ptr(XA_save))
     f32 = torch.float32
-    _run_scratch(
-        "slora_linear_bwd_act8",
-        [dtype_code(W), ctypes.byref(tok), k, n, _fit(W, "W", n * k, BF), _fit(A, "A", r * k, BF),
-         _fit(B, "B", n * r, BF), r, float(lora_scale), side, pidx, n_idx, _ref(xc), _ref(xo),
-         _fit(XA_save, "XA_save", T * r, f32),
-         _fit(dY_ctx, "dY_ctx", TC * n_idx if rows else T * n, BF),
-         _fit(dY_out, "dY_out", (T - TC) * n, BF),
-         _fit(dX_ctx, "dX_ctx", TC * n_idx if cols else T * k, BF),
-         _fit(dX_out, "dX_out", (T - TC) * k, BF), _fit(dA, "dA", r * k, f32),
-         _fit(dB, "dB", n * r, f32)], ws, stream)
+    args = [dtype_code(W), ctypes.byref(tok), k, n, _fit(W, "W", n * k, BF), _fit(A, "A", r * k, BF),
+            _fit(B, "B", n * r, BF), r, float(lora_scale), side, pidx, n_idx, _ref(xc), _ref(xo),
+            _fit(XA_save, "XA_save", T * r, f32),
+            _fit(dY_ctx, "dY_ctx", TC * n_idx if rows else T * n, BF),
+            _fit(dY_out, "dY_out", (T - TC) * n, BF),
+            _fit(dX_ctx, "dX_ctx", TC * n_idx if cols else T * k, BF),
+            _fit(dX_out, "dX_out", (T - TC) * k, BF), _fit(dA, "dA", r * k, f32),
+            _fit(dB, "dB", n * r, f32)]
+    _here(W, A, B, idx, *(X8_ctx or ()), *(X8_out or ()), XA_save, dY_ctx, dY_out, dX_ctx, dX_out, dA, dB, ws)
+    _run_scratch("slora_linear_bwd_act8", args, ws, stream)
     del keep

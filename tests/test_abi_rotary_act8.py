@@ -305,3 +305,55 @@ def test_scratch_comes_from_the_pool_of_the_call_s_stream(L, monkeypatch):
     L._run_scratch("call", [], None, st)  # by the last call's need
     assert seen == [(96, st)] * 3
     assert L._last_need == {"call": 96} and current == [None]
+
+
+def test_binding_refuses_tensors_off_the_device(L, monkeypatch):
+    """Tensors that fit in type and size but lie on the CPU: their addresses never reach a call."""
+    class Calls:
+        def __getattr__(self, name):
+            raise AssertionError(f"{name} was reached")
+
+    monkeypatch.setattr(L, "_lib", Calls())
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    z = lambda *s, dt=bf: torch.zeros(*s, dtype=dt)  # noqa: E731
+    ck = lambda T, d: L.act8_empty(T, d, device="cpu")  # noqa: E731
+    X, g = z(4, 128), z(64)
+    dense = L.qk_rows(2, X=X, g=g, Y=z(4, 128), dY=z(4, 128), dX=z(4, 128), dg=z(64, dt=f32))
+    cut = L.qk_rows(2, g=g, idx=z(8, dt=i32), X_ctx=z(2, 8), X_out=z(2, 128), Y=z(4, 128), dY=z(4, 128),
+                    dX_ctx=z(2, 8), dX_out=z(2, 128))
+    calls = [lambda f=f, r=r, c=c: f(2, 2, 64, r, ctx_len=c)
+             for f in (L.slora_qk_rotary_fwd, L.slora_qk_rotary_bwd) for r, c in ((dense, None), (cut, [1, 1]))]
+    calls += [lambda: L.slora_act8_pack(X, *ck(4, 128)), lambda: L.slora_act8_unpack(*ck(4, 128), X),
+              lambda: L.slora_rmsnorm_fwd_act8(X, z(128), z(4, 128), H8=ck(4, 128)),
+              lambda: L.slora_rmsnorm_bwd_act8(ck(4, 128), z(4, dt=f32), z(128), X, z(4, 128)),
+              lambda: L.slora_linear_bwd_act8(
+                  L.SLICE_OUT_ROWS, 2, 2, [1, 1], 64, 64, z(64, 64), z(8, 64), z(64, 8), 1.0, z(16, dt=i32),
+                  ck(4, 64), z(4, 8, dt=f32), z(2, 16), z(4, 64), z(8, 64, dt=f32), z(64, 8, dt=f32),
+                  dY_out=z(2, 64))]
+    for call in calls:
+        with pytest.raises(ValueError, match="on cpu"):
+            call()
+
+
+def test_binding_refuses_tensors_of_another_device(L, monkeypatch):
+    """The same for a tensor of a GPU that is not the current one, and for rows on two devices."""
+    class On(torch.Tensor):  # stands in for a tensor of GPU `gpu`
+        def get_device(self):
+            return self.gpu
+
+    def on(gpu):
+        t = torch.zeros(4, 128, dtype=torch.bfloat16).as_subclass(On)
+        t.gpu = gpu
+        return t
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    L._here(on(1), None, on(1))
+    for bad in ([on(0)], [on(1), on(2)], [on(-1)]):
+        with pytest.raises(ValueError):
+            L._here(*bad)
+    assert L.qk_rows(2, X=on(1), Y=on(1)).at == 1
+    with pytest.raises(ValueError):
+        L.qk_rows(2, X=on(1), Y=on(0))
+    rows = L.qk_rows(2, X=on(0), Y=on(0))
+    with pytest.raises(ValueError):
+        L.slora_qk_rotary_fwd(2, 2, 64, rows)
