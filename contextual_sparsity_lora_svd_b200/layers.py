@@ -365,6 +365,13 @@ class DecoderStack(_Runner):
                  seq, ctx_len, qk_sparsity, ffn_sparsity, X, dY, rope_base=10000.0,
                  eps=1e-5, rotary=None, qk_norm=False, act8=False):
         H, KV, hd = heads, kv_heads, head_dim
+        if qk_norm:  # the calls get their addresses alone
+            for l, w in enumerate(layers):
+                for nm in ("gq", "gk"):
+                    if w.get(nm) is None:
+                        raise ValueError(f"layer {l}: qk_norm needs the gain {nm}")
+                    L._fit(w[nm], f"layer {l}: {nm}", hd, torch.bfloat16)
+                    L._here(w[nm])
         nq, nkv, T = H * hd, KV * hd, batch * seq
         tok, tok_keep = L.make_tokens(batch, seq, ctx_len)
         self._keep = [tok, tok_keep, X, dY, layers]
@@ -514,7 +521,7 @@ class DecoderStack(_Runner):
                     back = lin_bwd(base, [L.SLICE_OUT_ROWS, L.ptr(ii), ni], S_, XA, dYc, dYo, dXn,
                                    G["dA" + nm], G["dB" + nm])
                     if turn:
-                        rope, unrope = qk_turn(nm, n // hd, w.get("g" + nm) if qk_norm else None,
+                        rope, unrope = qk_turn(nm, n // hd, w["g" + nm] if qk_norm else None,
                                                R, dR, idx=ii, X_ctx=Yc, X_out=Yo, dX_ctx=dYc,
                                                dX_out=dYo)
                 else:
@@ -531,7 +538,7 @@ class DecoderStack(_Runner):
                     back = lin_bwd(base, [L.SLICE_NONE, None, 0], S_, XA, dYd, None, dXn,
                                    G["dA" + nm], G["dB" + nm])
                     if turn:
-                        rope, unrope = qk_turn(nm, n // hd, w.get("g" + nm) if qk_norm else None,
+                        rope, unrope = qk_turn(nm, n // hd, w["g" + nm] if qk_norm else None,
                                                R, dR, X=Y, dX=dYd)
                 proj[nm] = (fwd, rope, unrope, back)
             vbase = [L.BF16, ctypes.byref(tok), d, nkv, L.ptr(w["Wv"]), L.ptr(w["Av"]),

@@ -357,3 +357,28 @@ def test_binding_refuses_tensors_of_another_device(L, monkeypatch):
     rows = L.qk_rows(2, X=on(0), Y=on(0))
     with pytest.raises(ValueError):
         L.slora_qk_rotary_fwd(2, 2, 64, rows)
+
+
+@pytest.mark.parametrize("which", ["gq", "gk"])
+@pytest.mark.parametrize("bad,error", [
+    (None, ValueError), (torch.ones(63, dtype=torch.bfloat16), ValueError), (torch.ones(64), TypeError),
+    (torch.ones(128, dtype=torch.bfloat16)[::2], ValueError), (torch.ones(64, dtype=torch.bfloat16), ValueError)])
+def test_stack_refuses_gains_that_do_not_fit(L, which, bad, error, monkeypatch):
+    """A layer without a gain, with a short or strided one or one of another type (and the last: one
+    off the device) is refused before anything is allocated."""
+    from contextual_sparsity_lora_svd_b200 import layers
+
+    def nothing(*a, **k):
+        raise AssertionError("allocated")
+
+    good = torch.ones(64, dtype=torch.bfloat16)
+    lays = [dict(gq=good, gk=good), dict(gq=good, gk=good)]
+    lays[1][which] = bad
+    if bad is None:
+        del lays[1][which]
+    here = L._here
+    monkeypatch.setattr(L, "_here", lambda t: None if t is good else here(t))
+    monkeypatch.setattr(torch, "empty", nothing)
+    with pytest.raises(error):
+        layers.DecoderStack(lays, 256, 4, 2, 64, 688, 8, 8, 1.0, 1, 8, [8], [0.0] * 2, [0.0] * 2, None, None,
+                            qk_norm=True)
