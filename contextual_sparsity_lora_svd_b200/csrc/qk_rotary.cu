@@ -9,7 +9,8 @@
 //   backward  dn = R^T dy;  u = g dn;  dx = r u - x r^3 mean(x u);
 //             dg = sum over rows and heads of dn x r
 // R turns pair p of the leading `dims` channels by pos * f_p; the remaining
-// channels are pairs of angle 0.  r is recomputed in the backward: the head is
+// channels are grouped into pairs too, but not turned by angle 0: an infinite or NaN
+// partner times sin 0 is no zero.  r is recomputed in the backward: the head is
 // in registers anyway, so no statistic is stored between the two.
 //
 // Angles: f_p / 2 pi is held in units of 2^-64 turn, so pos * f_p modulo one
@@ -381,7 +382,10 @@ constexpr int blocks_of(bool backward, int V) {
   return backward && (V == 8 || V == 1) ? 2 : 3;
 }
 
-template <typename T, typename G, int V, bool kInter, bool kBwd, bool kSliced>
+// kPart: heads of which only the leading channels are rotated.  (With the whole heads'
+// kernels looking at each unit too, 32 + 8 heads of 128, 8192 rows, forward with norms
+// took 33 us for 32.)
+template <typename T, typename G, int V, bool kInter, bool kBwd, bool kSliced, bool kPart>
 __global__ void __launch_bounds__(kWarps * 32, blocks_of(kBwd, V))
     qk_rotary_kernel(const __grid_constant__ QkParams P) {
   constexpr int NU = units_per_lane<V>(), NP = packs<V>();
@@ -445,7 +449,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_of(kBwd, V))
   // this lane's place: team `team` of the warp, units lt, lt + tl, ...; group B
   // lies `apart` channels behind group A
   const int lt = lane % tl, team = lane / tl, tpw = 32 / tl;
-  int offa[NU], apart[NU];
+  int offa[NU], apart[NU], turned[NU];  // turned: the unit's leading pairs that are rotated
   bool act[NU];
   f2 glo[NU][NP], ghi[NU][NP];
   const bool norm = q.g != nullptr;
@@ -454,6 +458,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_of(kBwd, V))
   for (int j = 0; j < NU; ++j) {
     const int u = lt + j * tl, p0 = u * V;
     act[j] = u < U;
+    turned[j] = dims / 2 - p0;
     if (!act[j]) {
       offa[j] = apart[j] = 0;
     } else if (kInter) {
@@ -490,6 +495,39 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_of(kBwd, V))
   }
   f2 cs[NU][NP], sn[NU][NP];
   const f2 minus1 = pack2(-1.0f, -1.0f);
+  // Pack i of unit j by its angles, forwards or back.
+  auto turn = [&](int j, int i, f2& lo, f2& hi) {
+    const f2 l = lo, m = hi;
+    if constexpr (kBwd) {
+      lo = fma2(m, sn[j][i], mul2(l, cs[j][i]));
+      hi = fma2(mul2(l, sn[j][i]), minus1, mul2(m, cs[j][i]));
+    } else {
+      lo = fma2(mul2(m, sn[j][i]), minus1, mul2(l, cs[j][i]));
+      hi = fma2(m, cs[j][i], mul2(l, sn[j][i]));
+    }
+  };
+  // Unit j: of a head that is rotated in part only the pairs that are (in the half layout
+  // all of a unit's or none, else the leading ones).
+  auto turn_unit = [&](int j, f2 (&lo)[NP], f2 (&hi)[NP]) {
+    if (!kPart || turned[j] >= V) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) turn(j, i, lo[i], hi[i]);
+    } else if (kInter && turned[j] > 0) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        f2 a = lo[i], b = hi[i];
+        turn(j, i, a, b);
+        float a0, a1, b0, b1, l0, l1, m0, m1;
+        unpack2(a, a0, a1);
+        unpack2(b, b0, b1);
+        unpack2(lo[i], l0, l1);
+        unpack2(hi[i], m0, m1);
+        const bool first = 2 * i < turned[j], second = 2 * i + 1 < turned[j];
+        lo[i] = pack2(first ? a0 : l0, second ? a1 : l1);
+        hi[i] = pack2(first ? b0 : m0, second ? b1 : m1);
+      }
+    }
+  };
 
   using At = Place<T, G>;
   const int units = P.T << q.lg_chunks, stride = q.blocks * nwarps, step = tpw * hd;
@@ -683,9 +721,10 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_of(kBwd, V))
             l = mul2(mul2(l, rs2), glo[j][i]);
             m = mul2(mul2(m, rs2), ghi[j][i]);
           }
-          lo[i] = fma2(mul2(m, sn[j][i]), minus1, mul2(l, cs[j][i]));
-          hi[i] = fma2(m, cs[j][i], mul2(l, sn[j][i]));
+          lo[i] = l;
+          hi[i] = m;
         }
+        turn_unit(j, lo, hi);
         if (valid && act[j]) store(w, j, lo, hi);
       }
     } else {
@@ -705,17 +744,14 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_of(kBwd, V))
             ld_vec(y + apart[j], yb);
           }
         }
-        f2 ylo[NP], yhi[NP];
-        members<G, V, kInter>(ya, yb, ylo, yhi);
+        members<G, V, kInter>(ya, yb, dlo[j], dhi[j]);
+        turn_unit(j, dlo[j], dhi[j]);
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          dlo[j][i] = fma2(yhi[i], sn[j][i], mul2(ylo[i], cs[j][i]));
-          dhi[j][i] = fma2(mul2(ylo[i], sn[j][i]), minus1, mul2(yhi[i], cs[j][i]));
+        for (int i = 0; i < NP; ++i)
           if (norm) {
             dot = fma2(mul2(xlo[j][i], glo[j][i]), dlo[j][i], dot);
             dot = fma2(mul2(xhi[j][i], ghi[j][i]), dhi[j][i], dot);
           }
-        }
       }
       if (norm) {
         float sum, proj;
@@ -982,9 +1018,9 @@ struct Geometry {
   int warps, smem, grid;
 };
 
-template <typename T, typename G, int V, bool kInter, bool kBwd, bool kSliced>
+template <typename T, typename G, int V, bool kInter, bool kBwd, bool kSliced, bool kPart>
 slora_status launch(const QkParams& P, const Geometry& g, cudaStream_t st) {
-  auto kernel = qk_rotary_kernel<T, G, V, kInter, kBwd, kSliced>;
+  auto kernel = qk_rotary_kernel<T, G, V, kInter, kBwd, kSliced, kPart>;
   if (g.smem > 48 * 1024)
     SLORA_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, g.smem));
   SLORA_CUDA(launch_early(kernel, dim3(unsigned(g.grid)), g.warps * 32, size_t(g.smem), st, P));
@@ -992,10 +1028,14 @@ slora_status launch(const QkParams& P, const Geometry& g, cudaStream_t st) {
 }
 template <typename T, typename G, int V, bool kInter, bool kBwd>
 slora_status launch_s(bool sliced, const QkParams& P, const Geometry& g, cudaStream_t st) {
+  const bool part = P.dims < P.hd;
   if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-    if (sliced) return launch<T, G, V, kInter, kBwd, true>(P, g, st);
+    if (sliced)
+      return part ? launch<T, G, V, kInter, kBwd, true, true>(P, g, st)
+                  : launch<T, G, V, kInter, kBwd, true, false>(P, g, st);
   }
-  return launch<T, G, V, kInter, kBwd, false>(P, g, st);
+  return part ? launch<T, G, V, kInter, kBwd, false, true>(P, g, st)
+              : launch<T, G, V, kInter, kBwd, false, false>(P, g, st);
 }
 template <typename T, typename G, bool kBwd>
 slora_status launch_v(int V, bool inter, bool sliced, const QkParams& P,

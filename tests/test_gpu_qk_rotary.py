@@ -421,3 +421,54 @@ def test_equals_the_packed_rotation(L):
     want = R.rotate(heads_of(X, h), np.tile(np.arange(s), b), freq, m, hd, "half")
     for t in (Y, Z):
         check(t, want, pair_size(want, hd, "half"), torch.bfloat16, "rotation")
+
+
+def same_places(got, want, what):
+    """Infinities and NaN where the formula has them, none elsewhere."""
+    got = R.f64(got).reshape(want.shape)
+    assert np.array_equal(np.isnan(got), np.isnan(want)), what
+    inf = np.isinf(want)
+    assert np.array_equal(np.isinf(got), inf) and np.array_equal(got[inf], want[inf]), what
+    return np.isfinite(want)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("hd,dims", [(64, 32), (96, 48), (80, 20), (128, 8), (24, 4), (36, 34), (48, 20), (10, 4)])
+@pytest.mark.parametrize("norm", [False, True])
+def test_infinities_in_unrotated_channels_stay_there(L, dt, layout, hd, dims, norm):
+    """Channels behind the rotated ones meet no other channel: an infinite or NaN value of one is
+    seen by its head's norm alone, and by no other channel's output, gradient or gain gradient."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(hd + dims)
+    T, h = 4, 3
+    X, dY = rand(gen, (T, h * hd), dt), rand(gen, (T, h * hd), dt)
+    g = rand(gen, (hd,), dt, 0.3) + 1 if norm else None
+    for t in (X, dY):  # in an even, an odd and the last unrotated channel of different heads
+        t[0, dims], t[1, hd + dims + 1], t[2, 3 * hd - 1] = float("inf"), float("nan"), float("-inf")
+    rt = L.rotary(layout=layout, dims=dims)
+    freq, m = R.frequencies(dims)
+    place = np.arange(T)
+    Y, dX = torch.empty_like(X), torch.empty_like(X)
+    L.slora_qk_rotary_fwd(1, T, hd, L.qk_rows(h, X=X, g=g, Y=Y), rotary=rt)
+    gg = None if g is None else R.f64(g)
+    with np.errstate(invalid="ignore"):
+        want = R.qk_forward(heads_of(X, h), gg, 1e-5, place, freq, m, dims, layout)
+    fine = same_places(Y, want, "Y")
+    size = np.where(fine, pair_size(np.where(fine, want, 0), dims, layout), 0)
+    check(torch.from_numpy(np.where(fine, R.f64(Y).reshape(want.shape), 0)), np.where(fine, want, 0), size, dt, "Y")
+    if not norm:
+        L.slora_qk_rotary_bwd(1, T, hd, L.qk_rows(h, X=X, dY=dY, dX=dX), rotary=rt)
+        want = R.rotate(heads_of(dY, h), place, freq, m, dims, layout, back=True)
+        fine = same_places(dX, want, "dX")
+        got = torch.from_numpy(np.where(fine, R.f64(dX).reshape(want.shape), 0))
+        want = np.where(fine, want, 0)
+        check(got, want, pair_size(want, dims, layout), dt, "dX")
+        assert torch.equal(dX.view(T, h, hd)[..., dims:].isfinite(), dY.view(T, h, hd)[..., dims:].isfinite())
+        return
+    dg = torch.empty(hd, device="cuda")  # a clean x under this dY: its heads' dX are lost, the sums are not
+    X = rand(gen, (T, h * hd), dt)
+    L.slora_qk_rotary_bwd(1, T, hd, L.qk_rows(h, X=X, g=g, dY=dY, dX=dX, dg=dg), rotary=rt)
+    bad = torch.zeros(hd, dtype=torch.bool, device="cuda")
+    bad[dims], bad[dims + 1], bad[hd - 1] = True, True, True
+    assert torch.equal(~dg.isfinite(), bad)
