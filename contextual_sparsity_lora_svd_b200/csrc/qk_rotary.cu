@@ -1017,12 +1017,17 @@ __global__ void __launch_bounds__(1024) qk_offsets_kernel(const __grid_constant_
 struct Geometry {
   int warps, smem, grid;
 };
+constexpr int kSmShared = 226 * 1024;            // that blocks share, 2 KB of each its own
+constexpr int kMostShared = kSmShared - 2 * 1024;  // a block's dynamic part
 
 template <typename T, typename G, int V, bool kInter, bool kBwd, bool kSliced, bool kPart>
 slora_status launch(const QkParams& P, const Geometry& g, cudaStream_t st) {
   auto kernel = qk_rotary_kernel<T, G, V, kInter, kBwd, kSliced, kPart>;
+  // the limit belongs to the kernel, not to this call: always the same one, or a smaller
+  // call on another host thread would lower it under this call's launch
   if (g.smem > 48 * 1024)
-    SLORA_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, g.smem));
+    SLORA_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kMostShared));
   SLORA_CUDA(launch_early(kernel, dim3(unsigned(g.grid)), g.warps * 32, size_t(g.smem), st, P));
   return SLORA_OK;
 }
@@ -1100,7 +1105,7 @@ Shape block_shape(const QkDesc& D, bool backward, bool sliced, int V) {
     s.stage = stage;
     s.smem = (w * D.head_dim * 4 + 15) / 16 * 16 + w * ring;
     if (sliced) s.smem += (n + 7) / 8 * 16 + w * stage * 2;
-    s.per_sm = std::min(kWarps * blocks_of(backward, V) / w, 226 * 1024 / (s.smem + 2048));
+    s.per_sm = std::min(kWarps * blocks_of(backward, V) / w, kSmShared / (s.smem + 2048));
     if (w == kWarps || s.warps * s.per_sm > best.warps * best.per_sm) best = s;
   }
   return best;

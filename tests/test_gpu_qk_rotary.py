@@ -7,6 +7,9 @@ Tolerances count roundings: a stored bf16 value is off by half a step, 2^-8
 relative; the fp32 work before it (angle 2^-23, products, rsqrt 2^-22, sums of
 at most 256 squares) by less than 2^-18 of the terms it adds, which is what an
 fp32 result may be off by."""
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -472,3 +475,56 @@ def test_infinities_in_unrotated_channels_stay_there(L, dt, layout, hd, dims, no
     bad = torch.zeros(hd, dtype=torch.bool, device="cuda")
     bad[dims], bad[dims + 1], bad[hd - 1] = True, True, True
     assert torch.equal(~dg.isfinite(), bad)
+
+
+@pytest.mark.parametrize("shapes,kept", [([(32, 128), (8, 128)], 0.5), ([(4, 256), (4, 128)], None)])
+def test_calls_from_host_threads(L, shapes, kept):
+    """Calls of one kernel whose shared memory differs, from six host threads at once: every one is
+    launched and gives its bits (sliced backward of 32 and of 8 heads; dense backward in fp32 of
+    heads of 256 and of 128 channels)."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    b, s, ctx = 1, 40, [25]
+    tok, keep = L.make_tokens(b, s, ctx)
+    rot, size, dt = L.rotary(), L.c_sz(0), L.BF16 if kept else L.F32
+    jobs = []
+    for h, hd in shapes * 3:
+        n = h * hd
+        if kept:
+            idx = torch.randperm(n, generator=gen, device="cuda")[:int(kept * n)].int()
+            Xc, Xo, _, _ = sliced(gen, b, s, ctx, h, hd, idx)
+            outs = [torch.empty_like(Xc), torch.empty_like(Xo)]
+            rows = dict(idx=idx, X_ctx=Xc, X_out=Xo, dX_ctx=outs[0], dX_out=outs[1])
+        else:
+            outs = [torch.empty(b * s, n, device="cuda")]
+            rows = dict(X=rand(gen, (b * s, n), torch.float32), dX=outs[0])
+        g = rand(gen, (hd,), torch.bfloat16 if kept else torch.float32)
+        rows = L.qk_rows(h, g=g, dY=rand(gen, (b * s, n), torch.float32), **rows)
+        stream = torch.cuda.Stream()
+        # the C call alone: the binding's Python would hold the interpreter most of the time
+        args = (dt, L.F32, ctypes.byref(tok), hd, 1e-5, ctypes.byref(rot), None, ctypes.byref(rows), None, 16,
+                ctypes.byref(size), stream.cuda_stream)
+        torch.cuda.synchronize()
+        assert L.lib().slora_qk_rotary_bwd(*args) == 0
+        torch.cuda.synchronize()
+        jobs.append((args, rows, stream, outs, [t.clone() for t in outs]))
+    failed = []
+    start = threading.Barrier(len(jobs))
+
+    def loop(args):
+        call = L.lib().slora_qk_rotary_bwd
+        start.wait()
+        for i in range(5000):
+            if call(*args):
+                failed.append((i, L._lib_err()))
+                return
+
+    threads = [threading.Thread(target=loop, args=(j[0],)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    for _, _, _, outs, want in jobs:
+        assert all(torch.equal(a, w) for a, w in zip(outs, want))
