@@ -56,8 +56,12 @@
 
 namespace slora {
 
+constexpr long long kWaitBudget = 2000000000LL;  // ~1 s of SM clocks per wait
 __device__ int g_rank_error = 0;
 __device__ int g_rank_bad_index = 0;
+// Budget of rank_sums' pipeline waits (settable for tests of the error path); what a block
+// waits for before it may leave has the full one.
+__device__ long long g_rank_budget = kWaitBudget;
 
 namespace {
 
@@ -304,7 +308,6 @@ constexpr int kSumSmem = 1024 + kRing * (kABytes + kBBytes);  // 89 KB
 static_assert(kRing * (kXBytes + kBBytes) + kSlots8 * kABytes <= kRing * (kABytes + kBBytes),
               "codes' layout inside the bf16 layout's memory");
 constexpr int kTmemCols = 256;  // kAcc * 64, of which 48 each are used
-constexpr long long kWaitBudget = 2000000000LL;  // ~1 s of SM clocks per wait
 
 struct alignas(64) SumJob {
   CUtensorMap xmap;       // codes: 128 x 64 boxes; bf16: 64 x 64, 128-byte swizzle
@@ -350,19 +353,44 @@ __device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Bounded wait for the phase of parity `parity`; false on abort or expiry.
-__device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
-  if (mbar_try(b, parity)) return true;
+// One poll (try_wait may park the thread until the phase completes).
+__device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(su32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void wait_expired(volatile int* abort) {
+  *abort = 1;
+  atomicExch(&g_rank_error, 1);
+}
+// Bounded wait for the phase of parity `parity`; false on abort or expiry (a budget of 0:
+// unless the first poll succeeds).
+__device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity, volatile int* abort,
+                                          long long budget) {
+  if (mbar_test(b, parity)) return true;
   const long long t0 = clock64();
-  while (true) {
+  while (budget > 0) {
     if (mbar_try(b, parity)) return true;
     if (*abort) return false;
-    if (clock64() - t0 > kWaitBudget) {
-      *abort = 1;
-      atomicExch(&g_rank_error, 1);
-      return false;
-    }
+    if (clock64() - t0 > budget) break;
   }
+  wait_expired(abort);
+  return false;
+}
+// What a block has in flight, before it leaves.
+__device__ __forceinline__ void mbar_drain(uint64_t* b, uint32_t parity, volatile int* abort) {
+  const long long t0 = clock64();
+  while (!mbar_try(b, parity))
+    if (clock64() - t0 > kWaitBudget) {
+      wait_expired(abort);
+      return;
+    }
 }
 // Shared-memory matrix descriptor, 128-byte swizzle.
 __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
@@ -511,9 +539,10 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tbase = s_tmem;
   volatile int* abort = &s_abort;
+  const long long budget = g_rank_budget;
   // the products of stage st (which used its ring place and operand slot) are done
   auto products_done = [&](int st) {
-    return st < 0 || mbar_wait(&empty[st % kRing], uint32_t(st / kRing) & 1u, abort);
+    return st < 0 || mbar_wait(&empty[st % kRing], uint32_t(st / kRing) & 1u, abort, budget);
   };
 
   if (warp == kXWarps + 1) {
@@ -522,20 +551,17 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
       int issued = min(stages, kRing);
       for (; issued < stages && products_done(issued - kRing); ++issued) copy(issued);
       // the copies land before the block may leave (normally long since read)
-      for (int st = max(0, issued - kRing); st < issued; ++st) {
-        const long long t0 = clock64();
-        while (!mbar_try(&copied[st % kRing], uint32_t(st / kRing) & 1u) &&
-               clock64() - t0 < kWaitBudget) {
-        }
-      }
+      for (int st = max(0, issued - kRing); st < issued; ++st)
+        mbar_drain(&copied[st % kRing], uint32_t(st / kRing) & 1u, abort);
     }
   } else if (warp == kXWarps) {
     // ---------------------------------------------------------- products
     if (lane == 0 && stages > 0) {
       for (int st = 0; st < stages; ++st) {
         const int place = st % kRing;
-        if (!mbar_wait(&copied[place], uint32_t(st / kRing) & 1u, abort)) break;
-        if (codes && !mbar_wait(&ready[place], uint32_t(st / kRing) & 1u, abort)) break;
+        const uint32_t phase = uint32_t(st / kRing) & 1u;
+        if (!mbar_wait(&copied[place], phase, abort, budget)) break;
+        if (codes && !mbar_wait(&ready[place], phase, abort, budget)) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t a = codes ? sA + (st % kSlots8) * kABytes : sX + place * kABytes;
         const uint32_t b = sB + place * kBBytes;
@@ -548,13 +574,7 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
       }
       mma_commit(&done);
       // nothing of this block may be in flight when it leaves, aborted or not
-      const long long t0 = clock64();
-      while (!mbar_try(&done, 0) && clock64() - t0 < kWaitBudget) {
-      }
-      if (!mbar_try(&done, 0)) {
-        s_abort = 1;
-        atomicExch(&g_rank_error, 1);
-      }
+      mbar_drain(&done, 0, abort);
     }
   } else if (codes) {
     // --------------------------------------------------------- expansion
@@ -581,7 +601,7 @@ __global__ void __launch_bounds__(kSumThreads, 2) rank_sums_kernel(const __grid_
     for (int st = group; st < stages; st += kSlots8) {
       const int place = st % kRing;
       bytes_of(st + kSlots8, next);
-      if (!mbar_wait(&copied[place], uint32_t(st / kRing) & 1u, abort)) break;
+      if (!mbar_wait(&copied[place], uint32_t(st / kRing) & 1u, abort, budget)) break;
       uint4 w[kEach];
 #pragma unroll
       for (int i = 0; i < kEach; ++i) w[i] = lds128(sX + place * kXBytes + gt * 16 + i * 2048);
@@ -900,6 +920,12 @@ slora_status rank_sums(const RankSum* jobs, int n, int cols, float scale, float*
   LaunchScope ls(kSkinny, bytes * slices(cols), st);
   SLORA_CUDA(launch_early(rank_sums_kernel, dim3(unsigned(blocks), unsigned(slices(cols))),
                           kSumThreads, kSumSmem, st, p));
+  return SLORA_OK;
+}
+
+slora_status rank_set_wait_budget(long long cycles) {
+  const long long v = cycles < 0 ? kWaitBudget : cycles;
+  SLORA_CUDA(cudaMemcpyToSymbol(g_rank_budget, &v, sizeof(v)));
   return SLORA_OK;
 }
 

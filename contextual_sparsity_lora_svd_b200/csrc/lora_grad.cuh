@@ -90,6 +90,8 @@ int64_t rank_sums_counters(const RankSum* jobs, int n, int cols);
 slora_status rank_sums(const RankSum* jobs, int n, int cols, float scale, float* part,
                        unsigned* counters, bool beside, cudaStream_t st);
 
+// Budget of rank_sums' pipeline waits, in SM clocks; negative: the default.
+slora_status rank_set_wait_budget(long long cycles);
 // Raised when a rank_sums wait ran out of its budget, or by an index outside its weight.
 slora_status rank_check_error(bool clear);
 

@@ -302,7 +302,8 @@ extern "C" slora_status slora_device_error(int clear) {
 
 extern "C" slora_status slora_set_wait_budget(int64_t cycles) {
   slora::clear_error();
-  return slora::skinny_set_wait_budget(static_cast<long long>(cycles));
+  SLORA_TRY(slora::skinny_set_wait_budget(static_cast<long long>(cycles)));
+  return slora::rank_set_wait_budget(static_cast<long long>(cycles));
 }
 
 // ------------------------------------------------------------ launch record

@@ -117,7 +117,8 @@ slora_status slora_device_error(int clear);
 /*
  * Test hook for the error path above (not part of the method): the budget, in
  * SM clock cycles, of the pipeline waits of the skinny-contraction stream
- * kernel (the LoRA projections and gradients on strided inputs).  0 makes
+ * kernel (the LoRA projections and gradients on strided inputs) and of the
+ * sums of slora_linear_bwd_act8.  0 makes
  * every wait that does not succeed at its first poll give up, so the next
  * call raises the device flag that slora_device_error reports as
  * SLORA_ERR_TIMEOUT and leaves its outputs undefined; the device stays usable.

@@ -620,3 +620,25 @@ def test_scratch_of_a_pending_call_is_not_given_to_another_stream(L):
         for g, w in zip(got, want):
             assert all(torch.equal(a, b) for a, b in zip(g, w))
     assert L.lib().slora_device_error(1) == 0
+
+
+@pytest.mark.parametrize("side", ["none", "out_rows", "in_cols"])
+def test_expired_wait_of_the_sums_is_reported(L, side):
+    """With a wait budget of 0 the sums' pipeline gives up (its products' warp cannot find the first
+    operand expanded at its first poll): reported and cleared, and the next call is right again."""
+    b, s, ctx, k, n, r = 2, 512, [400, 300], 512, 384, 16
+    lib = L.lib()
+    assert lib.slora_device_error(1) == 0
+    cols = {"none": 0, "out_rows": n, "in_cols": k}[side]
+    assert lib.slora_set_wait_budget(0) == 0
+    try:
+        with pytest.raises(AssertionError):  # outputs undefined: dA or dB is off
+            linear_case(L, side, b, s, ctx, k, n, r, cols // 2)
+        torch.cuda.synchronize()
+    finally:
+        assert lib.slora_set_wait_budget(-1) == 0
+    assert lib.slora_device_error(1) == 7  # SLORA_ERR_TIMEOUT
+    assert b"wait expired" in L._lib_err()
+    assert lib.slora_device_error(0) == 0
+    linear_case(L, side, b, s, ctx, k, n, r, cols // 2)
+    assert lib.slora_device_error(0) == 0
