@@ -453,26 +453,33 @@ def _rows(t, what):
     return t.data_ptr(), st[0] if n[0] > 1 else max(st[0], n[1])
 
 
-def _whole(t, what, dt):
+def _whole(t, what, dt, at):
     if t.dtype is not dt:
         raise TypeError(f"{what} is {t.dtype}, not {dt}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous tensor is needed")
+    if t.get_device() != at:
+        raise ValueError(f"{what} is on {t.device}, not where the rows are")
     return t.data_ptr()
 
 
-def _same(t, what, dt):
+def _same(t, what, dt, at):
     if t.dtype != dt:
         raise TypeError(f"{what} is {t.dtype}, the rows are {dt}")
+    if t.get_device() != at:
+        raise ValueError(f"{what} is on {t.device}, not where the rows are")
 
 
 def _here(*tensors):
     """Refuses tensors (None stays None) that are not on the current CUDA device."""
+    at = None
     for t in tensors:
         if t is not None:
-            at = t.get_device()  # -1: on the CPU
-            if at < 0 or at != torch._C._cuda_getDevice():
-                raise ValueError(f"a tensor on {t.device} is no operand of a call on the current CUDA device")
+            d = t.get_device()  # -1: on the CPU
+            if d != at:
+                if at is not None or d < 0 or d != torch._C._cuda_getDevice():
+                    raise ValueError(f"a tensor on {t.device} is no operand of a call on the current CUDA device")
+                at = d
 
 
 def _fit(t, what, n, dt):
@@ -498,7 +505,8 @@ def qk_rows(heads, X=None, g=None, Y=None, dY=None, dX=None, dg=None, idx=None, 
         first = next((t for t in (X_ctx, X_out, dX_ctx, dX_out, dY) if t is not None), None)
         if first is None:
             raise ValueError("rows without a tensor")
-    dt = first.dtype
+    dt, at = first.dtype, first.get_device()
+    r.at = at
     r.dt = _DTYPES.get(dt)
     if r.dt is None:
         raise TypeError("the rows are bf16 or fp32 tensors")
@@ -509,35 +517,32 @@ def qk_rows(heads, X=None, g=None, Y=None, dY=None, dX=None, dg=None, idx=None, 
             r.Y, r.ldy = r.X, r.ldx
         else:
             r.Y, r.ldy = _rows(Y, "Y")
-            _same(Y, "Y", dt)
+            _same(Y, "Y", dt, at)
     if dX is not None:
         r.dX, r.lddx = _rows(dX, "dX")
-        _same(dX, "dX", dt)
+        _same(dX, "dX", dt, at)
     if g is not None:
-        r.g = _whole(g, "g", dt)
+        r.g = _whole(g, "g", dt, at)
     r.gdt = F32
     if dY is not None:
         r.dY, r.lddy = _rows(dY, "dY")
         r.gdt = dtype_code(dY)
+        _same(dY, "dY", dY.dtype, at)
     if dg is not None:
-        r.dg = _whole(dg, "dg", torch.float32)
+        r.dg = _whole(dg, "dg", torch.float32, at)
     if idx is not None:
         r.n_idx = idx.numel()
         if X_ctx is not None:
-            r.X_ctx = _whole(X_ctx, "X_ctx", dt)
+            r.X_ctx = _whole(X_ctx, "X_ctx", dt, at)
         if X_out is not None:
-            r.X_out = _whole(X_out, "X_out", dt)
+            r.X_out = _whole(X_out, "X_out", dt, at)
         if dX_ctx is not None:
-            r.dX_ctx = _whole(dX_ctx, "dX_ctx", dt)
+            r.dX_ctx = _whole(dX_ctx, "dX_ctx", dt, at)
         if dX_out is not None:
-            r.dX_out = _whole(dX_out, "dX_out", dt)
+            r.dX_out = _whole(dX_out, "dX_out", dt, at)
         # an empty list is still a list: its address, never read, may be null
-        r.idx = _whole(idx, "idx", torch.int32) or r.X_out or r.dX_out or r.Y or r.dY
+        r.idx = _whole(idx, "idx", torch.int32, at) or r.X_out or r.dX_out or r.Y or r.dY
     r.tensors = (X, g, Y, dY, dX, dg, idx, X_ctx, X_out, dX_ctx, dX_out)
-    r.at = first.get_device()
-    for t in r.tensors:
-        if t is not None and t.get_device() != r.at:
-            raise ValueError(f"rows on {first.device} and on {t.device}")
     return r
 
 
@@ -584,10 +589,10 @@ def _qk(fn, head, batch, seq, head_dim, q, k, rotary_, pos, eps, ctx_len, ws, st
     _sizes(q, batch * seq, TC, head_dim)
     if k is not None:
         _sizes(k, batch * seq, TC, head_dim)
-    for rows in (q, k):  # (a qk_rows' tensors are all where its first one is)
-        if rows is not None and (rows.at < 0 or rows.at != torch._C._cuda_getDevice()):
-            _here(*rows.tensors)
-    _here(pos, ws)
+    at = q.at  # where each of a qk_rows' tensors is
+    if (at < 0 or at != torch._C._cuda_getDevice() or (k is not None and k.at != at)
+            or (pos is not None and pos.get_device() != at) or ws is not None):
+        _here(*q.tensors, *(() if k is None else k.tensors), pos, ws)
     args = head + [ctypes.byref(tok), head_dim, eps, ctypes.byref(rotary_ or rotary()), ptr(pos),
                    ctypes.byref(q), kr]
     _run_scratch(fn, args, ws, stream)
