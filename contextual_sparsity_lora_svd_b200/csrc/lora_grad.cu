@@ -99,11 +99,24 @@ __device__ __forceinline__ long long setup_index(const LoraCopy& c, long long i)
   atomicExch(&g_rank_bad_index, 1);
   return -1;
 }
+// v as the sum of its terms.  The first holds what rounds past bf16's largest number as
+// that number, and an infinity alone (its difference to itself is no zero).
 __device__ __forceinline__ void put_terms(__nv_bfloat16* o, long long plane, float v) {
+  __nv_bfloat16 h = __float2bfloat16_rn(v);
+  if (__hisinf(h)) {
+    if (isinf(v)) {
+      o[0] = h;
 #pragma unroll
-  for (int k = 0; k < kTerms; ++k) {
-    const __nv_bfloat16 h = __float2bfloat16_rn(v);
+      for (int k = 1; k < kTerms; ++k) o[k * plane] = __float2bfloat16_rn(0.0f);
+      return;
+    }
+    h = __float2bfloat16_rz(v);
+  }
+  o[0] = h;
+#pragma unroll
+  for (int k = 1; k < kTerms; ++k) {
     v -= __bfloat162float(h);
+    h = __float2bfloat16_rn(v);
     o[k * plane] = h;
   }
 }

@@ -642,3 +642,58 @@ def test_expired_wait_of_the_sums_is_reported(L, side):
     assert lib.slora_device_error(0) == 0
     linear_case(L, side, b, s, ctx, k, n, r, cols // 2)
     assert lib.slora_device_error(0) == 0
+
+
+@pytest.mark.parametrize("value", [3.4e38, -3.4e38, float("inf"), float("-inf"), float("nan")])
+def test_rank_operands_at_the_top_of_fp32(L, value):
+    """X A^T and dY B between bf16's and fp32's largest numbers stay finite in the sums' operands, and
+    an infinity or NaN reaches its rank column with the formula's signs and no other column."""
+    T, k, n, r = 70, 64, 96, 20
+    gen = gen_of(17)
+    W, A = rand(gen, (n, k)), rand(gen, (r, k))
+    X, XA = rand(gen, (T, k)), rand(gen, (T, r), torch.float32)
+    X8 = L.act8_empty(T, k)
+    L.slora_act8_pack(X, *X8)
+    x = R.act8(R.f64(X))[2]
+    B = torch.zeros(n, r, device="cuda").bfloat16()
+    dY = rand(gen, (T, n), scale=2.0 ** -12)
+    dY[:, 0] = 0
+    XA[33, 18] = value
+    # dY B: row 40 of column 5 is 2^127 + 2^127 (1 - 2^-8), past bf16's largest number; with a value
+    # that is not finite, that value
+    finite = np.isfinite(value)
+    big = np.sign(value) * 2.0 ** 127 * (2 - 2.0 ** -8) if finite else value
+    B[0, 5] = 1.0
+    if finite:
+        B[1, 5] = 1.0
+        dY[:, 1] = 0
+        dY[40, 0] = dY[40, 1] = float(np.sign(value)) * 2.0 ** 127 * (1 - 2.0 ** -8)
+        dY[40, 1] *= 1 + 2.0 ** -7  # 2^127 (1 - 2^-16) rounds to 2^127
+        big = float(dY[40, 0].double() + dY[40, 1].double())
+        assert 3.3895e38 < abs(big) < 3.4028e38
+        X[40] *= 2.0 ** -10  # the sums over tokens stay finite
+        L.slora_act8_pack(X, *X8)
+        x = R.act8(R.f64(X))[2]
+    else:
+        dY[40, 0] = value
+    dX, dA, dB = torch.empty_like(X), torch.empty(r, k, device="cuda"), torch.empty(n, r, device="cuda")
+    L.slora_linear_bwd_act8(L.SLICE_NONE, 1, T, [T], k, n, W, A, B, 0.5, None, X8, XA, dY, dX, dA, dB)
+    dy, xa, b = R.f64(dY), R.f64(XA), R.f64(B)
+    if not finite:
+        # an infinite dY meets zeros of B and the three terms of X A^T: its row of dB, and the
+        # columns of dY B that are zero times it, are not finite; column 5 alone is stated
+        assert np.isfinite(R.f64(dB)[1:, :18]).all() and np.isfinite(R.f64(dB)[1:, 19]).all()
+        col = 0.5 * dy[33, 1:] * value
+        got = R.f64(dB)[1:, 18]
+        if np.isnan(value):
+            assert np.isnan(got).all()
+        else:
+            assert np.array_equal(got, col)
+            assert np.array_equal(R.f64(dA)[5][x[40] != 0], 0.5 * value * x[40][x[40] != 0])
+        return
+    # (column 18 of dB in rows 0 and 1 overflows by the formula too)
+    want = 0.5 * dy.T @ xa
+    size = 0.5 * np.abs(dy).T @ np.abs(xa)
+    assert (np.abs(R.f64(dB) - want)[2:] <= 1e-5 * size[2:]).all()
+    want, size = 0.5 * (dy @ b).T @ x, 0.5 * np.abs(dy @ b).T @ np.abs(x)
+    assert (np.abs(R.f64(dA) - want) <= 1e-5 * size).all()
