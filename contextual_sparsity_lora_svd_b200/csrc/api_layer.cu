@@ -300,6 +300,8 @@ slora_status qk_common(const char* fn, bool backward, slora_dtype dt, slora_dtyp
       LREQ(r.dY);
       SLORA_TRY(check_stride(fn, "lddy", r.lddy, n));
       LOPT(r.dg);
+      if (r.dg && !r.g)
+        SLORA_FAIL(SLORA_ERR_INVALID_ARG, "%s: dg is the gradient of a gain, and g is NULL", fn);
     } else {
       LREQ(r.Y);
       SLORA_TRY(check_stride(fn, "ldy", r.ldy, n));

@@ -556,7 +556,8 @@ typedef struct {
   int64_t lddx;
   void* dX_ctx;         /* backward, sliced: written, shaped like X_ctx                  */
   void* dX_out;         /* backward, sliced: written, shaped like X_out                  */
-  float* dg;            /* backward: gradient of g [head_dim], written; NULL: g frozen   */
+  float* dg;            /* backward: gradient of g [head_dim], written; NULL: g frozen
+                           (or no norm: only with a gain)                                */
 } slora_qk_rows;
 
 /*

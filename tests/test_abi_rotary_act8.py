@@ -382,3 +382,10 @@ def test_stack_refuses_gains_that_do_not_fit(L, which, bad, error, monkeypatch):
     with pytest.raises(error):
         layers.DecoderStack(lays, 256, 4, 2, 64, 688, 8, 8, 1.0, 1, 8, [8], [0.0] * 2, [0.0] * 2, None, None,
                             qk_norm=True)
+
+
+def test_a_gain_s_gradient_needs_the_gain(L):
+    """dg without g would never be written: refused, of either tensor."""
+    assert bwd(L, dense(L, g=None, dg=FAKE))[0] == INVALID
+    assert bwd(L, dense(L), dense(L, 2, g=None, dg=FAKE))[0] == INVALID
+    assert bwd(L, dense(L, dg=FAKE), dense(L, 2, g=None))[0] == OK
