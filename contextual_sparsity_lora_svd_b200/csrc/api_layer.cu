@@ -415,13 +415,15 @@ extern "C" slora_status slora_rmsnorm_fwd_act8(slora_dtype dt, int64_t T, int64_
   SLORA_TRY(check_norm8(fn, dt, T, d));
   if (!(eps >= 0.f) || !std::isfinite(eps))
     SLORA_FAIL(SLORA_ERR_INVALID_ARG, "%s: eps %g", fn, double(eps));
-  LREQ(X); LREQ(g); LREQ(N); LOPT(A); LOPT(H); LOPT(rstd);
-  if (H8) SLORA_TRY(check_ckpt(fn, "H8", H8));
-  if (N8) SLORA_TRY(check_ckpt(fn, "N8", N8));
-  if (A && H8 && !H) SLORA_FAIL(SLORA_ERR_INVALID_ARG, "%s: with A and H8, H is required", fn);
+  if (T > 0) {  // tensors without rows have no address
+    LREQ(X); LREQ(g); LREQ(N); LOPT(A); LOPT(H); LOPT(rstd);
+    if (H8) SLORA_TRY(check_ckpt(fn, "H8", H8));
+    if (N8) SLORA_TRY(check_ckpt(fn, "N8", N8));
+    if (A && H8 && !H) SLORA_FAIL(SLORA_ERR_INVALID_ARG, "%s: with A and H8, H is required", fn);
+  }
   const bool query = ws == nullptr;
   SLORA_TRY(ws_none(fn, ws, ws_bytes));
-  if (query) return SLORA_OK;
+  if (query || T == 0) return SLORA_OK;
   SLORA_TRY(check_device());
   return rmsnorm_fwd_act8_run(X, A, g, T, d, eps, H, N, rstd, H8, N8,
                               static_cast<cudaStream_t>(stream));
@@ -436,11 +438,13 @@ extern "C" slora_status slora_rmsnorm_bwd_act8(slora_dtype dt, int64_t T, int64_
   const char* fn = "slora_rmsnorm_bwd_act8";
   clear_error();
   SLORA_TRY(check_norm8(fn, dt, T, d));
-  SLORA_TRY(check_ckpt(fn, "H8", H8));
-  LREQ(rstd); LREQ(g); LREQ(dN0); LREQ(dX); LOPT(dN1); LOPT(dN2); LOPT(dRes);
+  if (T > 0) {
+    SLORA_TRY(check_ckpt(fn, "H8", H8));
+    LREQ(rstd); LREQ(g); LREQ(dN0); LREQ(dX); LOPT(dN1); LOPT(dN2); LOPT(dRes);
+  }
   const bool query = ws == nullptr;
   SLORA_TRY(ws_none(fn, ws, ws_bytes));
-  if (query) return SLORA_OK;
+  if (query || T == 0) return SLORA_OK;
   SLORA_TRY(check_device());
   return rmsnorm_bwd_act8_run(*H8, rstd, g, dN0, dN1, dN2, dRes, T, d, dX,
                               static_cast<cudaStream_t>(stream));

@@ -389,3 +389,16 @@ def test_a_gain_s_gradient_needs_the_gain(L):
     assert bwd(L, dense(L, g=None, dg=FAKE))[0] == INVALID
     assert bwd(L, dense(L), dense(L, 2, g=None, dg=FAKE))[0] == INVALID
     assert bwd(L, dense(L, dg=FAKE), dense(L, 2, g=None))[0] == OK
+
+
+def test_norms_of_no_rows(L):
+    """Tensors without rows have no address; there is nothing to do, as in slora_act8_pack."""
+    assert status(L, "slora_rmsnorm_fwd_act8",
+                  [L.BF16, 0, 64, 1e-5, None, None, FAKE, None, None, None, None, None]) == (OK, 0)
+    assert status(L, "slora_rmsnorm_bwd_act8",
+                  [L.BF16, 0, 64, None, None, FAKE, None, None, None, None, None]) == (OK, 0)
+    none = L.Act8(None, None)
+    assert status(L, "slora_rmsnorm_fwd_act8", [L.BF16, 0, 64, 1e-5, None, None, FAKE, None, None, None,
+                                                ctypes.byref(none), ctypes.byref(none)]) == (OK, 0)
+    assert status(L, "slora_rmsnorm_fwd_act8",
+                  [L.BF16, 0, 60, 1e-5, None, None, FAKE, None, None, None, None, None])[0] == SHAPE

@@ -697,3 +697,15 @@ def test_rank_operands_at_the_top_of_fp32(L, value):
     assert (np.abs(R.f64(dB) - want)[2:] <= 1e-5 * size[2:]).all()
     want, size = 0.5 * (dy @ b).T @ x, 0.5 * np.abs(dy @ b).T @ np.abs(x)
     assert (np.abs(R.f64(dA) - want) <= 1e-5 * size).all()
+
+
+def test_checkpoints_of_no_rows(L):
+    d = 64
+    X, g = torch.empty(0, d, device="cuda").bfloat16(), torch.ones(d, device="cuda").bfloat16()
+    c, c2, rstd = L.act8_empty(0, d), L.act8_empty(0, d), torch.empty(0, device="cuda")
+    L.slora_act8_pack(X, *c)
+    L.slora_act8_unpack(*c, X)
+    L.slora_rmsnorm_fwd_act8(X, g, torch.empty_like(X), rstd, A=X, H=torch.empty_like(X), H8=c, N8=c2)
+    L.slora_rmsnorm_bwd_act8(c, rstd, g, X, torch.empty_like(X), dRes=X)
+    torch.cuda.synchronize()
+    assert L.lib().slora_device_error(1) == 0
