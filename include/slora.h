@@ -573,8 +573,9 @@ typedef struct {
  *   q, k      the tensors, both dense or both sliced; k may be NULL (one
  *             tensor).  Y may be X itself (same stride) on dense rows; no other
  *             overlap.
- * Angles are exact to about 1e-7 at every position: the turns are counted in
- * 64-bit fixed point.  Of the forward, sliced tensors of more than 64 sequences
+ * Cosines and sines are off by less than 3e-7 + 4e-16 |pos|: the turns are
+ * counted in 64-bit fixed point, exact modulo one turn, from frequencies that
+ * are rounded as doubles.  Of the forward, sliced tensors of more than 64 sequences
  * need a workspace, nothing else; a query gives 0 where none is needed, and any
  * aligned address but NULL runs the call then.
  * A sliced tensor has at most 32768 channels (heads * head_dim).  An entry of
@@ -614,7 +615,8 @@ slora_status slora_qk_rotary_bwd(slora_dtype dt, slora_dtype gdt, const slora_to
  *           ties to even.  A block that holds an infinity or a NaN has b = 255
  *           and stands for NaNs; a block of zeros has b = 7.
  * Every value is exact in bf16 (7 bits of magnitude).  Rounding error: at most
- * 2^-7 of the block's largest magnitude (saturation at 127 included).
+ * 2^-7 of the block's largest magnitude (saturation at 127 included), or 2^-127
+ * where that is more: a block below 2^-120 has the least step, 2^-126.
  * ---------------------------------------------------------------------- */
 typedef struct {
   int8_t* codes;
@@ -635,7 +637,7 @@ slora_status slora_act8_unpack(slora_dtype dt, int64_t T, int64_t d, const slora
  * slora_rmsnorm_fwd_act8 — slora_rmsnorm_fwd that also writes checkpoints of H
  * and / or of N in the same pass (H8, N8 may be NULL).  N is required; with A
  * and H8, H is required too (without A, H8 is the checkpoint of X).  d up to
- * 16384 here and in slora_rmsnorm_bwd_act8.
+ * 16384 here and in slora_rmsnorm_bwd_act8; T may be 0 in both.
  */
 slora_status slora_rmsnorm_fwd_act8(slora_dtype dt, int64_t T, int64_t d, float eps,
                                     const void* X, const void* A, const void* g, void* H,
@@ -653,8 +655,12 @@ slora_status slora_rmsnorm_bwd_act8(slora_dtype dt, int64_t T, int64_t d, const 
  * slora_linear_bwd_act8 — slora_linear_bwd whose layer input is a checkpoint:
  * X_ctx (and X_out, for SLORA_SLICE_IN_COLS) of the same shapes, read as codes
  * by the dA contraction itself.  SLORA_BF16 only.  The rank-r operands dY B and
- * XA_save enter the sums in fp32, so dA and dB are exact to fp32 rounding for
- * the values that the checkpoint holds.  The same call gives the same bits.  An
+ * XA_save enter the sums of dA and dB with fp32's 24 bits; the tensor cores
+ * truncate as they add, which leaves dA and dB within 1e-6 of their norm at 4096
+ * tokens.  dX is that of slora_linear_bwd to the bit: its LoRA part takes
+ * lora_scale * dY B rounded to bf16, 2^-8 of each of its r terms.  An infinite or
+ * NaN operand makes the sums that it enters infinite or NaN (not always the one
+ * that IEEE addition would).  The same call gives the same bits.  An
  * entry of idx outside the weight counts as a channel of zeros and is reported
  * by slora_device_error (SLORA_ERR_INVALID_ARG).
  */

@@ -709,3 +709,23 @@ def test_checkpoints_of_no_rows(L):
     L.slora_rmsnorm_bwd_act8(c, rstd, g, X, torch.empty_like(X), dRes=X)
     torch.cuda.synchronize()
     assert L.lib().slora_device_error(1) == 0
+
+
+@pytest.mark.parametrize("k,n,r", [(256, 688, 16), (136, 72, 64), (64, 520, 5)])
+def test_linear_input_gradient_counts_its_roundings(L, k, n, r):
+    """dX to its roundings: half a bf16 step of the result, 2^-8 of each term of the LoRA part (whose
+    operand lora_scale * dY B is bf16) and 2^-23 of what n + r tensor-core additions add."""
+    T, scale = 150, 2.0
+    gen = gen_of(n)
+    W, A, B = rand(gen, (n, k), scale=k ** -0.5), rand(gen, (r, k), scale=k ** -0.5), rand(gen, (n, r), scale=0.1)
+    X, dY, XA = rand(gen, (T, k)), rand(gen, (T, n)), rand(gen, (T, r), torch.float32)
+    X8, dX = L.act8_empty(T, k), torch.empty_like(X)
+    L.slora_act8_pack(X, *X8)
+    dA, dB = torch.empty(r, k, device="cuda"), torch.empty(n, r, device="cuda")
+    L.slora_linear_bwd_act8(L.SLICE_NONE, 1, T, [T], k, n, W, A, B, scale, None, X8, XA, dY, dX, dA, dB)
+    w, a, dy = R.f64(W), R.f64(A), R.f64(dY)
+    p = scale * dy @ R.f64(B)
+    want, lora = dy @ w + p @ a, np.abs(p) @ np.abs(a)
+    # the operand's own sum over n channels is fp32: n 2^-23 of its terms
+    fine = (n + r) * 2.0 ** -23 * (np.abs(dy) @ np.abs(w) + scale * np.abs(dy) @ np.abs(R.f64(B)) @ np.abs(a) + lora)
+    assert (np.abs(R.f64(dX) - want) <= 2.0 ** -8 * (np.abs(want) + (1 + 2.0 ** -8) * lora) + (1 + 2.0 ** -8) * fine).all()

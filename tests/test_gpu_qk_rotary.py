@@ -8,6 +8,7 @@ relative; the fp32 work before it (angle 2^-23, products, rsqrt 2^-22, sums of
 at most 256 squares) by less than 2^-18 of the terms it adds, which is what an
 fp32 result may be off by."""
 import ctypes
+import decimal
 import threading
 
 import numpy as np
@@ -528,3 +529,35 @@ def test_calls_from_host_threads(L, shapes, kept):
     assert not failed, failed
     for _, _, _, outs, want in jobs:
         assert all(torch.equal(a, w) for a, w in zip(outs, want))
+
+
+def exact_cos_sin(pos, base, dims):
+    """cos and sin of pos base^(-2p / dims), the angle reduced in 60 digits."""
+    with decimal.localcontext() as ctx:
+        ctx.prec = 60
+        pi = decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+        ln = decimal.Decimal(base).ln()
+        f = [(-ln * 2 * p / dims).exp() for p in range(dims // 2)]
+        angle = [[float((decimal.Decimal(int(t)) * v) % (2 * pi)) for v in f] for t in pos]
+    a = np.array(angle)
+    return np.cos(a), np.sin(a)
+
+
+@pytest.mark.parametrize("base", [10000, 500000])
+def test_angles_at_far_positions(L, base):
+    """Pairs (1, 0) turned: cosine and sine against angles in 60 digits, to the stated bound.  Of the
+    angle in a quarter turn, at most pi / 4, the fixed point's float, its factor and their product are
+    rounded by 2^-24 each (1.4e-7 together); the Taylor sums leave 3e-8 and round by less than 2^-23
+    (1.2e-7).  The frequency, 2 pi and their quotient are doubles: 3 * 2^-53 of the angle, 4e-16 |pos|."""
+    hd = 64
+    rng = np.random.default_rng(base)
+    pos = np.concatenate([np.arange(40), rng.integers(0, 10 ** 6, 200), rng.integers(-2 ** 31, 2 ** 31, 200),
+                          [2 ** 31 - 1, -2 ** 31, 131072, 1 << 20]])
+    X = torch.zeros(len(pos), hd, device="cuda")
+    X[:, :hd // 2] = 1
+    Y = torch.empty_like(X)
+    dpos = torch.tensor(pos, dtype=torch.int32, device="cuda")
+    L.slora_qk_rotary_fwd(1, len(pos), hd, L.qk_rows(1, X=X, Y=Y), rotary=L.rotary(base=float(base)), pos=dpos)
+    c, s = exact_cos_sin(pos, base, hd)
+    err = np.maximum(np.abs(R.f64(Y)[:, :hd // 2] - c), np.abs(R.f64(Y)[:, hd // 2:] - s)).max(1)
+    assert (err <= 3e-7 + 4e-16 * np.abs(pos)).all(), err.max()
