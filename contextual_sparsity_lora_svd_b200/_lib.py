@@ -554,6 +554,8 @@ def _tokens(batch, seq, ctx_len):
     """(struct, its host array, context rows); ctx_len a tuple, or None: undivided."""
     if ctx_len is None:
         ctx_len = (seq,) * batch
+    if len(ctx_len) != batch:
+        raise ValueError(f"{len(ctx_len)} context lengths for {batch} sequences")
     return *make_tokens(batch, seq, ctx_len), sum(ctx_len)
 
 

@@ -402,3 +402,18 @@ def test_norms_of_no_rows(L):
                                                 ctypes.byref(none), ctypes.byref(none)]) == (OK, 0)
     assert status(L, "slora_rmsnorm_fwd_act8",
                   [L.BF16, 0, 60, 1e-5, None, None, FAKE, None, None, None, None, None])[0] == SHAPE
+
+
+@pytest.mark.parametrize("ctx", [[3], [3, 2, 1], []])
+def test_binding_refuses_context_lengths_of_another_batch(L, ctx):
+    """A sequence without a length is no sequence without context rows."""
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt)  # noqa: E731
+    tc = sum(ctx)
+    rows = L.qk_rows(2, idx=z(5, dt=torch.int32), X_ctx=z(tc, 5), X_out=z(10 - tc, 128), Y=z(10, 128))
+    with pytest.raises(ValueError, match="context lengths for 2 sequences"):
+        L.slora_qk_rotary_fwd(2, 5, 64, rows, ctx_len=ctx)
+    f32 = torch.float32
+    with pytest.raises(ValueError, match="context lengths for 2 sequences"):
+        L.slora_linear_bwd_act8(L.SLICE_OUT_ROWS, 2, 5, ctx, 64, 64, z(64, 64), z(8, 64), z(64, 8), 1.0,
+                                z(16, dt=torch.int32), L.act8_empty(10, 64, device="cpu"), z(10, 8, dt=f32),
+                                z(tc, 16), z(10, 64), z(8, 64, dt=f32), z(64, 8, dt=f32), dY_out=z(10 - tc, 64))
