@@ -37,7 +37,7 @@
 // heads pass through the same stage, two ahead.  The next row is asked into L2
 // meanwhile: a second stage a warp would cost more resident warps than it
 // hides.  A forward and backward of 64 heads x 4096 rows at half the channels
-// take 113 us, bound by issue and latency at 16 (backward) and 24 warps an SM.
+// take 112 us, bound by issue and latency at 16 (backward) and 24 warps an SM.
 // Other ways, at an earlier state of the rest: two stages a warp 131 us against
 // 129, a full-width row a warp 147; the staged row swizzled against bank conflicts
 // (a quarter fewer) 120 against 116.
@@ -1061,7 +1061,7 @@ slora_status launch_v(int V, bool inter, bool sliced, const QkParams& P,
 // The widest vector (in channels of one group) that every row of the call
 // takes.  A unit may not straddle the members of a pair, so in the half layout
 // the width divides both halves.  (16 + 4 heads of 96 channels, 24 of them
-// rotated, 8192 rows: forward 38 us with single loads of 2, 28 us at 4.)
+// rotated, 8192 rows: forward 38 us with single loads of 2, 28 us at 4, by now 26.)
 int vector_width(const QkDesc& D, bool backward) {
   for (int V : {8, 4, 2}) {
     bool ok = D.rot.inter ? D.head_dim % (2 * V) == 0

@@ -352,9 +352,9 @@ class DecoderStack(_Runner):
     `idx_ffn[l]` (first `k_ffn[l]` entries) the channel sets used.
 
     `rotary` (L.rotary(...)) chooses another rotation than half pairs of the whole
-    head at unscaled angles; `rope_base` is then unused.  `qk_norm`: every q and
-    k head is RMS-normalised before the rotation with the frozen gains gq, gk
-    (bf16 [head_dim]) of its layer's dict.  `act8`: what only the backward reads
+    head at unscaled angles; `rope_base` is then unused.  Positions count from each
+    sequence's start.  `qk_norm`: every q and k head is RMS-normalised before the
+    rotation with the frozen gains gq, gk (bf16 [head_dim]) of its layer's dict.  `act8`: what only the backward reads
     of the inputs of both norms and of the q, k and v linears is kept as 8-bit
     checkpoints, 1.03 bytes a value in place of 2, and the bf16 tensors x, h and
     n1 hold the last layer's; the forward's numbers do not change."""
